@@ -48,7 +48,7 @@ typedef enum { SPECV_F32 = 0, SPECV_BF16 = 1 } specv_dtype_t;
 #define SPECV_E_DTYPE      -3   /* dtype is not a specv_dtype_t */
 #define SPECV_E_TEMP       -4   /* T is NaN, infinite, negative, or so small that 1/T overflows */
 #define SPECV_E_WORKSPACE  -5   /* workspace NULL, misaligned, or smaller than required */
-#define SPECV_E_ALIGN      -6   /* a logits pointer is not aligned to its element size */
+#define SPECV_E_ALIGN      -6   /* a logits pointer is not aligned to its element size, or a cache array or stride to 16 bytes */
 #define SPECV_E_HIP        -7   /* a kernel launch failed */
 #define SPECV_E_SCRATCH    -8   /* spec_verify_noalloc: the shape needs more than SPECV_NOALLOC_SCRATCH bytes */
 
@@ -366,6 +366,121 @@ size_t spec_ngram_map_bytes(int B, int capacity);
 int spec_ngram_map_update(void* tables, int capacity, const int32_t* history, const int32_t* len_old,
                           const int32_t* len_new, int B, int L_max, int n_min, int n_max, int min_hits, int K,
                           int32_t* out_draft, int32_t* out_count, int32_t* out_status, void* stream);
+
+/*
+ * The 8-bit paged cache: keys and values of the committed tokens, kept in 8
+ * bits, and the attention of a draft's nodes over it.  A verify round runs
+ * spec_kv_attention in every layer of the target's pass over the nodes (a
+ * chain of drafts or a token tree: [C] 3.1, a node sees the shared prefix and
+ * its own ancestors only), then a verify call, then spec_kv_append of the
+ * accepted path in every layer ([C] 9.1; out_path of spec_verify_tree_greedy
+ * says which nodes' entries to keep).  Nodes are not cached before they are
+ * accepted, so a rejected draft changes nothing in the cache.
+ *
+ * A page holds page_size tokens of every head.  The block of one page and
+ * one head has one scale for K and one for V; an entry stands for
+ * code * scale.  spec_kv_append writes scales that are powers of two, the
+ * smallest that brings the block's largest magnitude into the format's
+ * range; spec_kv_read and spec_kv_attention take any finite positive scale.
+ */
+typedef enum {
+  SPECV_E4M3 = 0, /* 8-bit float, 4 exponent and 3 fraction bits, no infinities, largest value 448 */
+  SPECV_I8 = 1    /* int8, codes -127 .. 127 */
+} specv_kvtype_t;
+
+typedef struct {
+  void* k_pages;   /* [num_pages][heads][page_size][dim] codes, 16-byte aligned */
+  void* v_pages;   /* [num_pages][heads][dim][page_size] codes (transposed), 16-byte aligned */
+  float* k_scales; /* [num_pages][heads] */
+  float* v_scales; /* [num_pages][heads] */
+  const int32_t* page_table; /* [B][max_pages]: page of positions c*page_size .. of sequence b */
+  int num_pages;   /* pages in k_pages and v_pages */
+  int max_pages;   /* columns of page_table; max_pages * page_size < 2^31 */
+  int page_size;   /* 16, 32, 64 or 128 tokens */
+  int heads;       /* cached (key and value) heads */
+  int dim;         /* 64, 96, 128 or 256 */
+  int type;        /* specv_kvtype_t */
+} specv_kv_t;      /* read on the host during the call; the arrays are device memory */
+
+#define SPECV_KV_MAX_APPEND (1 << 24)  /* tokens per sequence one spec_kv_append or spec_kv_read takes */
+
+/*
+ * spec_kv_append - quantise tokens and write them behind each sequence's
+ * cached ones.  Sequence b takes the tokens index[b][0], index[b][1], ... of
+ * its N (0, 1, ... when index is NULL): counts[b] of them (clamped to [0, N];
+ * N when counts is NULL), but none from the first index outside [0, N) on
+ * (out_path of spec_verify_tree_greedy can be passed as it is), nor from the
+ * first position on whose page_table entry is missing or outside [0,
+ * num_pages).  They become positions lengths[b], lengths[b] + 1, ...
+ *
+ * A block that the call begins gets the scale of its new tokens.  A block
+ * begun before keeps its scale if its new tokens fit; else its scale grows
+ * and its codes are rounded again.  Codes round to nearest even; infinite
+ * values saturate and do not count for the scale, NaN stays NaN in e4m3 and
+ * becomes 0 in int8.  Slots of a page behind the last token are left as they
+ * were.
+ *   k, v        [B][N] token rows of heads*dim elements (dtype), 16-byte aligned
+ *   row_stride  elements from one token's row to the next (of k and of v), a
+ *               multiple of 16 bytes; 0: contiguous (heads * dim)
+ *   lengths     [B] int32 (device): tokens cached before, clamped to [0,
+ *               max_pages * page_size]
+ *   counts      [B] int32 (device) or NULL;  index [B][N] int32 (device) or NULL
+ *   out_lengths [B] int32 or NULL: tokens cached after the call (must not be
+ *               `lengths` itself)
+ *   B <= 65535;  1 <= N <= SPECV_KV_MAX_APPEND
+ * A page that the call writes may belong to one sequence only; pages that
+ * are only read may be shared.  Needs no workspace; nothing synchronises.
+ */
+int spec_kv_append(const specv_kv_t* kv, const void* k, const void* v, int64_t row_stride, const int32_t* lengths,
+                   const int32_t* counts, const int32_t* index, int B, int N, int32_t* out_lengths, int dtype,
+                   void* stream);
+
+/*
+ * spec_kv_read - cached tokens back as values: out_k[b][t] and out_v[b][t]
+ * are position starts[b] + t of sequence b (starts clamped to at least 0;
+ * NULL: 0), exact in both types for scales that are powers of two; 0 at and
+ * behind lengths[b] and where the page_table has no page.
+ *   out_k, out_v  [B][T][heads][dim] (dtype), 16-byte aligned; one may be NULL
+ *   B <= 65535;  1 <= T <= SPECV_KV_MAX_APPEND
+ * Needs no workspace; nothing synchronises.
+ */
+int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* lengths, int B, int T, void* out_k,
+                 void* out_v, int dtype, void* stream);
+
+/*
+ * spec_kv_attention - attention of N nodes per sequence over its cached
+ * tokens and over the nodes themselves.  With G = Hq / heads query heads per
+ * cached head, query (b, n, hq) sees the cached positions 0 .. lengths[b]-1
+ * of head hq / G and, when k_new is given, node n and its ancestors (as
+ * spec_tree_mask; without parents a chain: nodes 0 .. n):
+ *   s_j = scale * (q . k_j),  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
+ *   lse = ln sum_j e^(s_j).
+ * A query that sees nothing gets 0 and -infinity.  What a query does not see
+ * never reaches it, whatever its memory holds.  Cached positions without a
+ * page (entry outside [0, num_pages)) are not seen.
+ *   q           [B][N] token rows of Hq*dim elements (dtype)
+ *   k_new, v_new [B][N] token rows of heads*dim elements, or both NULL: the
+ *               cached tokens only
+ *   q_stride, kv_stride  elements between token rows, multiples of 16 bytes;
+ *               0: contiguous
+ *   lengths     [B] int32 (device): cached tokens, clamped to [0, max_pages * page_size]
+ *   num_nodes   [B] int32 (device) or NULL: nodes of sequence b, clamped to
+ *               [0, N] (NULL: N); the outputs of further nodes are 0 and -infinity
+ *   parents     [B][N] int32 (device) or NULL: a chain; read when k_new is given
+ *   scale       finite
+ *   out         [B][N][Hq][dim] (dtype);  out_lse [B][N][Hq] float or NULL
+ *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq a multiple of heads
+ *   q, k_new, v_new and out 16-byte aligned
+ *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
+ * Sums and softmax statistics are in 32 bits.  The same call gives the same
+ * bits.  Returns the SPECV_* codes of spec_verify; nothing synchronises.
+ */
+size_t spec_kv_attention_workspace_size(const specv_kv_t* kv, int B, int N, int Hq);
+
+int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, const void* k_new, const void* v_new,
+                      int64_t kv_stride, const int32_t* lengths, const int32_t* num_nodes, const int32_t* parents,
+                      float scale, int B, int N, int Hq, void* out, float* out_lse, int dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Device-side input validation, a debugging aid.  While it is on, every
  * spec_verify* call (spec_verify, _ex, _noalloc, _ragged, _ragged_ex) first

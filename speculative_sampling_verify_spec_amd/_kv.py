@@ -1,0 +1,240 @@
+"""Binding of the 8-bit paged cache (argument marshalling only): KVCache,
+kv_append, kv_read, kv_attention.  Checks shapes and dtypes, allocates outputs
+and workspaces with torch and passes device pointers plus torch's current
+stream of the tensors' device."""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+from ._lib import SpecVerifyError, _dtype_code, _ptr, load, strerror
+
+SPECV_E4M3, SPECV_I8 = 0, 1
+KV_PAGE_SIZES = (16, 32, 64, 128)
+KV_DIMS = (64, 96, 128, 256)
+
+
+class _Descriptor(ctypes.Structure):
+    """specv_kv_t."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("type", ctypes.c_int)]
+
+
+class KVCache:
+    """The pages and scales of an 8-bit cache.
+
+    k_pages [num_pages, heads, page_size, dim] and v_pages [num_pages, heads,
+    dim, page_size] (transposed) in torch.float8_e4m3fn or torch.int8,
+    k_scales and v_scales [num_pages, heads] float32, all contiguous on one
+    device.  KVCache.empty() allocates them."""
+
+    __slots__ = ("k_pages", "v_pages", "k_scales", "v_scales")
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales):
+        import torch
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, heads, page_size, dim]")
+        n, h, p, d = k_pages.shape
+        if k_pages.dtype not in (torch.float8_e4m3fn, torch.int8) or v_pages.dtype != k_pages.dtype:
+            raise TypeError(f"pages must both be torch.float8_e4m3fn or torch.int8, got {k_pages.dtype} and "
+                            f"{v_pages.dtype}")
+        if p not in KV_PAGE_SIZES or d not in KV_DIMS:
+            raise ValueError(f"page size must be one of {KV_PAGE_SIZES} and dim one of {KV_DIMS}, got {p} and {d}")
+        if tuple(v_pages.shape) != (n, h, d, p):
+            raise ValueError("v_pages must be [num_pages, heads, dim, page_size]")
+        for t in (k_scales, v_scales):
+            if t.dtype != torch.float32 or tuple(t.shape) != (n, h):
+                raise ValueError("scales must be float32 [num_pages, heads]")
+        for t in (k_pages, v_pages, k_scales, v_scales):
+            if t.device != k_pages.device or not t.is_contiguous():
+                raise ValueError("pages and scales must be contiguous tensors on the same device")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, heads: int, dim: int, dtype=None, device="cuda") -> "KVCache":
+        """A cache of num_pages pages (dtype: torch.float8_e4m3fn, the default, or torch.int8)."""
+        import torch
+        dtype = torch.float8_e4m3fn if dtype is None else dtype
+        return cls(torch.empty((num_pages, heads, page_size, dim), dtype=dtype, device=device),
+                   torch.empty((num_pages, heads, dim, page_size), dtype=dtype, device=device),
+                   torch.empty((num_pages, heads), dtype=torch.float32, device=device),
+                   torch.empty((num_pages, heads), dtype=torch.float32, device=device))
+
+    @property
+    def device(self):
+        return self.k_pages.device
+
+    @property
+    def page_size(self) -> int:
+        return self.k_pages.shape[2]
+
+    @property
+    def heads(self) -> int:
+        return self.k_pages.shape[1]
+
+    @property
+    def dim(self) -> int:
+        return self.k_pages.shape[3]
+
+
+def _descriptor(cache: KVCache, table_ptr: Optional[int], max_pages: int) -> _Descriptor:
+    import torch
+    n, h, p, d = cache.k_pages.shape
+    return _Descriptor(cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), cache.k_scales.data_ptr(),
+                       cache.v_scales.data_ptr(), table_ptr, n, max_pages, p, h, d,
+                       SPECV_I8 if cache.k_pages.dtype == torch.int8 else SPECV_E4M3)
+
+
+def _check_table(cache: KVCache, page_table) -> int:
+    import torch
+    if cache.device.type != "cuda":
+        raise ValueError("the cache must be on a GPU")
+    if page_table.device != cache.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+            not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
+    return page_table.shape[0]
+
+
+def _check_ints(cache: KVCache, shape, **tensors) -> None:
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.device != cache.device or t.dtype != torch.int32 or tuple(t.shape) != shape or
+                              not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
+
+
+def _token_stride(name: str, t, heads: int, dim: int) -> int:
+    """Elements between the token rows of t [B, N, heads, dim]: heads and
+    channels contiguous, one stride for all tokens (a slice of a fused
+    projection's rows will do)."""
+    B, N = t.shape[:2]
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != dim):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    row = sn if N > 1 else (sb if B > 1 else heads * dim)
+    if row < heads * dim or (N > 1 and B > 1 and sb != N * sn):
+        raise ValueError(f"{name}: tokens must be evenly spaced and must not overlap")
+    return row
+
+
+def _check_rows(cache: KVCache, name: str, t, B: int, N: int, heads: int) -> int:
+    if t.device != cache.device or t.dim() != 4 or tuple(t.shape) != (B, N, heads, cache.dim):
+        raise ValueError(f"{name} must be [{B}, {N}, {heads}, {cache.dim}] on the cache's device")
+    return _token_stride(name, t, heads, cache.dim)
+
+
+def _call(device, fn, *args) -> None:
+    """One library call on the device's current stream (the last argument)."""
+    import torch
+    st = torch.cuda.current_stream(device).cuda_stream
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = int(fn(*args, st))
+    else:
+        rc = int(fn(*args, st))
+    if rc != 0:
+        raise SpecVerifyError(rc, strerror(rc))
+
+
+def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=None, out_lengths=None):
+    """Quantise tokens into the cache behind each sequence's lengths[b] cached
+    ones (spec_kv_append).
+
+    k and v [B, N, heads, dim] (bf16 or fp32; a slice of a fused projection's
+    rows will do), page_table [B, max_pages], lengths [B] and optionally
+    counts [B] (tokens of each sequence) and index [B, N] (which tokens, up to
+    the first entry outside [0, N): the path of verify_tree_greedy), int32.
+    Returns the tokens cached after the call, [B] int32 (out_lengths if given;
+    lengths itself is left as it is, so every layer can pass it)."""
+    import torch
+    B = _check_table(cache, page_table)
+    if k.dim() != 4:
+        raise ValueError("k must be [B, N, heads, dim]")
+    N = k.shape[1]
+    row = _check_rows(cache, "k", k, B, N, cache.heads)
+    if _check_rows(cache, "v", v, B, N, cache.heads) != row or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same dtype and strides")
+    _check_ints(cache, (B,), lengths=lengths, counts=counts, out_lengths=out_lengths)
+    _check_ints(cache, (B, N), index=index)
+    if out_lengths is None:
+        out_lengths = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    elif out_lengths.data_ptr() == lengths.data_ptr():
+        raise ValueError("out_lengths must not be lengths itself")
+    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
+    _call(cache.device, load().spec_kv_append, ctypes.byref(kv), _ptr(k), _ptr(v), row, _ptr(lengths), _ptr(counts),
+          _ptr(index), B, N, _ptr(out_lengths), _dtype_code(k))
+    return out_lengths
+
+
+def kv_read(cache: KVCache, page_table, lengths, T: int, *, starts=None, dtype=None):
+    """Cached tokens back as values (spec_kv_read): positions starts[b] ..
+    starts[b] + T - 1 (from 0 without starts) of every sequence.  Returns (k,
+    v), each [B, T, heads, dim] in dtype (torch.bfloat16, the default, or
+    torch.float32), 0 at and behind lengths[b]."""
+    import torch
+    B = _check_table(cache, page_table)
+    _check_ints(cache, (B,), lengths=lengths, starts=starts)
+    dtype = torch.bfloat16 if dtype is None else dtype
+    k = torch.empty((B, T, cache.heads, cache.dim), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
+    code = _dtype_code(k)
+    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
+    _call(cache.device, load().spec_kv_read, ctypes.byref(kv), _ptr(starts), _ptr(lengths), B, T, _ptr(k), _ptr(v),
+          code)
+    return k, v
+
+
+def kv_attention_workspace_size(cache: KVCache, B: int, N: int, Hq: int, max_pages: int) -> int:
+    """Workspace bytes of kv_attention for page tables of max_pages columns (0: invalid sizes)."""
+    # the library reads the table's address only to see that there is one
+    kv = _descriptor(cache, 16, max_pages)
+    return int(load().spec_kv_attention_workspace_size(ctypes.byref(kv), B, N, Hq))
+
+
+def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None, *, parents=None, num_nodes=None,
+                 scale: Optional[float] = None, return_lse: bool = False, workspace=None):
+    """Attention of N nodes per sequence over the cache and over the nodes
+    themselves (spec_kv_attention).
+
+    q [B, N, Hq, dim], k_new and v_new [B, N, heads, dim] (both or neither;
+    bf16 or fp32), Hq a multiple of heads; lengths [B] cached tokens,
+    parents [B, N] the nodes' tree (None: a chain), num_nodes [B] the nodes of
+    each sequence, int32; scale defaults to dim ** -0.5.  Returns out [B, N,
+    Hq, dim] and, when asked, lse [B, N, Hq] float32."""
+    import torch
+    B = _check_table(cache, page_table)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, dim]")
+    N, Hq = q.shape[1], q.shape[2]
+    q_row = _check_rows(cache, "q", q, B, N, Hq)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    kv_row = 0
+    if k_new is not None:
+        kv_row = _check_rows(cache, "k_new", k_new, B, N, cache.heads)
+        if _check_rows(cache, "v_new", v_new, B, N, cache.heads) != kv_row or k_new.dtype != q.dtype or \
+                v_new.dtype != q.dtype:
+            raise ValueError("k_new and v_new must have the same strides, and q's dtype")
+    elif parents is not None:
+        raise ValueError("parents needs k_new and v_new")
+    _check_ints(cache, (B,), lengths=lengths, num_nodes=num_nodes)
+    _check_ints(cache, (B, N), parents=parents)
+    code = _dtype_code(q)
+    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
+    need = int(load().spec_kv_attention_workspace_size(ctypes.byref(kv), B, N, Hq))
+    if need == 0:
+        raise SpecVerifyError(-2, strerror(-2))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    elif workspace.device != cache.device:
+        raise ValueError("workspace must be on the cache's device")
+    out = torch.empty((B, N, Hq, cache.dim), dtype=q.dtype, device=cache.device)
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
+    _call(cache.device, load().spec_kv_attention, ctypes.byref(kv), _ptr(q), q_row, _ptr(k_new), _ptr(v_new), kv_row,
+          _ptr(lengths), _ptr(num_nodes), _ptr(parents),
+          1.0 / math.sqrt(cache.dim) if scale is None else float(scale), B, N, Hq, _ptr(out), _ptr(lse), code,
+          _ptr(workspace), workspace.numel() * workspace.element_size())
+    return (out, lse) if return_lse else out

@@ -34,6 +34,7 @@ EXPORTS = ("spec_verify_workspace_size", "spec_verify", "spec_verify_noalloc", "
            "spec_verify_ragged",
            "spec_verify_ragged_ex", "spec_verify_tree_workspace_size", "spec_verify_tree_greedy", "spec_tree_mask", "spec_ngram_propose",
            "spec_ngram_map_bytes", "spec_ngram_map_update", "spec_rounds_min_bytes", "spec_short_max_seqs",
+           "spec_kv_append", "spec_kv_read", "spec_kv_attention_workspace_size", "spec_kv_attention",
            "spec_debug_enable", "spec_debug_counters", "spec_debug_reset",
            "spec_verify_strerror", "spec_verify_version")
 
@@ -91,6 +92,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.spec_ngram_map_bytes.restype = sz
     lib.spec_ngram_map_update.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.spec_ngram_map_update.restype = i32
+    i64 = ctypes.c_int64
+    lib.spec_kv_append.argtypes = [vp, vp, vp, i64, vp, vp, vp, i32, i32, vp, i32, vp]
+    lib.spec_kv_append.restype = i32
+    lib.spec_kv_read.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp]
+    lib.spec_kv_read.restype = i32
+    lib.spec_kv_attention_workspace_size.argtypes = [vp, i32, i32, i32]
+    lib.spec_kv_attention_workspace_size.restype = sz
+    lib.spec_kv_attention.argtypes = [vp, vp, i64, vp, vp, i64, vp, vp, vp, f32, i32, i32, i32, vp, vp, i32, vp, sz, vp]
+    lib.spec_kv_attention.restype = i32
     lib.spec_debug_enable.argtypes = [i32]
     lib.spec_debug_enable.restype = i32
     lib.spec_debug_counters.argtypes = [vp, i32]

@@ -642,11 +642,11 @@ const char* spec_verify_strerror(int code) {
   switch (code) {
     case SPECV_OK: return "ok";
     case SPECV_E_NULL: return "a required pointer is NULL";
-    case SPECV_E_SHAPE: return "invalid shape or size (B >= 1, 1 <= K <= 32, 1 <= N <= 64 tree nodes, 1 <= n <= 16 n-gram sizes, V >= 1, sizes in range)";
-    case SPECV_E_DTYPE: return "dtype must be SPECV_F32 or SPECV_BF16";
+    case SPECV_E_SHAPE: return "invalid shape or size (B >= 1, 1 <= K <= 32, 1 <= N <= 64 tree nodes, 1 <= n <= 16 n-gram sizes, V >= 1, cache pages of 16, 32, 64 or 128 tokens, heads of 64, 96, 128 or 256, sizes in range)";
+    case SPECV_E_DTYPE: return "dtype must be SPECV_F32 or SPECV_BF16 (cache type: SPECV_E4M3 or SPECV_I8)";
     case SPECV_E_TEMP: return "T must be 0 (greedy) or finite and > 0 with 1/T finite";
     case SPECV_E_WORKSPACE: return "workspace NULL, not 256-byte aligned, or too small";
-    case SPECV_E_ALIGN: return "logits pointer not aligned to its element size";
+    case SPECV_E_ALIGN: return "logits pointer not aligned to its element size, or a cache array, token row or stride not to 16 bytes";
     case SPECV_E_HIP: return "a HIP launch failed";
     case SPECV_E_SCRATCH: return "the shape needs more than the 32 MiB static scratch of spec_verify_noalloc";
     default: return "unknown error";

@@ -1,0 +1,137 @@
+// The 8-bit paged cache: parameters shared by its host code and kernels, and
+// the device helpers for its formats.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "specverify.h"
+
+namespace sv {
+
+// The cache as the kernels see it (see specv_kv_t).
+struct KvView {
+  uint8_t* kp;           // K pages [pages][H][P][D]
+  uint8_t* vp;           // V pages [pages][H][D][P]
+  float* ks;             // scales [pages][H]
+  float* vs;
+  const int32_t* table;  // [B][width] page ids
+  int pages, width;
+  int P, pshift;         // tokens per page, log2
+  int H, D;
+};
+
+struct KvAppend {
+  KvView c;
+  const void* k;         // [B][N] token rows of H*D elements, row elements apart
+  const void* v;
+  long row;
+  const int32_t* lengths;
+  const int32_t* counts;  // or null
+  const int32_t* index;   // or null
+  int B, N;
+  int32_t* out_lengths;   // or null
+};
+
+struct KvRead {
+  KvView c;
+  const int32_t* starts;  // or null
+  const int32_t* lengths;
+  int B, T;
+  void* out_k;            // [B][T][H][D], or null
+  void* out_v;
+};
+
+struct KvAttn {
+  KvView c;
+  const void* q;          // [B][N] rows of Hq*D elements, q_row elements apart
+  const void* kn;         // [B][N] rows of H*D elements, kv_row elements apart, or null
+  const void* vn;
+  long q_row, kv_row;
+  const int32_t* lengths;
+  const int32_t* nodes;   // or null
+  const int32_t* parents; // or null: a chain
+  float scale;
+  int B, N, Hq, G;        // G = Hq / H query heads share a cached head
+  void* out;              // [B][N][Hq][D]
+  float* lse;             // [B][N][Hq] or null
+};
+
+// Launchers, next to their kernels.  dtype: SPECV_F32 or SPECV_BF16; fmt:
+// SPECV_E4M3 or SPECV_I8.
+hipError_t launch_kv_append(const KvAppend& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_read(const KvRead& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_attention(const KvAttn& p, int dtype, int fmt, hipStream_t s);
+
+#ifdef __HIPCC__
+
+constexpr float kE4m3Max = 448.f;  // largest e4m3 value: 0.875 * 2^9
+constexpr float kI8Max = 127.f;    // largest int8 code used (symmetric): 0.9921875 * 2^7
+
+// Four codes of a word to float; exact for both formats.
+template <int FMT>
+__device__ inline void kv_decode4(uint32_t w, float* f) {
+  if constexpr (FMT == SPECV_E4M3) {
+    f[0] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 0);
+    f[1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 1);
+    f[2] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 2);
+    f[3] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(w), 3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+  }
+}
+
+// Four values, in units of the scale, to codes: round to nearest, ties to
+// even (the formats' own 8-bit rounding: the cache's one deliberate loss).
+// Infinite values saturate; NaN stays NaN in e4m3 and becomes 0 in int8.
+template <int FMT>
+__device__ inline uint32_t kv_encode4(const float* x) {
+  constexpr float top = FMT == SPECV_E4M3 ? kE4m3Max : kI8Max;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float c = fminf(fmaxf(x[i], -top), top);
+    y[i] = x[i] == x[i] ? c : (FMT == SPECV_E4M3 ? x[i] : 0.f);
+  }
+  if constexpr (FMT == SPECV_E4M3) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true));
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= (static_cast<uint32_t>(static_cast<int>(rintf(y[i]))) & 0xffu) << (8 * i);
+    return w;
+  }
+}
+
+// The smallest power of two s with amax <= top * s, at least 2^-126 (the
+// smallest normal number, also for amax = 0).  amax is finite, so s <= 2^121.
+template <int FMT>
+__device__ inline float kv_scale(float amax) {
+  constexpr int bits = FMT == SPECV_E4M3 ? 9 : 7;
+  constexpr float top = FMT == SPECV_E4M3 ? 0.875f : 0.9921875f;
+  int e;
+  const float m = frexpf(amax, &e);  // amax = m 2^e, m in [1/2, 1)
+  int k = e - bits + (m > top ? 1 : 0);
+  if (!(amax > 0.f) || k < -126) k = -126;
+  return __int_as_float((k + 127) << 23);
+}
+
+// The page id in the table's column c of sequence b, or -1 when there is no
+// such column or its id names no page.
+__device__ inline int kv_page(const KvView& c, long b, long col) {
+  if (col >= c.width) return -1;
+  const int id = c.table[b * c.width + col];
+  return id >= 0 && id < c.pages ? id : -1;
+}
+
+// Cached tokens of sequence b: its length, clamped to what the table holds.
+__device__ inline int kv_len(const KvView& c, const int32_t* lengths, long b) {
+  return min(max(lengths[b], 0), c.width << c.pshift);
+}
+
+#endif  // __HIPCC__
+
+}  // namespace sv

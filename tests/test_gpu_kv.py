@@ -1,0 +1,427 @@
+"""The 8-bit paged cache on the GPU against the fp64 oracle: append (bit for
+bit), read back (exact), attention (within derived bounds)."""
+import numpy as np
+import pytest
+
+import kv_helpers as kh
+from oracle import kv as okv
+from oracle.tree import verify_tree_greedy
+
+pytestmark = pytest.mark.gpu
+
+
+def _dt(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _rand(rng, shape, dtype, device="cuda"):
+    """Device tensor and its exact fp64 values."""
+    import torch
+    t = torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(_dt(dtype))
+    return t.to(device), t.double().numpy()
+
+
+def _i32(a, device="cuda"):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(device)
+
+
+def _same_cache(got, want):
+    for n in ("k_pages", "v_pages"):
+        np.testing.assert_array_equal(kh.canonical(got[n], want["fmt"]), kh.canonical(want[n], want["fmt"]), n)
+    for n in ("k_scales", "v_scales"):
+        np.testing.assert_array_equal(got[n], want[n], n)
+
+
+# ---------------------------------------------------------------- append --
+APPEND = [  # fmt, dtype, P, H, D, N, lens
+    ("e4m3", "bf16", 16, 2, 64, 1, [0, 1, 15, 16, 17]),
+    ("int8", "f32", 16, 1, 96, 5, [0, 13, 14, 15, 16]),
+    ("e4m3", "f32", 32, 3, 128, 33, [0, 31, 40]),
+    ("int8", "bf16", 64, 2, 128, 200, [0, 1, 63, 64, 100]),
+    ("e4m3", "bf16", 128, 1, 256, 300, [5, 127, 128]),
+    ("int8", "f32", 128, 2, 256, 129, [0, 100]),
+    ("e4m3", "f32", 64, 1, 256, 64, [0, 32]),
+    ("int8", "bf16", 32, 4, 96, 64, [0, 7, 500]),
+]
+
+
+@pytest.mark.parametrize("fmt,dtype,P,H,D,N,lens", APPEND)
+def test_append_is_exact(gpu_lib, fmt, dtype, P, H, D, N, lens):
+    rng = np.random.default_rng(P * D + N)
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D, extra=N)
+    (k, k64), (v, v64) = _rand(rng, (len(lens), N, H, D), dtype), _rand(rng, (len(lens), N, H, D), dtype)
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k, v, _i32(lens))
+    want = okv.append(c, table, k64, v64, lens)
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    _same_cache(kh.to_host(dev, fmt), c)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_counts_index_and_growth(gpu_lib, fmt):
+    """Ragged counts, paths ended by -1 and by N, values that grow a begun
+    block's scale by far (old codes become subnormal or 0) and values too
+    small to move it."""
+    rng = np.random.default_rng(3)
+    lens, P, H, D, N = [3, 10, 30, 0, 31, 5, 17], 32, 2, 64, 9
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D, extra=N)
+    k, v = rng.normal(size=(2, len(lens), N, H, D))
+    k[0] *= 1e4
+    k[1] *= 1e-6
+    v[2] *= 2.0 ** 40
+    v[4] = 0.0
+    k[5] *= 2.0 ** -140          # subnormal inputs
+    k, v = k.astype(np.float32), v.astype(np.float32)
+    index = np.array([[0, 2, 5, -1, 7, 0, 0, 0, 0], [8, 7, 6, 5, 4, 3, 2, 1, 0], [1, 1, 1, 9, 0, 0, 0, 0, 0],
+                      [-1] * 9, [0, 1, 2, 3, 4, 5, 6, 7, 8], [2, 2 ** 31 - 1, 0, 0, 0, 0, 0, 0, 0],
+                      [4, 5, 6, -2 ** 31, 0, 0, 0, 0, 0]])
+    counts = np.array([9, 4, 100, 9, 7, 9, -3])
+    import torch
+    for cnt, idx in ((counts, index), (None, index), (counts, None)):
+        dev = kh.to_device(gpu_lib, c)
+        host = {n: (x.copy() if isinstance(x, np.ndarray) else x) for n, x in c.items()}
+        got = gpu_lib.kv_append(dev, _i32(table), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(),
+                                _i32(lens), counts=None if cnt is None else _i32(cnt),
+                                index=None if idx is None else _i32(idx))
+        want = okv.append(host, table, k.astype(np.float64), v.astype(np.float64), lens, cnt, idx)
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+        _same_cache(kh.to_host(dev, fmt), host)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_special_values(gpu_lib, fmt):
+    """Infinite values saturate and do not count for the scale, NaN does
+    neither, a block of zeros gets the smallest scale; ties round to even."""
+    import torch
+    P, H, D, N = 16, 1, 64, 20
+    c, table = kh.make_cache(np.random.default_rng(0), fmt, [7], P, H, D, extra=N)
+    k = np.zeros((1, N, H, D), np.float32)
+    v = np.random.default_rng(1).normal(size=k.shape).astype(np.float32)
+    v[0, 2, 0, 5], v[0, 3, 0, 6], v[0, 4, 0, 7], v[0, 12, 0, 0] = np.inf, -np.inf, np.nan, 3.4e38
+    k[0, 10, 0, :] = np.arange(64) + 0.5
+    k[0, 11, 0, 0] = okv.QMAX[fmt]
+    dev = kh.to_device(gpu_lib, c)
+    gpu_lib.kv_append(dev, _i32(table), torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), _i32([7]))
+    okv.append(c, table, k.astype(np.float64), v.astype(np.float64), [7])
+    _same_cache(kh.to_host(dev, fmt), c)
+
+
+def test_append_without_pages(gpu_lib):
+    """A missing or foreign page ends the tokens there; a full table, a
+    negative and a too large length write nothing out of place."""
+    rng = np.random.default_rng(4)
+    P, H, D, N = 16, 2, 64, 40
+    lens = [0, 0, 0, -5, 10 ** 6]
+    c, _ = kh.make_cache(rng, "e4m3", [0] * 12, P, H, D, extra=P, poison=False)
+    table = np.array([[0, 1, -1, 2], [3, 99, 4, 5], [-7, 6, 6, 6], [7, 8, 2 ** 31 - 1, 9], [10, 11, 10, 11]], np.int32)
+    (k, k64), (v, v64) = _rand(rng, (5, N, H, D), "f32"), _rand(rng, (5, N, H, D), "f32")
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k, v, _i32(lens)).cpu().numpy()
+    want = okv.append(c, table, k64, v64, lens)
+    assert got.tolist() == want.tolist() == [32, 16, 0, 32, 64]
+    _same_cache(kh.to_host(dev, "e4m3"), c)
+
+
+def test_append_in_pieces_and_strided_rows(gpu_lib):
+    """One token at a time and several, from the rows of a fused projection
+    (K and V slices of wider rows), against the oracle's same calls."""
+    rng = np.random.default_rng(5)
+    B, P, H, D = 3, 16, 2, 128
+    lens = np.array([0, 14, 31])
+    c, table = kh.make_cache(rng, "int8", lens.tolist(), P, H, D, extra=40)
+    dev, tab = kh.to_device(gpu_lib, c), _i32(table)
+    cur = _i32(lens)
+    for n in (1, 1, 5, 1, 17, 2):
+        fused, f64 = _rand(rng, (B, n, 4 * H + 2 * H, D), "bf16")
+        cur = gpu_lib.kv_append(dev, tab, fused[:, :, 4 * H:5 * H], fused[:, :, 5 * H:], cur)
+        lens = okv.append(c, table, f64[:, :, 4 * H:5 * H], f64[:, :, 5 * H:], lens)
+        np.testing.assert_array_equal(cur.cpu().numpy(), lens)
+    _same_cache(kh.to_host(dev, "int8"), c)
+
+
+# ------------------------------------------------------------------ read --
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,P,H,D", [("e4m3", 16, 3, 64), ("int8", 32, 1, 96), ("e4m3", 64, 2, 128),
+                                       ("int8", 128, 2, 256)])
+def test_read_is_exact(gpu_lib, fmt, P, H, D, dtype):
+    rng = np.random.default_rng(P)
+    lens = [0, 1, P - 1, P, P + 1, 3 * P + 5]
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D)
+    dev = kh.to_device(gpu_lib, c)
+    for T, starts in ((1, None), (2 * P + 3, None), (P, [0, 0, 5, 1, P, 2 * P + 7]),
+                      (70, [-3, 1, 2 ** 31 - 1, P - 1, 10 * P, P + 1])):
+        k, v = gpu_lib.kv_read(dev, _i32(table), _i32(lens), T, starts=None if starts is None else _i32(starts),
+                               dtype=_dt(dtype))
+        want = okv.read(c, table, lens, T, starts)
+        np.testing.assert_array_equal(k.double().cpu().numpy(), want[0])
+        np.testing.assert_array_equal(v.double().cpu().numpy(), want[1])
+
+
+def test_read_without_pages(gpu_lib):
+    rng = np.random.default_rng(8)
+    c, table = kh.make_cache(rng, "e4m3", [40, 40], 16, 2, 64)
+    table[0, 1], table[1, 0] = -1, 10 ** 6
+    k, v = gpu_lib.kv_read(kh.to_device(gpu_lib, c), _i32(table), _i32([10 ** 6, -2]), 50)
+    want = okv.read(c, table, [table.shape[1] * 16, 0], 50)
+    np.testing.assert_array_equal(k.double().cpu().numpy(), want[0])
+    np.testing.assert_array_equal(v.double().cpu().numpy(), want[1])
+
+
+# ------------------------------------------------------------- attention --
+def _tree(rng, B, N, bad=False):
+    par = np.array([[-1] + [int(rng.integers(0, n)) for n in range(1, N)] for _ in range(B)], np.int32)
+    if bad and N > 3:
+        par[0, 2], par[0, 3] = 7, -9
+    return par
+
+
+def _check_attention(sv, c, table, lens, q, k, v, scale, dtype, parents=None, nodes=None, lse=True, **kw):
+    (qd, q64), (kd, k64), (vd, v64) = q, k, v
+    dev = kw.pop("dev", None) or kh.to_device(sv, c)
+    got, glse = sv.kv_attention(dev, _i32(table), qd, _i32(lens), kd, vd, scale=scale, return_lse=True,
+                                parents=None if parents is None else _i32(parents),
+                                num_nodes=None if nodes is None else _i32(nodes), **kw)
+    out, wlse, mag, big, cnt = okv.attention(c, table, q64, lens, scale, k64, v64, parents, nodes)
+    tol, tol_lse = kh.attention_bounds(out, wlse, mag, big, cnt, scale, q64.shape[-1], dtype)
+    g, gl = got.double().cpu().numpy(), glse.double().cpu().numpy()
+    np.testing.assert_array_equal(np.isnan(g), np.isnan(out))
+    np.testing.assert_array_equal(np.isfinite(gl), np.isfinite(wlse))
+    err = np.where(np.isnan(out), 0.0, np.abs(g - out) - tol)
+    assert (err <= 0).all(), (np.unravel_index(err.argmax(), err.shape), err.max())
+    f = np.isfinite(wlse)
+    assert (np.abs(gl[f] - wlse[f]) <= tol_lse[f]).all()
+    return got, glse
+
+
+ATTEND = [  # fmt, dtype, P, H, G, D, N, lens, tree
+    ("e4m3", "bf16", 16, 2, 4, 128, 1, [0, 1, 63, 64, 65, 500], False),
+    ("int8", "bf16", 32, 1, 8, 64, 5, [0, 31, 32, 33, 700], False),
+    ("e4m3", "bf16", 64, 2, 4, 128, 9, [0, 5, 64, 300, 1030], False),
+    ("int8", "bf16", 64, 2, 4, 128, 16, [0, 127, 129, 640], True),
+    ("e4m3", "bf16", 128, 1, 7, 96, 13, [0, 100, 128, 400], True),
+    ("int8", "bf16", 128, 1, 2, 256, 33, [0, 1, 255, 513], True),
+    ("e4m3", "bf16", 64, 1, 3, 64, 64, [0, 70, 200], True),
+    ("e4m3", "bf16", 32, 3, 1, 256, 7, [33, 64, 0], False),
+    ("int8", "bf16", 16, 1, 16, 128, 64, [17, 90], True),
+    ("e4m3", "f32", 16, 2, 4, 128, 3, [0, 1, 63, 64, 65, 500], False),
+    ("int8", "f32", 64, 1, 8, 256, 9, [0, 31, 200], True),
+    ("int8", "f32", 32, 4, 1, 64, 9, [0, 65, 300], False),
+    ("e4m3", "f32", 128, 2, 3, 96, 40, [0, 129, 260], True),
+]
+
+
+@pytest.mark.parametrize("fmt,dtype,P,H,G,D,N,lens,tree", ATTEND)
+def test_attention(gpu_lib, fmt, dtype, P, H, G, D, N, lens, tree):
+    rng = np.random.default_rng(D + N + P)
+    B = len(lens)
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D)
+    q = _rand(rng, (B, N, H * G, D), dtype)
+    k, v = _rand(rng, (B, N, H, D), dtype), _rand(rng, (B, N, H, D), dtype)
+    par = _tree(rng, B, N, bad=True) if tree else None
+    _check_attention(gpu_lib, c, table, lens, q, k, v, D ** -0.5, dtype, par)
+    # the cached tokens alone: rows of empty sequences see nothing
+    none = (None, None)
+    got, lse = _check_attention(gpu_lib, c, table, lens, q, none, none, 0.3, dtype)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (got[b] == 0).all() and (lse[b] == -np.inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_long_and_split(gpu_lib, dtype):
+    """Few sequences with long caches next to short and empty ones: the
+    length is split over many workgroups."""
+    rng = np.random.default_rng(11)
+    lens, P, H, D, N = [9000, 0, 3, 4097], 64, 1, 64, 2
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    q = _rand(rng, (4, N, 2, D), dtype)
+    k, v = _rand(rng, (4, N, H, D), dtype), _rand(rng, (4, N, H, D), dtype)
+    _check_attention(gpu_lib, c, table, lens, q, k, v, 0.125, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_sharp_scores(gpu_lib, dtype):
+    """Scores of +-hundreds: one token carries almost all weight, and the
+    maximum grows along the sequence."""
+    rng = np.random.default_rng(12)
+    lens, P, H, D, N = [300, 129], 32, 2, 128, 4
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D)
+    q = _rand(rng, (2, N, 4, D), dtype)
+    k, v = _rand(rng, (2, N, H, D), dtype), _rand(rng, (2, N, H, D), dtype)
+    _check_attention(gpu_lib, c, table, lens, q, k, v, 20.0, dtype)
+    _check_attention(gpu_lib, c, table, lens, q, k, v, -3.0, dtype)
+    _check_attention(gpu_lib, c, table, lens, q, k, v, 0.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_ragged_nodes(gpu_lib, dtype):
+    rng = np.random.default_rng(13)
+    lens, P, H, D, N = [70, 0, 16, 33, 5], 16, 2, 64, 12
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    q = _rand(rng, (5, N, 6, D), dtype)
+    k, v = _rand(rng, (5, N, H, D), dtype), _rand(rng, (5, N, H, D), dtype)
+    nodes = [12, 0, -4, 7, 99]
+    for par in (None, _tree(rng, 5, N)):
+        got, lse = _check_attention(gpu_lib, c, table, lens, q, k, v, 0.125, dtype, par, nodes)
+        for b, n in enumerate([12, 0, 0, 7, 12]):
+            assert (got[b, n:] == 0).all() and (lse[b, n:] == -np.inf).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [6, 40])
+def test_attention_nan_and_infinity_in_unseen_nodes(gpu_lib, dtype, N):
+    """NaN, infinities and the type's largest values in nodes reach exactly
+    the queries that see them."""
+    import torch
+    rng = np.random.default_rng(14)
+    lens, P, H, D = [50, 0, 17], 16, 2, 64
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D)
+    q, k, v = (_rand(rng, (3, N, h, D), dtype) for h in (4, H, H))
+    par = _tree(rng, 3, N)
+    par[:, 3], par[:, 4], par[:, 5] = 1, 0, 0
+    see = np.stack([okv.node_sets(par[b], N) for b in range(3)])
+    dev = kh.to_device(gpu_lib, c)
+    args = (dev, _i32(table))
+    clean = gpu_lib.kv_attention(*args, q[0], _i32(lens), k[0], v[0], parents=_i32(par))
+    big = float(torch.finfo(_dt(dtype)).max)
+    for val in (float("nan"), float("inf"), -float("inf"), big, -big):
+        for where in ("k", "v"):
+            kk, vv = k[0].clone(), v[0].clone()
+            (kk if where == "k" else vv)[:, 3, :, 7] = val
+            got = gpu_lib.kv_attention(*args, q[0], _i32(lens), kk, vv, parents=_i32(par))
+            blind = torch.from_numpy(~see[:, :, 3]).cuda()
+            assert torch.equal(got[blind], clean[blind]), (val, where)
+            if val != val:
+                seen = got[~blind]
+                assert (seen.isnan().any(-1) if where == "v" else seen.isnan().all(-1)).all()
+            elif where == "v" and abs(val) == float("inf"):
+                assert (got[~blind][..., 7] == val).all() and got[~blind][..., :7].isfinite().all()
+
+
+def test_attention_bad_pages_and_lengths(gpu_lib):
+    """Positions without a page are not seen; lengths are clamped."""
+    rng = np.random.default_rng(15)
+    lens, P, H, D, N = [200, 200, 200, 200], 16, 2, 64, 3
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    table[0, 2], table[1, 12], table[2, :] = -1, 2 ** 31 - 1, -1
+    q, k, v = (_rand(rng, (4, N, h, D), "f32") for h in (4, H, H))
+    # a length past the table is clamped to it: the free slots it then reaches hold NaN here
+    _check_attention(gpu_lib, c, table, [10 ** 9, 200, 200, -1], q, k, v, 0.125, "f32")
+    full, ftab = kh.make_cache(rng, "e4m3", [14 * P] * 4, P, H, D, poison=False)
+    _check_attention(gpu_lib, full, ftab[:, :14], [10 ** 9, 14 * P, 0, -1], q, k, v, 0.125, "f32")
+    _check_attention(gpu_lib, c, table, [200, 200, 200, 0], q, (None, None), (None, None), 0.125, "f32")
+
+
+def test_attention_arbitrary_scales_and_shared_pages(gpu_lib):
+    """Scales that are no powers of two, and a prefix that two sequences share."""
+    rng = np.random.default_rng(16)
+    lens, P, H, D, N = [100, 100], 32, 2, 128, 3
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D)
+    c["k_scales"] = (c["k_scales"] * 1.37).astype(np.float32)
+    c["v_scales"] = (c["v_scales"] * 0.71).astype(np.float32)
+    table[1, :3] = table[0, :3]
+    q, k, v = (_rand(rng, (2, N, h, D), "bf16") for h in (4, H, H))
+    _check_attention(gpu_lib, c, table, lens, q, k, v, 0.1, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_fused_rows_and_repeatability(gpu_lib, dtype):
+    """q, k and v as slices of one projection's rows give the bits of
+    contiguous copies, twice."""
+    import torch
+    rng = np.random.default_rng(17)
+    lens, P, H, G, D, N = [1000, 0, 77], 64, 2, 4, 128, 5
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32(lens)
+    fused, _ = _rand(rng, (3, N, H * G + 2 * H, D), dtype)
+    q, k, v = fused[:, :, :H * G], fused[:, :, H * G:H * G + H], fused[:, :, H * G + H:]
+    a = gpu_lib.kv_attention(dev, tab, q, ln, k, v, return_lse=True)
+    for _ in range(3):
+        b = gpu_lib.kv_attention(dev, tab, q.contiguous(), ln, k.contiguous(), v.contiguous(), return_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    one = gpu_lib.kv_attention(dev, tab, q[:, :1], ln, k[:, :1], v[:, :1])  # N = 1: rows far apart
+    assert torch.equal(one, gpu_lib.kv_attention(dev, tab, q[:, :1].contiguous(), ln, k[:, :1].contiguous(),
+                                                 v[:, :1].contiguous()))
+
+
+def test_other_stream_and_graph(gpu_lib):
+    """Attention, append and read on a side stream, then captured into one
+    graph and replayed between eager work; every replay gives the eager bits."""
+    import torch
+    rng = np.random.default_rng(18)
+    lens, P, H, D, N = [130, 5], 16, 2, 64, 4
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D, extra=N)
+    q, k, v = (_rand(rng, (2, N, h, D), "bf16")[0] for h in (4, H, H))
+    tab, ln = _i32(table), _i32(lens)
+
+    def step(dev, ws):
+        out, lse = gpu_lib.kv_attention(dev, tab, q, ln, k, v, return_lse=True, workspace=ws)
+        after = gpu_lib.kv_append(dev, tab, k, v, ln)
+        return (out, lse, after) + gpu_lib.kv_read(dev, tab, after, 140)
+
+    dev = kh.to_device(gpu_lib, c)
+    ws = torch.empty(gpu_lib.kv_attention_workspace_size(dev, 2, N, 4, table.shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    want = [t.clone() for t in step(kh.to_device(gpu_lib, c), ws)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step(dev, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the append may have rounded the begun blocks again; from here on the same call changes nothing
+    want = [t.clone() for t in step(dev, ws)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(dev, ws)
+    for _ in range(4):
+        for t in outs:
+            t.fill_(1)
+        ws.fill_(0xff)
+        graph.replay()
+        eager = step(dev, torch.empty_like(ws))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager, want))
+
+
+def test_verify_round_with_trees(gpu_lib):
+    """A run of them together: prompts cached, then rounds of attention over
+    a token tree, greedy verification of the logits its outputs give, and the
+    accepted path appended straight from the verification's outputs."""
+    import torch
+    rng = np.random.default_rng(19)
+    B, N, H, G, D, P, V = 4, 12, 2, 2, 64, 16, 50
+    prompt = [0, 9, 16, 40]
+    c, table = kh.make_cache(rng, "e4m3", [0] * B, P, H, D, extra=40 + 4 * N, poison=False)
+    dev, tab = kh.to_device(gpu_lib, c), _i32(table)
+    (k, k64), (v, v64) = _rand(rng, (B, 40, H, D), "bf16"), _rand(rng, (B, 40, H, D), "bf16")
+    cur = gpu_lib.kv_append(dev, tab, k, v, _i32([0] * B), counts=_i32(prompt))
+    lens = okv.append(c, table, k64, v64, [0] * B, prompt)
+    head = torch.from_numpy(rng.normal(size=(H * G * D, V)).astype(np.float32)).cuda()
+    for _ in range(3):
+        par = _tree(rng, B, N)
+        (q, q64), (k, k64), (v, v64) = (_rand(rng, (B, N, h, D), "bf16") for h in (H * G, H, H))
+        out, _ = _check_attention(gpu_lib, c, table, lens, (q, q64), (k, k64), (v, v64), D ** -0.5, "bf16", par,
+                                  dev=dev)
+        logits = (out.float().view(B, N, -1) @ head).contiguous()
+        tok = np.zeros((B, N), np.int32)
+        arg = logits.argmax(-1).cpu().numpy()
+        for b in range(B):  # half of the nodes propose the target's choice after their parent
+            for n in range(1, N):
+                tok[b, n] = arg[b, par[b, n]] if rng.random() < 0.6 else (arg[b, par[b, n]] + 1) % V
+        _, path, n_acc = gpu_lib.verify_tree_greedy(logits, _i32(tok), _i32(par))
+        want = verify_tree_greedy(logits.cpu().numpy(), tok, par)
+        np.testing.assert_array_equal(path.cpu().numpy(), want[1])
+        cur = gpu_lib.kv_append(dev, tab, k, v, cur, index=path)
+        lens = okv.append(c, table, k64, v64, lens, index=path.cpu().numpy())
+        np.testing.assert_array_equal(cur.cpu().numpy(), lens)
+        np.testing.assert_array_equal(n_acc.cpu().numpy() + 1 + np.asarray(prompt), lens)
+        prompt = lens
+        _same_cache(kh.to_host(dev, "e4m3"), c)
+    kk, vv = gpu_lib.kv_read(dev, tab, cur, int(lens.max()))
+    want = okv.read(c, table, lens, int(lens.max()))
+    np.testing.assert_array_equal(kk.double().cpu().numpy(), want[0])
+    np.testing.assert_array_equal(vv.double().cpu().numpy(), want[1])

@@ -1,0 +1,194 @@
+"""The 8-bit cache's C ABI and binding without a GPU: sizes, refusals on the
+host before any HIP call, and the same checks under AddressSanitizer."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import speculative_sampling_verify_spec_amd as sv
+from speculative_sampling_verify_spec_amd import _kv
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "speculative_sampling_verify_spec_amd", "csrc")
+F32, BF16 = sv.SPECV_F32, sv.SPECV_BF16
+BASE = 0x10000  # fake device addresses: every call fails before it could touch them
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sv.load()
+
+
+def kv(**kw):
+    a = dict(k_pages=BASE, v_pages=2 * BASE, k_scales=3 * BASE, v_scales=4 * BASE, page_table=5 * BASE, num_pages=100,
+             max_pages=10, page_size=64, heads=8, dim=128, type=sv.SPECV_E4M3)
+    a.update(kw)
+    return _kv._Descriptor(**a)
+
+
+BAD_CACHE = [(dict(k_pages=None), -1), (dict(v_pages=None), -1), (dict(k_scales=None), -1), (dict(v_scales=None), -1),
+             (dict(page_table=None), -1), (dict(type=2), -3), (dict(type=-1), -3), (dict(page_size=0), -2),
+             (dict(page_size=8), -2), (dict(page_size=48), -2), (dict(page_size=256), -2), (dict(num_pages=0), -2),
+             (dict(max_pages=0), -2), (dict(max_pages=1 << 25), -2), (dict(heads=0), -2), (dict(heads=1 << 15), -2),
+             (dict(dim=0), -2), (dict(dim=80), -2), (dict(dim=512), -2), (dict(k_pages=BASE + 8), -6),
+             (dict(v_pages=BASE + 1), -6), (dict(k_scales=BASE + 2), -6)]
+
+
+def append(lib, c=None, **kw):
+    a = dict(k=6 * BASE, v=7 * BASE, row=0, lengths=8 * BASE, counts=None, index=None, B=4, N=3, out=None, dtype=BF16)
+    a.update(kw)
+    c = kv() if c is None else c
+    return lib.spec_kv_append(ctypes.byref(c), a["k"], a["v"], a["row"], a["lengths"], a["counts"], a["index"], a["B"],
+                              a["N"], a["out"], a["dtype"], None)
+
+
+def read(lib, c=None, **kw):
+    a = dict(starts=None, lengths=8 * BASE, B=4, T=3, k=6 * BASE, v=7 * BASE, dtype=BF16)
+    a.update(kw)
+    c = kv() if c is None else c
+    return lib.spec_kv_read(ctypes.byref(c), a["starts"], a["lengths"], a["B"], a["T"], a["k"], a["v"], a["dtype"], None)
+
+
+def attend(lib, c=None, **kw):
+    a = dict(q=6 * BASE, qs=0, k=7 * BASE, v=8 * BASE, ks=0, lengths=9 * BASE, nodes=None, parents=None, scale=0.1, B=4,
+             N=3, Hq=32, out=10 * BASE, lse=None, dtype=BF16, ws=16 * BASE, wsb=1 << 40)
+    a.update(kw)
+    c = kv() if c is None else c
+    return lib.spec_kv_attention(ctypes.byref(c), a["q"], a["qs"], a["k"], a["v"], a["ks"], a["lengths"], a["nodes"],
+                                 a["parents"], a["scale"], a["B"], a["N"], a["Hq"], a["out"], a["lse"], a["dtype"],
+                                 a["ws"], a["wsb"], None)
+
+
+def test_header_constants():
+    text = open(os.path.join(ROOT, "include", "specverify.h")).read()
+    assert re.search(r"SPECV_E4M3 = (\d+)", text).group(1) == str(sv.SPECV_E4M3)
+    assert re.search(r"SPECV_I8 = (\d+)", text).group(1) == str(sv.SPECV_I8)
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHE)
+def test_bad_caches(lib, kw, code):
+    assert append(lib, kv(**kw)) == code
+    assert read(lib, kv(**kw)) == code
+    assert attend(lib, kv(**kw)) == code
+    assert lib.spec_kv_attention_workspace_size(ctypes.byref(kv(**kw)), 4, 3, 32) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), -3), (dict(k=None), -1), (dict(v=None), -1), (dict(lengths=None), -1), (dict(B=0), -2),
+    (dict(B=65536), -2), (dict(N=0), -2), (dict(N=(1 << 24) + 1), -2), (dict(row=8 * 128 - 8), -2), (dict(row=-1), -2),
+    (dict(row=8 * 128 + 4), -6), (dict(k=BASE + 8), -6), (dict(v=BASE + 4), -6)])
+def test_append_refusals(lib, kw, code):
+    assert append(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=-1), -3), (dict(lengths=None), -1), (dict(k=None, v=None), -1), (dict(B=0), -2), (dict(T=0), -2),
+    (dict(T=(1 << 24) + 1), -2), (dict(B=65536), -2), (dict(k=BASE + 8), -6), (dict(v=BASE + 8), -6)])
+def test_read_refusals(lib, kw, code):
+    assert read(lib, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=7), -3), (dict(q=None), -1), (dict(lengths=None), -1), (dict(out=None), -1), (dict(k=None), -1),
+    (dict(v=None), -1), (dict(B=0), -2), (dict(B=65536), -2), (dict(N=0), -2), (dict(N=65), -2), (dict(Hq=0), -2),
+    (dict(Hq=12), -2), (dict(Hq=1 << 15), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2),
+    (dict(qs=100), -2), (dict(qs=32 * 128 + 4), -6), (dict(ks=8 * 128 + 1), -6), (dict(q=BASE + 2), -6),
+    (dict(k=BASE + 8), -6), (dict(v=BASE + 8), -6), (dict(out=BASE + 8), -6), (dict(ws=None), -5),
+    (dict(ws=BASE + 16), -5), (dict(wsb=8), -5)])
+def test_attention_refusals(lib, kw, code):
+    assert attend(lib, **kw) == code
+
+
+def test_null_descriptor(lib):
+    assert lib.spec_kv_append(None, BASE, BASE, 0, BASE, None, None, 1, 1, None, BF16, None) == -1
+    assert lib.spec_kv_read(None, None, BASE, 1, 1, BASE, BASE, BF16, None) == -1
+    assert lib.spec_kv_attention_workspace_size(None, 1, 1, 8) == 0
+
+
+def test_workspace_sizes(lib):
+    """Every valid shape has a size, and it does not overflow at the largest ones."""
+    for B, N, Hq, c in ((1, 1, 8, kv()), (256, 9, 32, kv()), (65535, 64, 1024, kv(heads=512, dim=256)),
+                        (1, 64, 32760, kv(heads=8, dim=256, max_pages=(1 << 24) - 1))):
+        n = lib.spec_kv_attention_workspace_size(ctypes.byref(c), B, N, Hq)
+        assert 0 < n < 1 << 46 and n % 256 == 0, (B, N, Hq, n)
+    for B, N, Hq in ((0, 1, 8), (1, 0, 8), (1, 65, 8), (1, 1, 0), (1, 1, 9), (65536, 1, 8)):
+        assert lib.spec_kv_attention_workspace_size(ctypes.byref(kv()), B, N, Hq) == 0
+
+
+def _parts(pages=4, h=2, p=16, d=64, dtype=torch.int8):
+    return [torch.zeros(pages, h, p, d, dtype=dtype), torch.zeros(pages, h, d, p, dtype=dtype),
+            torch.zeros(pages, h), torch.zeros(pages, h)]
+
+
+def test_cache_checks():
+    c = sv.KVCache(*_parts())
+    assert (c.page_size, c.heads, c.dim) == (16, 2, 64)
+    assert sv.KVCache.empty(3, 32, 1, 96, device="cpu").k_pages.dtype == torch.float8_e4m3fn
+    for i, bad in ((0, torch.zeros(4, 2, 16, 64)), (0, torch.zeros(4, 2, 16, dtype=torch.int8)),
+                   (0, torch.zeros(4, 2, 8, 64, dtype=torch.int8)), (0, torch.zeros(4, 2, 16, 80, dtype=torch.int8)),
+                   (1, torch.zeros(4, 2, 16, 64, dtype=torch.int8)), (1, torch.zeros(4, 2, 64, 16, dtype=torch.uint8)),
+                   (2, torch.zeros(4, 2, dtype=torch.float64)), (3, torch.zeros(4, 3)),
+                   (1, torch.zeros(4, 2, 16, 64, dtype=torch.int8).transpose(2, 3)), (2, torch.zeros(2, 4).t())):
+        parts = _parts()
+        parts[i] = bad
+        with pytest.raises((TypeError, ValueError)):
+            sv.KVCache(*parts)
+
+
+def test_host_tensors_are_refused():
+    c = sv.KVCache(*_parts())
+    tab, ln = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    x = torch.zeros(1, 3, 2, 64)
+    for call in (lambda: sv.kv_append(c, tab, x, x, ln), lambda: sv.kv_read(c, tab, ln, 3),
+                 lambda: sv.kv_attention(c, tab, x, ln, x, x)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_token_strides():
+    f = _kv._token_stride
+    x = torch.zeros(3, 5, 10, 64)
+    assert f("x", x[:, :, :4], 4, 64) == 640 and f("x", x[:, :, 9:], 1, 64) == 640
+    assert f("x", x[:, :1, :4], 4, 64) == 3200 and f("x", x[:1, :1, :4], 4, 64) == 256
+    assert f("x", x[:1, 1:3, :4], 4, 64) == 640
+    for bad in (x[:, :, ::2], x[:, :3], x[..., ::2], x.transpose(1, 2), x[:, :1].expand(3, 5, 10, 64),
+                x[:1, :1].expand(3, 1, 10, 64)):
+        with pytest.raises(ValueError):
+            f("x", bad, bad.shape[2], bad.shape[3])
+
+
+STUBS = """
+#include "specverify.h"
+#include "sv_kv.h"
+namespace sv {
+hipError_t launch_kv_append(const KvAppend&, int, int, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_kv_read(const KvRead&, int, int, hipStream_t) { return hipErrorInvalidValue; }
+hipError_t launch_kv_attention(const KvAttn&, int, int, hipStream_t) { return hipErrorInvalidValue; }
+}
+"""
+
+
+def test_host_checks_under_address_sanitizer(tmp_path):
+    gxx = shutil.which("g++")
+    asan = subprocess.run([gxx, "-print-file-name=libasan.so"], capture_output=True, text=True).stdout.strip() \
+        if gxx else ""
+    if not os.path.isabs(asan) or not os.path.exists(asan):
+        pytest.skip("g++ or libasan not found")
+    stubs, so = tmp_path / "stubs.cpp", tmp_path / "libkv_asan.so"
+    stubs.write_text(STUBS)
+    r = subprocess.run([gxx, "-std=c++17", "-shared", "-fPIC", "-g", "-O1", "-fsanitize=address", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", "/opt/rocm/include",
+                        os.path.join(CSRC, "api_kv.cpp"), str(stubs), "-o", str(so)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    env = dict(os.environ, LD_PRELOAD=asan, ASAN_OPTIONS="detect_leaks=0:halt_on_error=1")
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "tests", "asan", "host_checks_kv.py"), str(so)],
+                       capture_output=True, text=True, timeout=300, env=env)
+    out = r.stdout + r.stderr
+    assert "AddressSanitizer" not in out, out[-4000:]
+    assert r.returncode == 0 and "host checks ok" in r.stdout, out[-4000:]
