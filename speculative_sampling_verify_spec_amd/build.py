@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cpp", "k_sweep.hip", "k_rounds.hip", "k_verify.hip", "k_exact.hip", "k_short.hip", "k_greedy.hip", "k_stats.hip",
            "k_tree.hip", "k_ngram.hip", "k_ngram_map.hip", "k_validate.hip", "api_kv.cpp", "k_kv_cache.hip",
-           "k_kv_attn.hip"]
+           "k_kv_attn_64.hip", "k_kv_attn_96.hip", "k_kv_attn_128.hip", "k_kv_attn_256.hip", "k_kv_join.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

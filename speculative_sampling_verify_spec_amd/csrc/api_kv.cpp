@@ -1,6 +1,7 @@
 // Host side of the 8-bit paged cache: argument checks and launches of
 // spec_kv_append, spec_kv_read and spec_kv_attention.  Nothing here
 // allocates, synchronises or keeps state.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -53,6 +54,41 @@ int check_row(int64_t* row, long heads, int D, int dtype) {
   return *row * (dtype == SPECV_F32 ? 4 : 2) % 16 ? SPECV_E_ALIGN : SPECV_OK;
 }
 
+// How an attention call is cut into workgroups; from sizes alone (the lengths
+// are on the device), so that the workspace's size is known before.
+struct KvPlan {
+  int mt, mb, granule, splits;
+};
+
+constexpr long kTargetGroups = 2048;  // workgroups to aim at: 256 CUs, a few resident each, a few times over
+constexpr int kMinGranule = 4;        // tiles per part, at least one for each wave
+
+KvPlan kv_plan(const KvView& c, int B, int N, int Hq, int dtype) {
+  KvPlan pl;
+  const int rows = N * (Hq / c.H), most = 16 * kv_max_mt(dtype, c.D);
+  pl.mb = (rows + most - 1) / most;
+  pl.mt = ((rows + pl.mb - 1) / pl.mb + 15) / 16;
+  const long tiles = ((static_cast<long>(c.width) << c.pshift) + 63) / 64;
+  const long groups = static_cast<long>(B) * c.H * pl.mb;
+  const long per = std::max(1L, kTargetGroups / groups);  // parts a longest sequence should have
+  pl.granule = static_cast<int>(std::max<long>(kMinGranule, (tiles + per - 1) / per));
+  pl.splits = static_cast<int>(std::max(1L, (tiles + pl.granule - 1) / pl.granule));
+  return pl;
+}
+
+bool valid_attention(const KvView& c, int B, int N, int Hq) {
+  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % c.H) return false;
+  for (int dt : {SPECV_F32, SPECV_BF16}) {  // a grid's workgroups times their threads stay below 2^32
+    const KvPlan pl = kv_plan(c, B, N, Hq, dt);
+    if ((static_cast<long>(B) * c.H * pl.splits + 7) * pl.mb * 256 >= (1L << 32)) return false;
+  }
+  return static_cast<long>(B) * N * Hq * 64 < (1L << 32);
+}
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+size_t part_rows(int B, int N, int Hq, const KvPlan& pl) { return static_cast<size_t>(B) * N * Hq * pl.splits; }
+
 }  // namespace
 }  // namespace sv
 
@@ -104,8 +140,14 @@ size_t spec_kv_attention_workspace_size(const specv_kv_t* kv, int B, int N, int 
   using namespace sv;
   KvView c{};
   if (check_cache(kv, &c) != SPECV_OK) return 0;
-  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % c.H) return 0;
-  return kAlign;
+  if (!valid_attention(c, B, N, Hq)) return 0;
+  size_t most = kAlign;  // a call in one part per sequence uses none of it
+  for (int dt : {SPECV_F32, SPECV_BF16}) {
+    const KvPlan pl = kv_plan(c, B, N, Hq, dt);
+    const size_t rows = part_rows(B, N, Hq, pl);
+    if (pl.splits > 1) most = std::max(most, align_up(rows * c.D * sizeof(float)) + align_up(rows * sizeof(float2)));
+  }
+  return most;
 }
 
 int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, const void* k_new, const void* v_new,
@@ -117,8 +159,7 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
   if (dtype != SPECV_F32 && dtype != SPECV_BF16) return SPECV_E_DTYPE;
   if (const int rc = check_cache(kv, &p.c)) return rc;
   if (!q || !lengths || !out || !k_new != !v_new) return SPECV_E_NULL;
-  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % p.c.H)
-    return SPECV_E_SHAPE;
+  if (!valid_attention(p.c, B, N, Hq)) return SPECV_E_SHAPE;
   if (!std::isfinite(scale)) return SPECV_E_SHAPE;
   if (const int rc = check_row(&q_stride, Hq, p.c.D, dtype)) return rc;
   if (k_new)
@@ -142,6 +183,14 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
   p.G = Hq / p.c.H;
   p.out = out;
   p.lse = out_lse;
+  const KvPlan pl = kv_plan(p.c, B, N, Hq, dtype);
+  p.mt = pl.mt;
+  p.mb = pl.mb;
+  p.granule = pl.granule;
+  p.splits = pl.splits;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
+                                        align_up(part_rows(B, N, Hq, pl) * p.c.D * sizeof(float)));
   return launch_kv_attention(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK
                                                                                                 : SPECV_E_HIP;
 }

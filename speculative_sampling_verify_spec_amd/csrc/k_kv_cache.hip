@@ -32,21 +32,6 @@ __device__ inline void load4(const void* row, long i, float* f) {
   }
 }
 
-// Four elements to a row; bf16 by round to nearest even.  What the cache
-// holds (4 or 7 significant bits times a power of two) is exact in bf16.
-template <int DT>
-__device__ inline void store4(void* row, long i, const float* f) {
-  if constexpr (DT == SPECV_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(row) + i) = make_float4(f[0], f[1], f[2], f[3]);
-  } else {
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    bf16x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = static_cast<__bf16>(f[j]);
-    *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(row) + i) = v;
-  }
-}
-
 __device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
   v = wave_min_i32(v);
   __syncthreads();
@@ -182,7 +167,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] *= s;
     }
-    store4<DT>(out, ((b * p.T + (pos - start)) * c.H + h) * c.D + d, f);
+    kv_store4<DT>(out, ((b * p.T + (pos - start)) * c.H + h) * c.D + d, f);
   }
 }
 

@@ -1,0 +1,550 @@
+// Attention of a draft's nodes over the 8-bit paged cache and over the nodes
+// themselves (the kernel template; k_kv_attn_<dim>.hip instantiate it).
+//
+// The R = N G queries that share a cached head (N nodes, G query heads per
+// cached head) are the columns of every product, so a cached byte is read
+// once for all of them:
+//   S^T = K Q^T       A = 16 tokens x 32 channels,  B = 32 channels x 16 queries
+//   O^T += V^T P^T    A = 16 channels x 32 tokens,  B = 32 tokens x 16 queries
+// with v_mfma_f32_16x16x32_bf16.  Codes become bf16 exactly (4 or 7
+// significant bits); a block's K scale multiplies the scores of its tokens,
+// its V scale their weights.
+//
+// A wave takes 64 tokens at a time.  Tile t (0..3) of S^T has token 16 (i/4)
+// + 4 t + i%4 in its row i, so that the four results a lane gets from each of
+// the four tiles belong to 16 consecutive tokens: the softmax's weights are
+// then already the B operand of the second product, and the matching A
+// operand is 16 consecutive bytes of a transposed V page.  Nothing passes
+// through LDS until the end, there is no barrier in the loop, and every load
+// is 16 bytes a lane.  The channels of Q are permuted the way 16-byte loads
+// of K deliver them.
+//
+// Softmax: the running maximum is held per query and only moved when a tile
+// exceeds it by more than 2^8 (the weights then stay below 2^8, and the sums
+// are in 32 bits), so most tiles rescale nothing.
+//
+// 32-bit inputs: q, the weights, and the nodes' k and v are split into three
+// bf16 pieces whose sum has 24 bits; products with codes take three matrix
+// instructions, products of two split operands the six largest of nine.
+#pragma once
+
+#include "sv_device.h"
+#include "sv_kv.h"
+
+namespace sv {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLazyMax = 8.f;  // log2: how far a score may exceed the held maximum
+
+// Eight codes to bf16, exact.
+template <int FMT>
+__device__ inline bf16x8 codes8(uint32_t a, uint32_t b) {
+  union { uint32_t w[4]; bf16x2 h[4]; bf16x8 v; } u;
+  if constexpr (FMT == SPECV_E4M3) {
+    u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
+    u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
+    u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
+    u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
+  } else {
+    // integers up to 127 have at most 7 significant bits: their floats' upper halves are their bf16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? a : b;
+      const int s = 16 * (i & 1);
+      const uint32_t lo = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> s)));
+      const uint32_t hi = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> (s + 8))));
+      u.w[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+    }
+  }
+  return u.v;
+}
+
+__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Number of bf16 pieces of an element.
+template <int DT>
+constexpr int kPieces = DT == SPECV_F32 ? 3 : 1;
+
+// x as a sum of NP bf16 pieces.  One piece: round to nearest.  Three: the
+// leading 8 bits, the next 8 and the last 8 of the 24, an exact sum (by
+// truncation, so that the largest floats stay finite); x that is not finite
+// is its own first piece.
+template <int NP>
+__device__ inline void split(float x, __bf16* piece) {
+  if constexpr (NP == 1) {
+    piece[0] = static_cast<__bf16>(x);
+  } else {
+    auto lead = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
+    auto bits = [](float f) { return __builtin_bit_cast(__bf16, static_cast<uint16_t>(__float_as_uint(f) >> 16)); };
+    piece[0] = bits(x);
+    const float r = isfinite(x) ? x - lead(x) : 0.f;
+    piece[1] = bits(r);
+    piece[2] = bits(r - lead(r));
+  }
+}
+
+// Eight consecutive elements as NP operand fragments.
+template <int DT>
+__device__ inline void load8(const void* base, long i, bf16x8* frag) {
+  if constexpr (DT == SPECV_BF16) {
+    frag[0] = *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(base) + i);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const float4 x = p[0], y = p[1];
+    const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      __bf16 s[3];
+      split<3>(f[j], s);
+      frag[0][j] = s[0];
+      frag[1][j] = s[1];
+      frag[2][j] = s[2];
+    }
+  }
+}
+
+template <int DT>
+__device__ inline float load1(const void* base, long i) {
+  if constexpr (DT == SPECV_F32) return static_cast<const float*>(base)[i];
+  else return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
+}
+
+// First channel of the 8 that lane group g holds of fragment f: fragments 2c
+// and 2c + 1 are the halves of the 16 bytes a lane loads of 64 channels; a
+// last odd fragment is an 8-byte load of 32.
+template <int D>
+__device__ inline int chan(int f, int g) {
+  return f < D / 64 * 2 ? f / 2 * 64 + 16 * g + f % 2 * 8 : D / 64 * 64 + 8 * g;
+}
+
+// Maximum and sum over the four lanes that hold the same query (lane % 16).
+__device__ inline float groups_max(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const unsigned w = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float groups_sum(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const unsigned w = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+constexpr int kTile = 64;                       // cached tokens a wave takes at a time
+constexpr int kDc = 128;                        // channels per round of the final join
+constexpr int kJoinRow = kDc + 4;               // its padded row in LDS
+
+// One workgroup: MT x 16 queries of one (sequence, cached head) over one of
+// the parts of the sequence's tokens; its waves take the part's tiles in turn.
+template <int DT, int FMT, int D, int MT>
+__global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
+  constexpr int NP = kPieces<DT>, NF = D / 32, ND = D / 16, NC = D / 64;
+  const KvView& c = p.c;
+  // workgroups of one part and head that differ only in their queries read
+  // the same cache: eight apart, they run on the same XCD and share its L2
+  const int per = 8 * p.mb;
+  const long outer = static_cast<long>(blockIdx.x / per) * 8 + blockIdx.x % 8;
+  const int mblk = blockIdx.x % per / 8;
+  const int part = static_cast<int>(outer % p.splits);
+  const long pair = outer / p.splits;
+  if (pair >= static_cast<long>(p.B) * c.H) return;
+  const int h = static_cast<int>(pair % c.H);
+  const long b = pair / c.H;
+  const int len = kv_len(c, p.lengths, b);
+  const int ntile = (len >> 6) + ((len & 63) != 0);
+  const int parts = kv_parts(ntile, p.granule);
+  if (part >= parts) return;
+  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  const int col = lane % 16, g = lane / 16;
+  const int nn = p.nodes ? min(max(p.nodes[b], 0), p.N) : p.N;
+  const int rows = nn * p.G;           // queries that exist
+  const int row0 = mblk * MT * 16;
+
+  // ---- queries: B operands, negated where the scale is (kept >= 0) ----
+  const float kscale = fabsf(p.scale) * kLog2e;
+  bf16x8 qf[MT][NF][NP];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = row0 + mt * 16 + col;
+    if (r < rows) {
+      const int n = r / p.G;
+      const long base = (b * p.N + n) * p.q_row + static_cast<long>(h * p.G + (r - n * p.G)) * D;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        load8<DT>(p.q, base + chan<D>(f, g), qf[mt][f]);
+        if (p.scale < 0.f)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) qf[mt][f][i] = -qf[mt][f][i];
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) qf[mt][f][i] = bf16x8{};
+    }
+  }
+
+  f32x4 o[MT][ND];
+  float m[MT], l[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = -INFINITY;
+    l[mt] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[mt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // moves the held maximum of a query to x, its maximum so far, where x
+  // exceeds it by too much; each query decides for itself, so that its bits do
+  // not depend on what the queries beside it see
+  auto raise = [&](int mt, float x) {
+    const bool need = x > m[mt] + kLazyMax;  // true for the first finite x
+    if (!__any(need)) return;
+    const float a = need ? ex2(m[mt] - x) : 1.f;
+    m[mt] = need ? x : m[mt];
+    l[mt] *= a;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[mt][d] *= a;
+  };
+
+  // ---- cached tokens ----
+  const int tile0 = static_cast<int>(static_cast<long>(ntile) * part / parts);
+  const int tile1 = static_cast<int>(static_cast<long>(ntile) * (part + 1) / parts);
+  uint4 kraw[4][NC > 0 ? NC : 1], vraw[ND];
+  uint2 ktail[4];
+  const size_t blkbytes = static_cast<size_t>(c.P) * D;
+  // page of this lane's 16 tokens (group g) of a tile, -1: none
+  auto page_of = [&](int tile) {
+    const unsigned tok = static_cast<unsigned>(tile) * kTile + 16 * g;
+    return kv_page(c, b, tok >> c.pshift);
+  };
+  auto load_k = [&](int tile, int pid) {
+    const int grp = col >> 2;
+    const int id = max(__shfl(pid, grp * 16, kWave), 0);
+    const int off = ((tile % 2 * kTile + 16 * grp) & (c.P - 1)) + (col & 3);  // pages of at most two tiles
+    const uint8_t* a = c.kp + (static_cast<size_t>(id) * c.H + h) * blkbytes + static_cast<size_t>(off) * D;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) kraw[t][i] = *reinterpret_cast<const uint4*>(a + 4 * t * D + 64 * i + 16 * g);
+      if constexpr (NF % 2) ktail[t] = *reinterpret_cast<const uint2*>(a + 4 * t * D + 64 * NC + 8 * g);
+    }
+  };
+  float ks = 0.f, vs = 0.f;
+  auto load_v = [&](int tile, int pid) {
+    const size_t blk = static_cast<size_t>(max(pid, 0)) * c.H + h;
+    const uint8_t* a = c.vp + blk * blkbytes + static_cast<size_t>(col) * c.P + ((tile % 2 * kTile + 16 * g) & (c.P - 1));
+#pragma unroll
+    for (int d = 0; d < ND; ++d) vraw[d] = *reinterpret_cast<const uint4*>(a + static_cast<size_t>(16 * d) * c.P);
+    ks = c.ks[blk];
+    vs = c.vs[blk];
+  };
+  int tile = tile0 + w;
+  int pid = -1, pid_next = -1;
+  if (tile < tile1) {
+    pid = page_of(tile);
+    pid_next = page_of(tile + kWaves);
+    load_k(tile, pid);
+    load_v(tile, pid);
+  }
+  for (; tile < tile1; tile += kWaves) {
+    f32x4 s[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const bf16x8 kf = f < 2 * NC ? (f % 2 ? codes8<FMT>(kraw[t][f / 2].z, kraw[t][f / 2].w)
+                                              : codes8<FMT>(kraw[t][f / 2].x, kraw[t][f / 2].y))
+                                     : codes8<FMT>(ktail[t].x, ktail[t].y);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = NP - 1; i >= 0; --i) s[mt][t] = mfma(kf, qf[mt][f][i], s[mt][t]);
+      }
+    const bool more = tile + kWaves < tile1;
+    if (more) load_k(tile + kWaves, pid_next);
+    // tokens of this lane's 16 that exist; the bytes behind them, and scales
+    // of no page, may be anything (NaN too) and are cleared
+    const int have = pid < 0 ? 0 : min(max(len - tile * kTile - 16 * g, 0), 16);
+    const bool whole = __all(have == 16);
+    if (!whole) {
+      if (have == 0) ks = vs = 0.f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&vraw[d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = have - 4 * i;
+          x[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+        }
+      }
+    }
+    const float kc = ks * kscale;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float x = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float y = s[mt][t][r] * kc;
+          if (!whole && 4 * t + r >= have) y = -INFINITY;
+          s[mt][t][r] = y;
+          x = fmaxf(x, y);
+        }
+      raise(mt, groups_max(x));
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float e = ex2(s[mt][t][r] - m[mt]);
+          if (!whole && 4 * t + r >= have) e = 0.f;  // also where the maximum is still -inf
+          sum += e;
+          s[mt][t][r] = e * vs;
+        }
+      l[mt] += sum;
+    }
+    // weights as B operands: bf16 (half a step of 2^-8 relative, as the
+    // output's own type has), or their three pieces
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      bf16x8 pf[MT][NP];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          __bf16 piece[3];
+          split<NP>(s[mt][2 * j + e / 4][e % 4], piece);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) pf[mt][i][e] = piece[i];
+        }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const bf16x8 vf = j ? codes8<FMT>(vraw[d].z, vraw[d].w) : codes8<FMT>(vraw[d].x, vraw[d].y);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = NP - 1; i >= 0; --i) o[mt][d] = mfma(vf, pf[mt][i], o[mt][d]);
+      }
+    }
+    if (more) load_v(tile + kWaves, pid_next);
+    pid = pid_next;
+    pid_next = page_of(tile + 2 * kWaves);
+  }
+
+  // ---- the nodes, 16 at a time, by the last part's waves in turn ----
+  if (p.kn && part == parts - 1 && 16 * w < nn) {
+    uint64_t set = 0;
+    if (p.parents) {
+      bool valid;
+      int depth;
+      ancestor_sets(p.parents + b * p.N, p.N, set, valid, depth);
+    } else {
+      set = ~0ull >> (63 - lane);
+    }
+    uint64_t sees[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = row0 + mt * 16 + col;
+      const int n = r < rows ? r / p.G : 0;
+      const uint64_t x = (static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(set >> 32), n, kWave))) << 32) |
+                         static_cast<uint32_t>(__shfl(static_cast<int>(set), n, kWave));
+      sees[mt] = r < rows ? x : 0;
+    }
+    for (int j0 = 16 * w; j0 < nn; j0 += 16 * kWaves) {
+      f32x4 s[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const long krow = (b * p.N + min(j0 + col, p.N - 1)) * p.kv_row + static_cast<long>(h) * D;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        bf16x8 kf[NP];
+        load8<DT>(p.kn, krow + chan<D>(f, g), kf);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int z = 2 * (NP - 1) > 2 ? 2 : 2 * (NP - 1); z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+              if (z - i >= 0 && z - i < NP) s[mt] = mfma(kf[z - i], qf[mt][f][i], s[mt]);
+      }
+      bf16x8 pf[MT][NP];
+      float keep[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool ok = (sees[mt] >> (j0 + 4 * g + r)) & 1;
+          s[mt][r] = ok ? s[mt][r] * kscale : -INFINITY;
+          x = fmaxf(x, s[mt][r]);
+        }
+        raise(mt, groups_max(x));
+        pf[mt][0] = bf16x8{};
+        if constexpr (NP == 3) pf[mt][1] = pf[mt][2] = bf16x8{};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool ok = (sees[mt] >> (j0 + 4 * g + r)) & 1;
+          const float e = ok ? ex2(s[mt][r] - m[mt]) : 0.f;
+          l[mt] += e;
+          keep[mt][r] = e;
+          __bf16 piece[3];
+          split<NP>(e, piece);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) pf[mt][i][r] = piece[i];
+        }
+      }
+      // values that are not finite must not meet a weight of 0: they stay out
+      // of the products and are added where they are seen
+      bool wild = false;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        bf16x8 vf[NP];
+        vf[0] = bf16x8{};
+        if constexpr (NP == 3) vf[1] = vf[2] = bf16x8{};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + 4 * g + r;
+          float x = load1<DT>(p.vn, (b * p.N + min(j, p.N - 1)) * p.kv_row + static_cast<long>(h) * D + 16 * d + col);
+          if (j >= nn) x = 0.f;
+          if (!isfinite(x)) {
+            wild = true;
+            x = 0.f;
+          }
+          __bf16 piece[3];
+          split<NP>(x, piece);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vf[i][r] = piece[i];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int z = NP == 3 ? 2 : 0; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+              if (z - i >= 0 && z - i < NP) o[mt][d] = mfma(vf[z - i], pf[mt][i], o[mt][d]);
+      }
+      if (__any(wild)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            if (j0 + k >= nn) continue;
+            const float e = __shfl(keep[mt][k % 4], col + 16 * (k / 4), kWave);
+            const bool ok = (sees[mt] >> (j0 + k)) & 1;
+            const long at = (b * p.N + j0 + k) * p.kv_row + static_cast<long>(h) * D + 4 * g;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float x = load1<DT>(p.vn, at + 16 * d + r);
+                if (ok && !isfinite(x)) o[mt][d][r] += e * x;
+              }
+          }
+      }
+    }
+  }
+
+  // ---- join the waves: 16 queries and at most 128 channels a round ----
+  __shared__ float sm[kWaves][MT * 16], sl[kWaves][MT * 16];
+  __shared__ float so[kWaves][16 * kJoinRow];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const float t = groups_sum(l[mt]);
+    if (g == 0) {
+      sm[w][mt * 16 + col] = m[mt];
+      sl[w][mt * 16 + col] = t;
+    }
+  }
+  __syncthreads();
+  constexpr int DC = D < kDc ? D : kDc;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float top = sm[0][mt * 16 + col];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, sm[i][mt * 16 + col]);
+    const float f = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top);
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += DC) {
+      if (mt || d0) __syncthreads();
+#pragma unroll
+      for (int d = 0; d < DC / 16; ++d)
+        *reinterpret_cast<f32x4*>(&so[w][col * kJoinRow + 16 * d + 4 * g]) = o[mt][d0 / 16 + d] * f;
+      __syncthreads();
+      for (int i = threadIdx.x; i < 16 * (DC / 4); i += kBlock) {
+        const int q = i / (DC / 4), d = i % (DC / 4) * 4;
+        const int r = row0 + mt * 16 + q;
+        if (r >= p.N * p.G) continue;
+        float mx = sm[0][mt * 16 + q], lt = 0.f;
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) mx = fmaxf(mx, sm[k][mt * 16 + q]);
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k)
+          lt += sm[k][mt * 16 + q] == -INFINITY ? sl[k][mt * 16 + q] : sl[k][mt * 16 + q] * ex2(sm[k][mt * 16 + q] - mx);
+        f32x4 acc = *reinterpret_cast<const f32x4*>(&so[0][q * kJoinRow + d]);
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) acc += *reinterpret_cast<const f32x4*>(&so[k][q * kJoinRow + d]);
+        const float y[4] = {acc[0], acc[1], acc[2], acc[3]};
+        const int n = r / p.G;
+        const long orow = (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
+        if (parts == 1) {
+          kv_finish<DT>(p, orow, d0 + d, y, mx, lt, r < rows);
+        } else {
+          const long at = orow * p.splits + part;
+          *reinterpret_cast<f32x4*>(p.part_o + at * D + d0 + d) = acc;
+          if (d0 + d == 0) p.part_ml[at] = make_float2(mx, lt);
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int FMT, int D, int MT>
+hipError_t launch_one(const KvAttn& p, hipStream_t st) {
+  const long outer = (static_cast<long>(p.B) * p.c.H * p.splits + 7) / 8 * 8;
+  hipLaunchKernelGGL((k_kv_attn<DT, FMT, D, MT>), dim3(static_cast<unsigned>(outer * p.mb)), dim3(kBlock), 0, st, p);
+  return hipGetLastError();
+}
+
+// The kernel for p.mt blocks of 16 queries (at most kv_max_mt).
+template <int DT, int FMT, int D>
+hipError_t launch_mt(const KvAttn& p, hipStream_t st) {
+  constexpr int most = kv_max_mt(DT, D);
+  if (p.mt == 1) return launch_one<DT, FMT, D, 1>(p, st);
+  if constexpr (most >= 2)
+    if (p.mt == 2) return launch_one<DT, FMT, D, 2>(p, st);
+  if constexpr (most >= 3)
+    if (p.mt == 3) return launch_one<DT, FMT, D, 3>(p, st);
+  if constexpr (most >= 4)
+    if (p.mt == 4) return launch_one<DT, FMT, D, 4>(p, st);
+  return hipErrorInvalidValue;
+}
+
+template <int D>
+hipError_t launch_dim(const KvAttn& p, int dtype, int fmt, hipStream_t st) {
+  if (dtype == SPECV_F32)
+    return fmt == SPECV_E4M3 ? launch_mt<SPECV_F32, SPECV_E4M3, D>(p, st) : launch_mt<SPECV_F32, SPECV_I8, D>(p, st);
+  return fmt == SPECV_E4M3 ? launch_mt<SPECV_BF16, SPECV_E4M3, D>(p, st) : launch_mt<SPECV_BF16, SPECV_I8, D>(p, st);
+}
+
+}  // namespace
+
+}  // namespace sv

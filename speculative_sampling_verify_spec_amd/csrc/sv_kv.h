@@ -56,13 +56,32 @@ struct KvAttn {
   int B, N, Hq, G;        // G = Hq / H query heads share a cached head
   void* out;              // [B][N][Hq][D]
   float* lse;             // [B][N][Hq] or null
+  // plan (kv_plan) and workspace
+  int mt, mb;             // blocks of 16 queries per workgroup, workgroups per (sequence, head, part)
+  int granule, splits;    // a part has at most `granule` tiles; no sequence has more than `splits` parts
+  float* part_o;          // [B][N][Hq][splits][D] sums of weight * value
+  float2* part_ml;        // [B][N][Hq][splits] (maximum, sum of weights), scores in log2
 };
+
+// Largest number of 16-query blocks a workgroup's registers hold.
+constexpr int kv_max_mt(int dtype, int D) {
+  return dtype == SPECV_F32 ? (D == 256 ? 1 : 2) : (D == 256 ? 2 : 4);
+}
+
+// Parts of a sequence of `ntile` tiles.
+__host__ __device__ inline int kv_parts(int ntile, int granule) {
+  return ntile <= granule ? 1 : (ntile + granule - 1) / granule;
+}
 
 // Launchers, next to their kernels.  dtype: SPECV_F32 or SPECV_BF16; fmt:
 // SPECV_E4M3 or SPECV_I8.
 hipError_t launch_kv_append(const KvAppend& p, int dtype, int fmt, hipStream_t s);
 hipError_t launch_kv_read(const KvRead& p, int dtype, int fmt, hipStream_t s);
 hipError_t launch_kv_attention(const KvAttn& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_attn_64(const KvAttn& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_attn_96(const KvAttn& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_attn_128(const KvAttn& p, int dtype, int fmt, hipStream_t s);
+hipError_t launch_kv_attn_256(const KvAttn& p, int dtype, int fmt, hipStream_t s);
 
 #ifdef __HIPCC__
 
@@ -130,6 +149,37 @@ __device__ inline int kv_page(const KvView& c, long b, long col) {
 // Cached tokens of sequence b: its length, clamped to what the table holds.
 __device__ inline int kv_len(const KvView& c, const int32_t* lengths, long b) {
   return min(max(lengths[b], 0), c.width << c.pshift);
+}
+
+// Four elements to a row; bf16 by round to nearest even (the type's own
+// rounding; what a cache holds under power-of-two scales is exact in bf16).
+template <int DT>
+__device__ inline void kv_store4(void* base, long i, const float* f) {
+  if constexpr (DT == SPECV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    bf16x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = static_cast<__bf16>(f[j]);
+    *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(base) + i) = v;
+  }
+}
+
+// Channels d .. d + 3 of an output row from its sums y of weight * value and
+// its softmax statistics; with channel 0 the row's lse.  A query that sees
+// nothing (l = 0) or does not exist gets 0 and -infinity.
+template <int DT>
+__device__ inline void kv_finish(const KvAttn& p, long row, int d, const float* y, float m, float l, bool exists) {
+  const bool some = exists && !(l == 0.f);
+  const float inv = 1.f / l;
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = some ? y[j] * inv : 0.f;
+  kv_store4<DT>(p.out, row * p.c.D + d, f);
+  if (d == 0 && p.lse)
+    p.lse[row] = some ? static_cast<float>(0.6931471805599453 * (static_cast<double>(m) + __builtin_amdgcn_logf(l)))
+                      : -INFINITY;
 }
 
 #endif  // __HIPCC__
