@@ -4,23 +4,14 @@ and workspaces with torch and passes device pointers plus torch's current
 stream of the tensors' device."""
 from __future__ import annotations
 
-import ctypes
-import math
+import struct
 from typing import Optional
 
-from ._lib import SpecVerifyError, _dtype_code, _ptr, load, strerror
+from ._lib import SPECV_BF16, SPECV_F32, SpecVerifyError, _ptr, load, strerror
 
 SPECV_E4M3, SPECV_I8 = 0, 1
 KV_PAGE_SIZES = (16, 32, 64, 128)
 KV_DIMS = (64, 96, 128, 256)
-
-
-class _Descriptor(ctypes.Structure):
-    """specv_kv_t."""
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
-                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("num_pages", ctypes.c_int),
-                ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
-                ("dim", ctypes.c_int), ("type", ctypes.c_int)]
 
 
 class KVCache:
@@ -31,7 +22,7 @@ class KVCache:
     k_scales and v_scales [num_pages, heads] float32, all contiguous on one
     device.  KVCache.empty() allocates them."""
 
-    __slots__ = ("k_pages", "v_pages", "k_scales", "v_scales")
+    __slots__ = ("_k", "_v", "_ks", "_vs", "_device", "_type")
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales):
         import torch
@@ -51,7 +42,9 @@ class KVCache:
         for t in (k_pages, v_pages, k_scales, v_scales):
             if t.device != k_pages.device or not t.is_contiguous():
                 raise ValueError("pages and scales must be contiguous tensors on the same device")
-        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self._k, self._v, self._ks, self._vs = k_pages, v_pages, k_scales, v_scales
+        self._device = k_pages.device
+        self._type = SPECV_I8 if k_pages.dtype == torch.int8 else SPECV_E4M3
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, heads: int, dim: int, dtype=None, device="cuda") -> "KVCache":
@@ -64,46 +57,68 @@ class KVCache:
                    torch.empty((num_pages, heads), dtype=torch.float32, device=device))
 
     @property
+    def k_pages(self):
+        return self._k
+
+    @property
+    def v_pages(self):
+        return self._v
+
+    @property
+    def k_scales(self):
+        return self._ks
+
+    @property
+    def v_scales(self):
+        return self._vs
+
+    @property
     def device(self):
-        return self.k_pages.device
+        return self._device
 
     @property
     def page_size(self) -> int:
-        return self.k_pages.shape[2]
+        return self._k.shape[2]
 
     @property
     def heads(self) -> int:
-        return self.k_pages.shape[1]
+        return self._k.shape[1]
 
     @property
     def dim(self) -> int:
-        return self.k_pages.shape[3]
+        return self._k.shape[3]
 
 
-def _descriptor(cache: KVCache, table_ptr: Optional[int], max_pages: int) -> _Descriptor:
+_pack = struct.Struct("@5P6i").pack  # specv_kv_t, read by the library during the call
+
+
+def _descriptor(cache: KVCache, table_ptr: int, max_pages: int) -> bytes:
+    n, h, p, d = cache._k.shape
+    return _pack(cache._k.data_ptr(), cache._v.data_ptr(), cache._ks.data_ptr(), cache._vs.data_ptr(), table_ptr, n, max_pages, p, h, d, cache._type)
+
+
+def _dtype_code(dtype) -> int:
     import torch
-    n, h, p, d = cache.k_pages.shape
-    return _Descriptor(cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), cache.k_scales.data_ptr(),
-                       cache.v_scales.data_ptr(), table_ptr, n, max_pages, p, h, d,
-                       SPECV_I8 if cache.k_pages.dtype == torch.int8 else SPECV_E4M3)
+    if dtype == torch.bfloat16:
+        return SPECV_BF16
+    if dtype == torch.float32:
+        return SPECV_F32
+    raise TypeError(f"queries, keys and values must be torch.bfloat16 or torch.float32, got {dtype}")
 
 
-def _check_table(cache: KVCache, page_table) -> int:
+def _check_table(cache: KVCache, page_table) -> None:
     import torch
-    if cache.device.type != "cuda":
+    if cache._device.type != "cuda":
         raise ValueError("the cache must be on a GPU")
-    if page_table.device != cache.device or page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != cache._device or \
             not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
-    return page_table.shape[0]
 
 
-def _check_ints(cache: KVCache, shape, **tensors) -> None:
+def _check_ints(cache: KVCache, shape, name: str, t) -> None:
     import torch
-    for name, t in tensors.items():
-        if t is not None and (t.device != cache.device or t.dtype != torch.int32 or tuple(t.shape) != shape or
-                              not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
+    if t.dtype != torch.int32 or t.shape != shape or t.device != cache._device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
 
 
 def _token_stride(name: str, t, heads: int, dim: int) -> int:
@@ -121,20 +136,20 @@ def _token_stride(name: str, t, heads: int, dim: int) -> int:
 
 
 def _check_rows(cache: KVCache, name: str, t, B: int, N: int, heads: int) -> int:
-    if t.device != cache.device or t.dim() != 4 or tuple(t.shape) != (B, N, heads, cache.dim):
+    if t.shape != (B, N, heads, cache._k.shape[3]) or t.device != cache._device:
         raise ValueError(f"{name} must be [{B}, {N}, {heads}, {cache.dim}] on the cache's device")
-    return _token_stride(name, t, heads, cache.dim)
+    return _token_stride(name, t, heads, t.shape[3])
 
 
 def _call(device, fn, *args) -> None:
     """One library call on the device's current stream (the last argument)."""
     import torch
     st = torch.cuda.current_stream(device).cuda_stream
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            rc = int(fn(*args, st))
+            rc = fn(*args, st)
     else:
-        rc = int(fn(*args, st))
+        rc = fn(*args, st)
     if rc != 0:
         raise SpecVerifyError(rc, strerror(rc))
 
@@ -150,22 +165,28 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
     Returns the tokens cached after the call, [B] int32 (out_lengths if given;
     lengths itself is left as it is, so every layer can pass it)."""
     import torch
-    B = _check_table(cache, page_table)
+    _check_table(cache, page_table)
+    B, width = page_table.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, N, heads, dim]")
-    N = k.shape[1]
-    row = _check_rows(cache, "k", k, B, N, cache.heads)
-    if _check_rows(cache, "v", v, B, N, cache.heads) != row or v.dtype != k.dtype:
+    N, heads = k.shape[1], cache._k.shape[1]
+    row = _check_rows(cache, "k", k, B, N, heads)
+    if _check_rows(cache, "v", v, B, N, heads) != row or v.dtype != k.dtype:
         raise ValueError("k and v must have the same dtype and strides")
-    _check_ints(cache, (B,), lengths=lengths, counts=counts, out_lengths=out_lengths)
-    _check_ints(cache, (B, N), index=index)
+    _check_ints(cache, (B,), "lengths", lengths)
+    if counts is not None:
+        _check_ints(cache, (B,), "counts", counts)
+    if index is not None:
+        _check_ints(cache, (B, N), "index", index)
     if out_lengths is None:
-        out_lengths = torch.empty((B,), dtype=torch.int32, device=cache.device)
-    elif out_lengths.data_ptr() == lengths.data_ptr():
-        raise ValueError("out_lengths must not be lengths itself")
-    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
-    _call(cache.device, load().spec_kv_append, ctypes.byref(kv), _ptr(k), _ptr(v), row, _ptr(lengths), _ptr(counts),
-          _ptr(index), B, N, _ptr(out_lengths), _dtype_code(k))
+        out_lengths = torch.empty_like(lengths)
+    else:
+        _check_ints(cache, (B,), "out_lengths", out_lengths)
+        if out_lengths.data_ptr() == lengths.data_ptr():
+            raise ValueError("out_lengths must not be lengths itself")
+    _call(cache._device, load().spec_kv_append, _descriptor(cache, page_table.data_ptr(), width), k.data_ptr(),
+          v.data_ptr(), row, lengths.data_ptr(), _ptr(counts), _ptr(index), B, N, out_lengths.data_ptr(),
+          _dtype_code(k.dtype))
     return out_lengths
 
 
@@ -175,23 +196,27 @@ def kv_read(cache: KVCache, page_table, lengths, T: int, *, starts=None, dtype=N
     v), each [B, T, heads, dim] in dtype (torch.bfloat16, the default, or
     torch.float32), 0 at and behind lengths[b]."""
     import torch
-    B = _check_table(cache, page_table)
-    _check_ints(cache, (B,), lengths=lengths, starts=starts)
+    _check_table(cache, page_table)
+    B, width = page_table.shape
+    if T < 1:
+        raise ValueError("T must be at least 1")
+    _check_ints(cache, (B,), "lengths", lengths)
+    if starts is not None:
+        _check_ints(cache, (B,), "starts", starts)
+    _, heads, _, dim = cache._k.shape
     dtype = torch.bfloat16 if dtype is None else dtype
-    k = torch.empty((B, T, cache.heads, cache.dim), dtype=dtype, device=cache.device)
+    code = _dtype_code(dtype)
+    k = torch.empty((B, T, heads, dim), dtype=dtype, device=cache._device)
     v = torch.empty_like(k)
-    code = _dtype_code(k)
-    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
-    _call(cache.device, load().spec_kv_read, ctypes.byref(kv), _ptr(starts), _ptr(lengths), B, T, _ptr(k), _ptr(v),
-          code)
+    _call(cache._device, load().spec_kv_read, _descriptor(cache, page_table.data_ptr(), width), _ptr(starts),
+          lengths.data_ptr(), B, T, k.data_ptr(), v.data_ptr(), code)
     return k, v
 
 
 def kv_attention_workspace_size(cache: KVCache, B: int, N: int, Hq: int, max_pages: int) -> int:
     """Workspace bytes of kv_attention for page tables of max_pages columns (0: invalid sizes)."""
     # the library reads the table's address only to see that there is one
-    kv = _descriptor(cache, 16, max_pages)
-    return int(load().spec_kv_attention_workspace_size(ctypes.byref(kv), B, N, Hq))
+    return int(load().spec_kv_attention_workspace_size(_descriptor(cache, 16, max_pages), B, N, Hq))
 
 
 def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None, *, parents=None, num_nodes=None,
@@ -205,36 +230,42 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
     each sequence, int32; scale defaults to dim ** -0.5.  Returns out [B, N,
     Hq, dim] and, when asked, lse [B, N, Hq] float32."""
     import torch
-    B = _check_table(cache, page_table)
+    _check_table(cache, page_table)
+    B, width = page_table.shape
     if q.dim() != 4:
         raise ValueError("q must be [B, N, Hq, dim]")
-    N, Hq = q.shape[1], q.shape[2]
+    _, N, Hq, dim = q.shape
     q_row = _check_rows(cache, "q", q, B, N, Hq)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     kv_row = 0
     if k_new is not None:
-        kv_row = _check_rows(cache, "k_new", k_new, B, N, cache.heads)
-        if _check_rows(cache, "v_new", v_new, B, N, cache.heads) != kv_row or k_new.dtype != q.dtype or \
+        heads = cache._k.shape[1]
+        kv_row = _check_rows(cache, "k_new", k_new, B, N, heads)
+        if _check_rows(cache, "v_new", v_new, B, N, heads) != kv_row or k_new.dtype != q.dtype or \
                 v_new.dtype != q.dtype:
             raise ValueError("k_new and v_new must have the same strides, and q's dtype")
     elif parents is not None:
         raise ValueError("parents needs k_new and v_new")
-    _check_ints(cache, (B,), lengths=lengths, num_nodes=num_nodes)
-    _check_ints(cache, (B, N), parents=parents)
-    code = _dtype_code(q)
-    kv = _descriptor(cache, _ptr(page_table), page_table.shape[1])
-    need = int(load().spec_kv_attention_workspace_size(ctypes.byref(kv), B, N, Hq))
+    _check_ints(cache, (B,), "lengths", lengths)
+    if num_nodes is not None:
+        _check_ints(cache, (B,), "num_nodes", num_nodes)
+    if parents is not None:
+        _check_ints(cache, (B, N), "parents", parents)
+    code = _dtype_code(q.dtype)
+    kv = _descriptor(cache, page_table.data_ptr(), width)
+    lib = load()
+    need = lib.spec_kv_attention_workspace_size(kv, B, N, Hq)
     if need == 0:
         raise SpecVerifyError(-2, strerror(-2))
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    elif workspace.device != cache.device:
-        raise ValueError("workspace must be on the cache's device")
-    out = torch.empty((B, N, Hq, cache.dim), dtype=q.dtype, device=cache.device)
-    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
-    _call(cache.device, load().spec_kv_attention, ctypes.byref(kv), _ptr(q), q_row, _ptr(k_new), _ptr(v_new), kv_row,
-          _ptr(lengths), _ptr(num_nodes), _ptr(parents),
-          1.0 / math.sqrt(cache.dim) if scale is None else float(scale), B, N, Hq, _ptr(out), _ptr(lse), code,
-          _ptr(workspace), workspace.numel() * workspace.element_size())
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=cache._device), need
+    elif workspace.device != cache._device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    out = torch.empty((B, N, Hq, dim), dtype=q.dtype, device=cache._device)
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache._device) if return_lse else None
+    _call(cache._device, lib.spec_kv_attention, kv, q.data_ptr(), q_row, _ptr(k_new), _ptr(v_new), kv_row,
+          lengths.data_ptr(), _ptr(num_nodes), _ptr(parents), dim ** -0.5 if scale is None else float(scale), B, N,
+          Hq, out.data_ptr(), _ptr(lse), code, workspace.data_ptr(), have)
     return (out, lse) if return_lse else out

@@ -5,6 +5,7 @@ Usage: python -m speculative_sampling_verify_spec_amd.build [-v]
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -24,7 +25,21 @@ ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-ffp-contract=fast",
          # packed fp32 instructions stay off: the compiler must not emit v_pk_*_f32
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         "-Rpass-analysis=kernel-resource-usage",  # read by _spills
          "-Wall", "-Wno-unused-result", "-I", INCLUDE, "-I", CSRC]
+
+
+def _spills(remarks: str) -> list:
+    """Kernels of a compilation that spill vector registers to memory.  The
+    compiler can reload a spilled register while lanes are still masked off, so
+    that they keep another value: no kernel here may spill."""
+    found, name = [], "?"
+    for m in re.finditer(r"remark: (?:.*?)(Function Name|VGPRs Spill): (\S+)", remarks):
+        if m[1] == "Function Name":
+            name = m[2]
+        elif int(m[2]):
+            found.append(f"{name}: {m[2]} VGPRs")
+    return found
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -35,6 +50,9 @@ def _compile(src: str, verbose: bool) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+    spills = _spills(r.stderr)
+    if spills:
+        raise RuntimeError(f"{src}: kernels spill registers:\n" + "\n".join(spills))
     noise = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
     if verbose and noise:
         print("\n".join(noise), file=sys.stderr)

@@ -12,25 +12,19 @@
 //
 // K pages are [P][D], V pages are [D][P]: the attention's second product
 // reads V along the tokens.
+//
+// Both kernels give one workgroup to the K or V of one block.  Its items are
+// 4 tokens x 16 bytes of a value row.  For K, neighbouring lanes take
+// neighbouring channels (whole rows on both sides); for V neighbouring lanes
+// take neighbouring tokens, so that the four codes of a channel, one word,
+// meet their neighbours in the transposed page and the rows are still touched
+// 64 bytes at a time: the transposition needs no LDS.
 #include "sv_device.h"
 #include "sv_kv.h"
 
 namespace sv {
 
 namespace {
-
-// Four elements of a row, at element i (a multiple of 4).
-template <int DT>
-__device__ inline void load4(const void* row, long i, float* f) {
-  if constexpr (DT == SPECV_F32) {
-    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + i);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + i);
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-}
 
 __device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
   v = wave_min_i32(v);
@@ -43,9 +37,23 @@ __device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
   return t;
 }
 
-// One workgroup per (page the call may touch, K or V of a head, sequence).
-template <int DT, int FMT>
+// Item i of a block: tokens 4 a .. 4 a + 3, vector v of the row.
+__device__ inline void item_of(const KvView& c, int isv, int i, int vpr, int& a, int& v) {
+  if (isv) {
+    a = i & (c.P / 4 - 1);
+    v = i >> (c.pshift - 2);
+  } else {
+    a = i / vpr;
+    v = i - a * vpr;
+  }
+}
+
+// One workgroup per (page the call may touch, K or V of a head, sequence);
+// NI items per thread, whose values stay in registers between the search for
+// the largest magnitude and the quantisation.
+template <int DT, int FMT, int NI>
 __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
+  constexpr int E = Elt<DT>::kPerVec;
   const KvView& c = p.c;
   const int slot = blockIdx.x, h = blockIdx.y >> 1, isv = blockIdx.y & 1;
   const long b = blockIdx.z;
@@ -84,57 +92,111 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
   const long blk = static_cast<long>(id) * c.H + h;
   float* sp = (isv ? c.vs : c.ks) + blk;
   const float s_old = *sp;
-  const void* src = isv ? p.v : p.k;
-  constexpr int eb = DT == SPECV_F32 ? 4 : 2;
-  auto row = [&](int t) -> const void* {  // token t of the page
-    const long i = p0 + t - len;
-    const long r = b * p.N + (p.index ? p.index[b * p.N + i] : i);
-    return static_cast<const char*>(src) + (r * p.row + static_cast<long>(h) * c.D) * eb;
-  };
-  const int nv = c.D / 4, work = (t1 - t0) * nv;
+  const char* src = static_cast<const char*>(isv ? p.v : p.k) + static_cast<long>(h) * c.D * Elt<DT>::kBytes;
+  const int vpr = c.D / E, items = (c.P / 4) * vpr;
+
+  uint4 raw[NI][4];
   float amax = 0.f;
-  for (int i = tid; i < work; i += kBlock) {
-    float f[4];
-    load4<DT>(row(t0 + i / nv), (i % nv) * 4, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) amax = fmaxf(amax, isfinite(f[j]) ? fabsf(f[j]) : 0.f);
+  for (int k = 0; k < NI; ++k) {
+    const int i = tid + k * kBlock;
+    int a, v;
+    item_of(c, isv, i, vpr, a, v);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * a + r;
+      raw[k][r] = make_uint4(0, 0, 0, 0);
+      if (i < items && t >= t0 && t < t1) {
+        const long at = p0 + t - len;
+        const long row = b * p.N + (p.index ? p.index[b * p.N + at] : at);
+        raw[k][r] = load16(src + row * p.row * Elt<DT>::kBytes, v);
+      }
+    }
   }
+#pragma unroll
+  for (int k = 0; k < NI; ++k)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float f[E];
+      Elt<DT>::unpack(raw[k][r], f);
+#pragma unroll
+      for (int j = 0; j < E; ++j) amax = fmaxf(amax, isfinite(f[j]) ? fabsf(f[j]) : 0.f);
+    }
   amax = block_max(amax, ldsf);
   float s = kv_scale<FMT>(amax);
   if (t0 > 0) s = fmaxf(s, s_old);
-  const float inv = 1.f / s;
+  const bool grow = t0 > 0 && s > s_old;  // the tokens that were there go to the grown scale
+  const float inv = 1.f / s, ratio = s_old * inv;
   uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
-  for (int i = tid; i < work; i += kBlock) {
-    const int t = t0 + i / nv, d = (i % nv) * 4;
-    float f[4];
-    load4<DT>(row(t), d, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] *= inv;
-    const uint32_t w = kv_encode4<FMT>(f);
-    if (!isv) {
-      *reinterpret_cast<uint32_t*>(page + static_cast<long>(t) * c.D + d) = w;
-    } else {
+  for (int k = 0; k < NI; ++k) {
+    const int i = tid + k * kBlock;
+    if (i >= items) break;
+    int a, v;
+    item_of(c, isv, i, vpr, a, v);
+    float f[4][E];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) page[static_cast<long>(d + j) * c.P + t] = static_cast<uint8_t>(w >> (8 * j));
+    for (int r = 0; r < 4; ++r) {
+      Elt<DT>::unpack(raw[k][r], f[r]);
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[r][j] *= inv;
     }
-  }
-  if (t0 > 0 && s > s_old) {  // the tokens that were there, to the grown scale
-    const float ratio = s_old * inv;
-    for (int i = tid; i < t0 * c.D; i += kBlock) {
-      const long at = isv ? static_cast<long>(i / t0) * c.P + i % t0 : i;
-      float f[4];
-      kv_decode4<FMT>(page[at], f);
-      f[0] *= ratio;
-      f[1] = f[2] = f[3] = 0.f;
-      page[at] = static_cast<uint8_t>(kv_encode4<FMT>(f));
+    if (!isv) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 4 * a + r;
+        uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(t) * c.D + v * E);
+        const bool fresh = t >= t0 && t < t1;
+        if (!fresh && !(grow && t < t0)) continue;
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) {
+          float g[4];
+          if (!fresh) {
+            kv_decode4<FMT>(at[j], g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] *= ratio;
+          }
+          w[j] = kv_encode4<FMT>(fresh ? &f[r][4 * j] : g);
+        }
+        if constexpr (E == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        else *at = w[0];
+      }
+    } else {
+      // byte masks of the word's new tokens and of those to round again; the
+      // other bytes of a word are kept
+      uint32_t fresh = 0, again = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 4 * a + r;
+        if (t >= t0 && t < t1) fresh |= 0xffu << (8 * r);
+        else if (grow && t < t0) again |= 0xffu << (8 * r);
+      }
+      if (!(fresh | again)) continue;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(v * E + j) * c.P + 4 * a);
+        const float x[4] = {f[0][j], f[1][j], f[2][j], f[3][j]};
+        uint32_t w = kv_encode4<FMT>(x);
+        if (fresh != ~0u) {
+          const uint32_t cur = *at;
+          float g[4];
+          kv_decode4<FMT>(cur, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] *= ratio;
+          w = (w & fresh) | (kv_encode4<FMT>(g) & again) | (cur & ~(fresh | again));
+        }
+        *at = w;
+      }
     }
   }
   if (tid == 0) *sp = s;
 }
 
 // One workgroup per (page the range may touch, K or V of a head, sequence).
-template <int DT, int FMT>
+template <int DT, int FMT, int NI>
 __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
+  constexpr int E = Elt<DT>::kPerVec;
   const KvView& c = p.c;
   const int slot = blockIdx.x, h = blockIdx.y >> 1, isv = blockIdx.y & 1;
   const long b = blockIdx.z;
@@ -143,61 +205,112 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   const int len = kv_len(c, p.lengths, b);
   const long start = p.starts ? max(p.starts[b], 0) : 0;
   const long p0 = ((start >> c.pshift) + slot) << c.pshift;
-  const long a = max(start, p0), z = min(start + p.T, p0 + c.P);  // positions this workgroup writes
-  if (z <= a) return;
+  // the page's tokens t0 .. t1 - 1 are written, those from `have` on as 0
+  const int t0 = static_cast<int>(max(start - p0, 0L));
+  const int t1 = static_cast<int>(min(start + p.T - p0, static_cast<long>(c.P)));
+  if (t1 <= t0) return;
   const int id = kv_page(c, b, p0 >> c.pshift);
+  const int have = id < 0 ? 0 : static_cast<int>(max(min(len - p0, static_cast<long>(c.P)), 0L));
   const long blk = static_cast<long>(max(id, 0)) * c.H + h;
-  const float s = id >= 0 ? (isv ? c.vs : c.ks)[blk] : 0.f;
+  const float s = (isv ? c.vs : c.ks)[blk];
   const uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
-  const int nv = c.D / 4;
-  const int work = static_cast<int>(z - a) * nv;
-  for (int i = threadIdx.x; i < work; i += kBlock) {
-    const long pos = a + i / nv;
-    const int t = static_cast<int>(pos - p0), d = (i % nv) * 4;
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (id >= 0 && pos < len) {
-      uint32_t w = 0;
-      if (!isv) {
-        w = *reinterpret_cast<const uint32_t*>(page + static_cast<long>(t) * c.D + d);
-      } else {
+  const int vpr = c.D / E, items = (c.P / 4) * vpr;
+  // row t's place in the output: token p0 + t - start
+  const long row0 = b * p.T + (p0 - start);
+
+  uint32_t raw[NI][E];  // K: words of 4 channels, [token][E / 4]; V: words of 4 tokens, [channel]
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(page[static_cast<long>(d + j) * c.P + t]) << (8 * j);
+  for (int k = 0; k < NI; ++k) {
+    const int i = static_cast<int>(threadIdx.x) + k * kBlock;
+    int a, v;
+    item_of(c, isv, i < items ? i : 0, vpr, a, v);
+    if (!isv) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(page + static_cast<long>(4 * a + r) * c.D + v * E);
+        if constexpr (E == 8) {
+          const uint2 w = *reinterpret_cast<const uint2*>(at);
+          raw[k][2 * r] = w.x;
+          raw[k][2 * r + 1] = w.y;
+        } else {
+          raw[k][r] = *at;
+        }
       }
-      kv_decode4<FMT>(w, f);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] *= s;
+      for (int j = 0; j < E; ++j)
+        raw[k][j] = *reinterpret_cast<const uint32_t*>(page + static_cast<long>(v * E + j) * c.P + 4 * a);
     }
-    kv_store4<DT>(out, ((b * p.T + (pos - start)) * c.H + h) * c.D + d, f);
   }
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    const int i = static_cast<int>(threadIdx.x) + k * kBlock;
+    if (i >= items) break;
+    int a, v;
+    item_of(c, isv, i, vpr, a, v);
+    float f[4][E];
+    if (!isv) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) kv_decode4<FMT>(raw[k][r * (E / 4) + j], &f[r][4 * j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        float g[4];
+        kv_decode4<FMT>(raw[k][j], g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[r][j] = g[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * a + r;
+      if (t < t0 || t >= t1) continue;
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[r][j] = t < have ? f[r][j] * s : 0.f;
+      kv_store16<DT>(out, ((row0 + t) * c.H + h) * c.D + v * E, f[r]);
+    }
+  }
+}
+
+// Pages that n consecutive tokens can touch, whatever position they start at.
+unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P + 1); }
+
+template <int DT, int FMT>
+hipError_t append(const KvAppend& p, hipStream_t st) {
+  const dim3 grid(kv_slots(p.N, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
+  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);  // at most 8 kBlock
+  if (items <= kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 1>), grid, block, 0, st, p);
+  else if (items <= 2 * kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 2>), grid, block, 0, st, p);
+  else if (items <= 4 * kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 4>), grid, block, 0, st, p);
+  else if constexpr (DT == SPECV_F32) hipLaunchKernelGGL((k_kv_append<DT, FMT, 8>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+template <int DT, int FMT>
+hipError_t read(const KvRead& p, hipStream_t st) {
+  const dim3 grid(kv_slots(p.T, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
+  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);
+  if (items <= kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 1>), grid, block, 0, st, p);
+  else if (items <= 2 * kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 2>), grid, block, 0, st, p);
+  else if (items <= 4 * kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 4>), grid, block, 0, st, p);
+  else if constexpr (DT == SPECV_F32) hipLaunchKernelGGL((k_kv_read<DT, FMT, 8>), grid, block, 0, st, p);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-// Pages that n consecutive tokens can touch, whatever position they start at.
-static unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P + 1); }
-
 hipError_t launch_kv_append(const KvAppend& p, int dtype, int fmt, hipStream_t st) {
-  const dim3 grid(kv_slots(p.N, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
-  if (dtype == SPECV_F32) {
-    if (fmt == SPECV_E4M3) hipLaunchKernelGGL((k_kv_append<SPECV_F32, SPECV_E4M3>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_append<SPECV_F32, SPECV_I8>), grid, block, 0, st, p);
-  } else {
-    if (fmt == SPECV_E4M3) hipLaunchKernelGGL((k_kv_append<SPECV_BF16, SPECV_E4M3>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_append<SPECV_BF16, SPECV_I8>), grid, block, 0, st, p);
-  }
-  return hipGetLastError();
+  if (dtype == SPECV_F32)
+    return fmt == SPECV_E4M3 ? append<SPECV_F32, SPECV_E4M3>(p, st) : append<SPECV_F32, SPECV_I8>(p, st);
+  return fmt == SPECV_E4M3 ? append<SPECV_BF16, SPECV_E4M3>(p, st) : append<SPECV_BF16, SPECV_I8>(p, st);
 }
 
 hipError_t launch_kv_read(const KvRead& p, int dtype, int fmt, hipStream_t st) {
-  const dim3 grid(kv_slots(p.T, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
-  if (dtype == SPECV_F32) {
-    if (fmt == SPECV_E4M3) hipLaunchKernelGGL((k_kv_read<SPECV_F32, SPECV_E4M3>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<SPECV_F32, SPECV_I8>), grid, block, 0, st, p);
-  } else {
-    if (fmt == SPECV_E4M3) hipLaunchKernelGGL((k_kv_read<SPECV_BF16, SPECV_E4M3>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((k_kv_read<SPECV_BF16, SPECV_I8>), grid, block, 0, st, p);
-  }
-  return hipGetLastError();
+  if (dtype == SPECV_F32)
+    return fmt == SPECV_E4M3 ? read<SPECV_F32, SPECV_E4M3>(p, st) : read<SPECV_F32, SPECV_I8>(p, st);
+  return fmt == SPECV_E4M3 ? read<SPECV_BF16, SPECV_E4M3>(p, st) : read<SPECV_BF16, SPECV_I8>(p, st);
 }
 
 }  // namespace sv

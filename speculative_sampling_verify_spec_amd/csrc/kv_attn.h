@@ -28,6 +28,8 @@
 // instructions, products of two split operands the six largest of nine.
 #pragma once
 
+#include <cfloat>
+
 #include "sv_device.h"
 #include "sv_kv.h"
 
@@ -148,10 +150,22 @@ constexpr int kTile = 64;                       // cached tokens a wave takes at
 constexpr int kDc = 128;                        // channels per round of the final join
 constexpr int kJoinRow = kDc + 4;               // its padded row in LDS
 
+// The queries' fragments stay in registers if they take fewer than 16.
+constexpr bool q_in_lds(int dt, int D, int MT) { return MT * (dt == SPECV_F32 ? 3 : 1) * D / 8 >= 16; }
+
+// Waves a SIMD should hold, which bounds the registers of each to 512 /
+// waves: the most that fit without spilling (the build refuses spills).
+constexpr int waves_per(int dt, int D, int MT) {
+  if (D == 256) return 1;
+  if (MT == 1) return D == 64 ? 4 : 3;
+  if (MT == 2) return D == 64 && dt == SPECV_BF16 ? 3 : 2;
+  return MT == 3 || D == 64 ? 2 : 1;
+}
+
 // One workgroup: MT x 16 queries of one (sequence, cached head) over one of
 // the parts of the sequence's tokens; its waves take the part's tiles in turn.
 template <int DT, int FMT, int D, int MT>
-__global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
+__global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn p) {
   constexpr int NP = kPieces<DT>, NF = D / 32, ND = D / 16, NC = D / 64;
   const KvView& c = p.c;
   // workgroups of one part and head that differ only in their queries read
@@ -174,29 +188,39 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
   const int rows = nn * p.G;           // queries that exist
   const int row0 = mblk * MT * 16;
 
+  // one buffer in LDS: the queries' fragments during the loop (where they
+  // would take too many registers), the waves' sums at the join
+  constexpr bool QL = q_in_lds(DT, D, MT);
+  constexpr int kJoinBytes = kWaves * 16 * kJoinRow * 4, kQBytes = QL ? MT * NF * NP * kWave * 16 : 0;
+  __shared__ __align__(16) char lds[kJoinBytes > kQBytes ? kJoinBytes : kQBytes];
+  bf16x8* const lq = reinterpret_cast<bf16x8*>(lds);
+
   // ---- queries: B operands, negated where the scale is (kept >= 0) ----
   const float kscale = fabsf(p.scale) * kLog2e;
-  bf16x8 qf[MT][NF][NP];
+  bf16x8 qreg[QL ? 1 : MT][QL ? 1 : NF][NP];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = row0 + mt * 16 + col;
-    if (r < rows) {
-      const int n = r / p.G;
-      const long base = (b * p.N + n) * p.q_row + static_cast<long>(h * p.G + (r - n * p.G)) * D;
+    const int n = min(r / p.G, p.N - 1);  // a row that exists; what others give is not written
+    const long base = (b * p.N + n) * p.q_row + static_cast<long>(h * p.G + (r < rows ? r - n * p.G : 0)) * D;
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        load8<DT>(p.q, base + chan<D>(f, g), qf[mt][f]);
-        if (p.scale < 0.f)
+    for (int f = 0; f < NF; ++f) {
+      if (QL && f % kWaves != w) continue;
+      bf16x8 x[NP];
+      load8<DT>(p.q, base + chan<D>(f, g), x);
 #pragma unroll
-          for (int i = 0; i < NP; ++i) qf[mt][f][i] = -qf[mt][f][i];
+      for (int i = 0; i < NP; ++i) {
+        if (p.scale < 0.f) x[i] = -x[i];
+        if constexpr (QL) lq[((mt * NF + f) * NP + i) * kWave + lane] = x[i];
+        else qreg[mt][f][i] = x[i];
       }
-    } else {
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int i = 0; i < NP; ++i) qf[mt][f][i] = bf16x8{};
     }
   }
+  if constexpr (QL) __syncthreads();
+  auto query = [&](int mt, int f, int i) -> bf16x8 {
+    if constexpr (QL) return lq[((mt * NF + f) * NP + i) * kWave + lane];
+    else return qreg[mt][f][i];
+  };
 
   f32x4 o[MT][ND];
   float m[MT], l[MT];
@@ -223,7 +247,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
   // ---- cached tokens ----
   const int tile0 = static_cast<int>(static_cast<long>(ntile) * part / parts);
   const int tile1 = static_cast<int>(static_cast<long>(ntile) * (part + 1) / parts);
-  uint4 kraw[4][NC > 0 ? NC : 1], vraw[ND];
+  uint4 kraw[4][NC], vraw[ND];
   uint2 ktail[4];
   const size_t blkbytes = static_cast<size_t>(c.P) * D;
   // page of this lane's 16 tokens (group g) of a tile, -1: none
@@ -231,17 +255,17 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
     const unsigned tok = static_cast<unsigned>(tile) * kTile + 16 * g;
     return kv_page(c, b, tok >> c.pshift);
   };
-  auto load_k = [&](int tile, int pid) {
+  // this lane's row of K: token 16 (col / 4) + col % 4 of a tile
+  auto k_rows = [&](int tile, int pid) -> const uint8_t* {
     const int grp = col >> 2;
     const int id = max(__shfl(pid, grp * 16, kWave), 0);
     const int off = ((tile % 2 * kTile + 16 * grp) & (c.P - 1)) + (col & 3);  // pages of at most two tiles
-    const uint8_t* a = c.kp + (static_cast<size_t>(id) * c.H + h) * blkbytes + static_cast<size_t>(off) * D;
+    return c.kp + (static_cast<size_t>(id) * c.H + h) * blkbytes + static_cast<size_t>(off) * D;
+  };
+  auto load_k = [&](const uint8_t* a, int t) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) kraw[t][i] = *reinterpret_cast<const uint4*>(a + 4 * t * D + 64 * i + 16 * g);
-      if constexpr (NF % 2) ktail[t] = *reinterpret_cast<const uint2*>(a + 4 * t * D + 64 * NC + 8 * g);
-    }
+    for (int i = 0; i < NC; ++i) kraw[t][i] = *reinterpret_cast<const uint4*>(a + 4 * t * D + 64 * i + 16 * g);
+    if constexpr (NF % 2) ktail[t] = *reinterpret_cast<const uint2*>(a + 4 * t * D + 64 * NC + 8 * g);
   };
   float ks = 0.f, vs = 0.f;
   auto load_v = [&](int tile, int pid) {
@@ -257,29 +281,13 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
   if (tile < tile1) {
     pid = page_of(tile);
     pid_next = page_of(tile + kWaves);
-    load_k(tile, pid);
+    const uint8_t* a = k_rows(tile, pid);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) load_k(a, t);
     load_v(tile, pid);
   }
   for (; tile < tile1; tile += kWaves) {
-    f32x4 s[MT][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) s[mt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const bf16x8 kf = f < 2 * NC ? (f % 2 ? codes8<FMT>(kraw[t][f / 2].z, kraw[t][f / 2].w)
-                                              : codes8<FMT>(kraw[t][f / 2].x, kraw[t][f / 2].y))
-                                     : codes8<FMT>(ktail[t].x, ktail[t].y);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = NP - 1; i >= 0; --i) s[mt][t] = mfma(kf, qf[mt][f][i], s[mt][t]);
-      }
     const bool more = tile + kWaves < tile1;
-    if (more) load_k(tile + kWaves, pid_next);
     // tokens of this lane's 16 that exist; the bytes behind them, and scales
     // of no page, may be anything (NaN too) and are cleared
     const int have = pid < 0 ? 0 : min(max(len - tile * kTile - 16 * g, 0), 16);
@@ -297,45 +305,62 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
       }
     }
     const float kc = ks * kscale;
+    const uint8_t* next_k = more ? k_rows(tile + kWaves, pid_next) : nullptr;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float x = -INFINITY;
+    for (int j = 0; j < 2; ++j) {  // halves of the tile: 8 of each lane's 16 tokens
+      // the queries' fragments are read from LDS here, not kept across the loop
+      if constexpr (QL) asm volatile("" ::: "memory");
+      f32x4 s[MT][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int mt = 0; mt < MT; ++mt) s[mt][0] = s[mt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float y = s[mt][t][r] * kc;
-          if (!whole && 4 * t + r >= have) y = -INFINITY;
-          s[mt][t][r] = y;
-          x = fmaxf(x, y);
+      for (int f = 0; f < NF; ++f) {
+        bf16x8 kf[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint4 x = kraw[2 * j + t][f / 2 < NC ? f / 2 : 0];
+          kf[t] = f >= 2 * NC ? codes8<FMT>(ktail[2 * j + t].x, ktail[2 * j + t].y)
+                  : f % 2     ? codes8<FMT>(x.z, x.w)
+                              : codes8<FMT>(x.x, x.y);
         }
-      raise(mt, groups_max(x));
-      float sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float e = ex2(s[mt][t][r] - m[mt]);
-          if (!whole && 4 * t + r >= have) e = 0.f;  // also where the maximum is still -inf
-          sum += e;
-          s[mt][t][r] = e * vs;
-        }
-      l[mt] += sum;
-    }
-    // weights as B operands: bf16 (half a step of 2^-8 relative, as the
-    // output's own type has), or their three pieces
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
+          for (int i = NP - 1; i >= 0; --i) {
+            const bf16x8 q = query(mt, f, i);
+            s[mt][0] = mfma(kf[0], q, s[mt][0]);
+            s[mt][1] = mfma(kf[1], q, s[mt][1]);
+          }
+      }
+      // weights as the B operand: bf16 (half a step of 2^-8 relative, as the
+      // output's own type has), or their three pieces
       bf16x8 pf[MT][NP];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) {
+        float x = -FLT_MAX;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
+          if (!whole && 8 * j + e >= have) s[mt][e / 4][e % 4] = -FLT_MAX;
+          x = fmaxf(x, s[mt][e / 4][e % 4]);
+        }
+        raise(mt, groups_max(x * kc));
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float y = ex2(fmaf(s[mt][e / 4][e % 4], kc, -m[mt]));
+          if (!whole && 8 * j + e >= have) y = 0.f;  // also where the maximum is still -inf
+          sum += y;
           __bf16 piece[3];
-          split<NP>(s[mt][2 * j + e / 4][e % 4], piece);
+          split<NP>(y * vs, piece);
 #pragma unroll
           for (int i = 0; i < NP; ++i) pf[mt][i][e] = piece[i];
         }
+        l[mt] += sum;
+      }
+      if (more) {
+        load_k(next_k, 2 * j);
+        load_k(next_k, 2 * j + 1);
+      }
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         const bf16x8 vf = j ? codes8<FMT>(vraw[d].z, vraw[d].w) : codes8<FMT>(vraw[d].x, vraw[d].y);
@@ -384,7 +409,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
           for (int z = 2 * (NP - 1) > 2 ? 2 : 2 * (NP - 1); z >= 0; --z)
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-              if (z - i >= 0 && z - i < NP) s[mt] = mfma(kf[z - i], qf[mt][f][i], s[mt]);
+              if (z - i >= 0 && z - i < NP) s[mt] = mfma(kf[z - i], query(mt, f, i), s[mt]);
       }
       bf16x8 pf[MT][NP];
       float keep[MT][4];
@@ -417,6 +442,8 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
       bool wild = false;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
+        // few loads at a time: this part's registers count for the whole kernel's occupancy
+        if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
         bf16x8 vf[NP];
         vf[0] = bf16x8{};
         if constexpr (NP == 3) vf[1] = vf[2] = bf16x8{};
@@ -443,29 +470,37 @@ __global__ __launch_bounds__(kBlock) void k_kv_attn(KvAttn p) {
               if (z - i >= 0 && z - i < NP) o[mt][d] = mfma(vf[z - i], pf[mt][i], o[mt][d]);
       }
       if (__any(wild)) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {  // nodes j0 + 4 k + i: lane group k holds their weights
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 4 * k + i;
+            const long at = (b * p.N + min(j, p.N - 1)) * p.kv_row + static_cast<long>(h) * D + 4 * g;
+            float e[MT];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            if (j0 + k >= nn) continue;
-            const float e = __shfl(keep[mt][k % 4], col + 16 * (k / 4), kWave);
-            const bool ok = (sees[mt] >> (j0 + k)) & 1;
-            const long at = (b * p.N + j0 + k) * p.kv_row + static_cast<long>(h) * D + 4 * g;
+            for (int mt = 0; mt < MT; ++mt) {
+              const float t = __shfl(keep[mt][i], col + 16 * k, kWave);
+              e[mt] = j < nn && ((sees[mt] >> (j & 63)) & 1) ? t : 0.f;
+            }
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
+                if (r == 0) __builtin_amdgcn_sched_barrier(0);
                 const float x = load1<DT>(p.vn, at + 16 * d + r);
-                if (ok && !isfinite(x)) o[mt][d][r] += e * x;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  if (!isfinite(x) && ((sees[mt] >> (j & 63)) & 1) && j < nn) o[mt][d][r] += e[mt] * x;
               }
           }
+        }
       }
     }
   }
 
   // ---- join the waves: 16 queries and at most 128 channels a round ----
   __shared__ float sm[kWaves][MT * 16], sl[kWaves][MT * 16];
-  __shared__ float so[kWaves][16 * kJoinRow];
+  float(*const so)[16 * kJoinRow] = reinterpret_cast<float(*)[16 * kJoinRow]>(lds);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const float t = groups_sum(l[mt]);

@@ -166,6 +166,20 @@ __device__ inline void kv_store4(void* base, long i, const float* f) {
   }
 }
 
+// A row's 16 bytes, as kv_store4.
+template <int DT>
+__device__ inline void kv_store16(void* base, long i, const float* f) {
+  if constexpr (DT == SPECV_F32) {
+    kv_store4<DT>(base, i, f);
+  } else {
+    typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+    bf16x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = static_cast<__bf16>(f[j]);
+    *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(base) + i) = v;
+  }
+}
+
 // Channels d .. d + 3 of an output row from its sums y of weight * value and
 // its softmax statistics; with channel 0 the row's lse.  A query that sees
 // nothing (l = 0) or does not exist gets 0 and -infinity.

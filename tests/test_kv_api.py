@@ -24,11 +24,17 @@ def lib():
     return sv.load()
 
 
+class Kv(ctypes.Structure):
+    """specv_kv_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scales", "v_scales", "page_table")] + \
+               [(n, ctypes.c_int) for n in ("num_pages", "max_pages", "page_size", "heads", "dim", "type")]
+
+
 def kv(**kw):
     a = dict(k_pages=BASE, v_pages=2 * BASE, k_scales=3 * BASE, v_scales=4 * BASE, page_table=5 * BASE, num_pages=100,
              max_pages=10, page_size=64, heads=8, dim=128, type=sv.SPECV_E4M3)
     a.update(kw)
-    return _kv._Descriptor(**a)
+    return Kv(**a)
 
 
 BAD_CACHE = [(dict(k_pages=None), -1), (dict(v_pages=None), -1), (dict(k_scales=None), -1), (dict(v_scales=None), -1),
@@ -123,6 +129,13 @@ def test_workspace_sizes(lib):
 def _parts(pages=4, h=2, p=16, d=64, dtype=torch.int8):
     return [torch.zeros(pages, h, p, d, dtype=dtype), torch.zeros(pages, h, d, p, dtype=dtype),
             torch.zeros(pages, h), torch.zeros(pages, h)]
+
+
+def test_descriptor_is_the_headers_struct():
+    c = sv.KVCache(*_parts())
+    want = Kv(c.k_pages.data_ptr(), c.v_pages.data_ptr(), c.k_scales.data_ptr(), c.v_scales.data_ptr(), 4096, 4, 9, 16,
+              2, 64, sv.SPECV_I8)
+    assert _kv._descriptor(c, 4096, 9) == bytes(want)
 
 
 def test_cache_checks():
