@@ -153,13 +153,16 @@ constexpr int kJoinRow = kDc + 4;               // its padded row in LDS
 // The queries' fragments stay in registers if they take fewer than 16.
 constexpr bool q_in_lds(int dt, int D, int MT) { return MT * (dt == SPECV_F32 ? 3 : 1) * D / 8 >= 16; }
 
+// Whether K is kept half a tile ahead instead of a whole one.
+constexpr bool k_half(int D, int MT) { return D == 256 || MT == 4; }
+
 // Waves a SIMD should hold, which bounds the registers of each to 512 /
 // waves: the most that fit without spilling (the build refuses spills).
 constexpr int waves_per(int dt, int D, int MT) {
-  if (D == 256) return 1;
+  if (D == 256) return 2;
   if (MT == 1) return D == 64 ? 4 : 3;
   if (MT == 2) return D == 64 && dt == SPECV_BF16 ? 3 : 2;
-  return MT == 3 || D == 64 ? 2 : 1;
+  return 2;
 }
 
 // One workgroup: MT x 16 queries of one (sequence, cached head) over one of
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
   const int ntile = (len >> 6) + ((len & 63) != 0);
   const int parts = kv_parts(ntile, p.granule);
   if (part >= parts) return;
-  const int lane = threadIdx.x % kWave, w = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int col = lane % 16, g = lane / 16;
   const int nn = p.nodes ? min(max(p.nodes[b], 0), p.N) : p.N;
   const int rows = nn * p.G;           // queries that exist
@@ -247,8 +250,10 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
   // ---- cached tokens ----
   const int tile0 = static_cast<int>(static_cast<long>(ntile) * part / parts);
   const int tile1 = static_cast<int>(static_cast<long>(ntile) * (part + 1) / parts);
-  uint4 kraw[4][NC], vraw[ND];
-  uint2 ktail[4];
+  // K is kept a tile ahead, or half a tile where registers are short
+  constexpr int KB = k_half(D, MT) ? 2 : 4;
+  uint4 kraw[KB][NC], vraw[ND];
+  uint2 ktail[KB];
   const size_t blkbytes = static_cast<size_t>(c.P) * D;
   // page of this lane's 16 tokens (group g) of a tile, -1: none
   auto page_of = [&](int tile) {
@@ -264,26 +269,31 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
   };
   auto load_k = [&](const uint8_t* a, int t) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) kraw[t][i] = *reinterpret_cast<const uint4*>(a + 4 * t * D + 64 * i + 16 * g);
-    if constexpr (NF % 2) ktail[t] = *reinterpret_cast<const uint2*>(a + 4 * t * D + 64 * NC + 8 * g);
+    for (int i = 0; i < NC; ++i) kraw[t % KB][i] = *reinterpret_cast<const uint4*>(a + 4 * t * D + 64 * i + 16 * g);
+    if constexpr (NF % 2) ktail[t % KB] = *reinterpret_cast<const uint2*>(a + 4 * t * D + 64 * NC + 8 * g);
   };
   float ks = 0.f, vs = 0.f;
   auto load_v = [&](int tile, int pid) {
     const size_t blk = static_cast<size_t>(max(pid, 0)) * c.H + h;
     const uint8_t* a = c.vp + blk * blkbytes + static_cast<size_t>(col) * c.P + ((tile % 2 * kTile + 16 * g) & (c.P - 1));
 #pragma unroll
-    for (int d = 0; d < ND; ++d) vraw[d] = *reinterpret_cast<const uint4*>(a + static_cast<size_t>(16 * d) * c.P);
+    for (int d = 0; d < ND; ++d) {
+      // four addresses at a time: all of them at once would cost registers at the loop's fullest point
+      if (d % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+      vraw[d] = *reinterpret_cast<const uint4*>(a + static_cast<size_t>(16 * d) * c.P);
+    }
     ks = c.ks[blk];
     vs = c.vs[blk];
   };
   int tile = tile0 + w;
   int pid = -1, pid_next = -1;
+  const uint8_t* this_k = nullptr;
   if (tile < tile1) {
     pid = page_of(tile);
     pid_next = page_of(tile + kWaves);
-    const uint8_t* a = k_rows(tile, pid);
+    this_k = k_rows(tile, pid);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) load_k(a, t);
+    for (int t = 0; t < KB; ++t) load_k(this_k, t);
     load_v(tile, pid);
   }
   for (; tile < tile1; tile += kWaves) {
@@ -318,8 +328,8 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
         bf16x8 kf[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint4 x = kraw[2 * j + t][f / 2 < NC ? f / 2 : 0];
-          kf[t] = f >= 2 * NC ? codes8<FMT>(ktail[2 * j + t].x, ktail[2 * j + t].y)
+          const uint4 x = kraw[(2 * j + t) % KB][f / 2 < NC ? f / 2 : 0];
+          kf[t] = f >= 2 * NC ? codes8<FMT>(ktail[(2 * j + t) % KB].x, ktail[(2 * j + t) % KB].y)
                   : f % 2     ? codes8<FMT>(x.z, x.w)
                               : codes8<FMT>(x.x, x.y);
         }
@@ -357,9 +367,12 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
         }
         l[mt] += sum;
       }
-      if (more) {
-        load_k(next_k, 2 * j);
-        load_k(next_k, 2 * j + 1);
+      if (KB == 2 && j == 0) {
+        load_k(this_k, 2);
+        load_k(this_k, 3);
+      } else if (more) {
+        load_k(next_k, KB == 2 ? 0 : 2 * j);
+        load_k(next_k, KB == 2 ? 1 : 2 * j + 1);
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
@@ -371,6 +384,7 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
       }
     }
     if (more) load_v(tile + kWaves, pid_next);
+    this_k = next_k;
     pid = pid_next;
     pid_next = page_of(tile + 2 * kWaves);
   }

@@ -65,7 +65,8 @@ struct KvAttn {
 
 // Largest number of 16-query blocks a workgroup's registers hold.
 constexpr int kv_max_mt(int dtype, int D) {
-  return dtype == SPECV_F32 ? (D == 256 ? 1 : 2) : (D == 256 ? 2 : 4);
+  if (D == 256) return 1;
+  return dtype == SPECV_F32 ? 2 : D == 128 ? 3 : 4;
 }
 
 // Parts of a sequence of `ntile` tiles.
