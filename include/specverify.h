@@ -403,6 +403,7 @@ typedef struct {
 } specv_kv_t;      /* read on the host during the call; the arrays are device memory */
 
 #define SPECV_KV_MAX_APPEND (1 << 24)  /* tokens per sequence one spec_kv_append or spec_kv_read takes */
+#define SPECV_KV_MAX_GROUP  1024       /* query heads per cached head */
 
 /*
  * spec_kv_append - quantise tokens and write them behind each sequence's
@@ -469,7 +470,8 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   parents     [B][N] int32 (device) or NULL: a chain; read when k_new is given
  *   scale       finite
  *   out         [B][N][Hq][dim] (dtype);  out_lse [B][N][Hq] float or NULL
- *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq a multiple of heads
+ *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq a multiple of heads, at
+ *               most SPECV_KV_MAX_GROUP times as many
  *   q, k_new, v_new and out 16-byte aligned
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
  * Sums and softmax statistics are in 32 bits.  The same call gives the same

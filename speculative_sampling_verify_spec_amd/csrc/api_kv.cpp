@@ -60,7 +60,7 @@ struct KvPlan {
   int mt, mb, granule, splits;
 };
 
-constexpr long kTargetGroups = 2048;  // workgroups to aim at: 256 CUs, a few resident each, a few times over
+constexpr long kTargetGroups = 512;   // workgroups to aim at: two on each of 256 CUs
 constexpr int kMinGranule = 4;        // tiles per part, at least one for each wave
 
 KvPlan kv_plan(const KvView& c, int B, int N, int Hq, int dtype) {
@@ -77,7 +77,8 @@ KvPlan kv_plan(const KvView& c, int B, int N, int Hq, int dtype) {
 }
 
 bool valid_attention(const KvView& c, int B, int N, int Hq) {
-  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % c.H) return false;
+  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % c.H || Hq / c.H > SPECV_KV_MAX_GROUP)
+    return false;
   for (int dt : {SPECV_F32, SPECV_BF16}) {  // a grid's workgroups times their threads stay below 2^32
     const KvPlan pl = kv_plan(c, B, N, Hq, dt);
     if ((static_cast<long>(B) * c.H * pl.splits + 7) * pl.mb * 256 >= (1L << 32)) return false;
@@ -181,6 +182,7 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
   p.N = N;
   p.Hq = Hq;
   p.G = Hq / p.c.H;
+  p.inv_g = 1.f / static_cast<float>(p.G);
   p.out = out;
   p.lse = out_lse;
   const KvPlan pl = kv_plan(p.c, B, N, Hq, dtype);

@@ -6,15 +6,20 @@ namespace sv {
 
 namespace {
 
-// D / 4 threads per output row: the parts' sums, each scaled to the largest
-// maximum, in the parts' order.  Rows of sequences in one part are already
-// written.
-template <int DT>
+// An output row's parts, each scaled to the largest maximum, summed by GR
+// groups of D / 4 threads: group i takes parts i, i + GR, ...; the groups'
+// sums meet in LDS in their order, so the same call gives the same bits.
+// WIDE: a workgroup per row, GR = 1024 / D; else GR = 1 and several rows per
+// workgroup, for few parts.  Rows of sequences in one part are already written.
+template <int DT, bool WIDE>
 __global__ __launch_bounds__(kBlock) void k_kv_join(KvAttn p) {
-  const int tpr = p.c.D / 4, rows_per = kBlock / tpr;
-  const int sub = threadIdx.x / tpr, d = threadIdx.x % tpr * 4;
-  const long row = static_cast<long>(blockIdx.x) * rows_per + sub;
-  if (sub >= rows_per || row >= static_cast<long>(p.B) * p.N * p.Hq) return;
+  __shared__ float4 sy[kBlock];
+  __shared__ float sl[kBlock];
+  const int tpr = p.c.D / 4, groups = kBlock / tpr;  // 16, 10, 8 or 4
+  const int grp = threadIdx.x / tpr, d = threadIdx.x % tpr * 4;
+  const long row = WIDE ? blockIdx.x : static_cast<long>(blockIdx.x) * groups + grp;
+  if (grp >= groups && !WIDE) return;
+  if (row >= static_cast<long>(p.B) * p.N * p.Hq) return;
   const long b = row / (static_cast<long>(p.N) * p.Hq);
   const int len = kv_len(p.c, p.lengths, b);
   const int parts = kv_parts((len >> 6) + ((len & 63) != 0), p.granule);
@@ -22,20 +27,55 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(KvAttn p) {
   const int n = static_cast<int>(row / p.Hq % p.N);
   const bool exists = n < (p.nodes ? min(max(p.nodes[b], 0), p.N) : p.N);
   const long at = row * p.splits;
+  const int first = WIDE ? grp : 0, step = WIDE ? groups : 1;
   float top = -INFINITY;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, p.part_ml[at + i].x);
+  if (WIDE) {
+    for (int i = threadIdx.x % kWave; i < parts; i += kWave) top = fmaxf(top, p.part_ml[at + i].x);
+    top = wave_max(top);
+  } else {
+    for (int i = 0; i < parts; ++i) top = fmaxf(top, p.part_ml[at + i].x);
+  }
   float y[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = p.part_ml[at + i];
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (at + i) * p.c.D + d);
-    y[0] += v.x * f;
-    y[1] += v.y * f;
-    y[2] += v.z * f;
-    y[3] += v.w * f;
-    l += ml.x == -INFINITY ? ml.y : ml.y * f;  // 0, or NaN of a part that saw only NaN
+  if (grp < groups)
+#pragma unroll 4
+    for (int i = first; i < parts; i += step) {
+      const float2 ml = p.part_ml[at + i];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (at + i) * p.c.D + d);
+      y[0] += v.x * f;
+      y[1] += v.y * f;
+      y[2] += v.z * f;
+      y[3] += v.w * f;
+      l += ml.x == -INFINITY ? ml.y : ml.y * f;  // 0, or NaN of a part that saw only NaN
+    }
+  if (WIDE) {
+    sy[threadIdx.x] = make_float4(y[0], y[1], y[2], y[3]);
+    sl[threadIdx.x] = l;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int i = 1; i < groups; ++i) {
+      const float4 v = sy[threadIdx.x + i * tpr];
+      y[0] += v.x;
+      y[1] += v.y;
+      y[2] += v.z;
+      y[3] += v.w;
+      l += sl[threadIdx.x + i * tpr];
+    }
   }
   kv_finish<DT>(p, row, d, y, top, l, exists);
+}
+
+// More parts than this: a workgroup per row.
+constexpr int kWideParts = 8;
+
+template <int DT>
+hipError_t launch_join(const KvAttn& p, hipStream_t st) {
+  const long rows = static_cast<long>(p.B) * p.N * p.Hq, per = kBlock / (p.c.D / 4);
+  if (p.splits > kWideParts)
+    hipLaunchKernelGGL((k_kv_join<DT, true>), dim3(static_cast<unsigned>(rows)), dim3(kBlock), 0, st, p);
+  else
+    hipLaunchKernelGGL((k_kv_join<DT, false>), dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kBlock), 0, st, p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -49,11 +89,7 @@ hipError_t launch_kv_attention(const KvAttn& p, int dtype, int fmt, hipStream_t 
     case 256: rc = launch_kv_attn_256(p, dtype, fmt, st); break;
   }
   if (rc != hipSuccess || p.splits == 1) return rc;
-  const long rows = static_cast<long>(p.B) * p.N * p.Hq, per = kBlock / (p.c.D / 4);
-  const dim3 grid(static_cast<unsigned>((rows + per - 1) / per)), block(kBlock);
-  if (dtype == SPECV_F32) hipLaunchKernelGGL(k_kv_join<SPECV_F32>, grid, block, 0, st, p);
-  else hipLaunchKernelGGL(k_kv_join<SPECV_BF16>, grid, block, 0, st, p);
-  return hipGetLastError();
+  return dtype == SPECV_F32 ? launch_join<SPECV_F32>(p, st) : launch_join<SPECV_BF16>(p, st);
 }
 
 }  // namespace sv

@@ -146,9 +146,8 @@ __device__ inline float groups_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+constexpr int kAWaves = 4, kABlock = kAWaves * kWave;  // waves and threads per workgroup
 constexpr int kTile = 64;                       // cached tokens a wave takes at a time
-constexpr int kDc = 128;                        // channels per round of the final join
-constexpr int kJoinRow = kDc + 4;               // its padded row in LDS
 
 // The queries' fragments stay in registers if they take fewer than 16.
 constexpr bool q_in_lds(int dt, int D, int MT) { return MT * (dt == SPECV_F32 ? 3 : 1) * D / 8 >= 16; }
@@ -159,8 +158,8 @@ constexpr bool k_half(int D, int MT) { return D == 256 || MT == 4; }
 // Waves a SIMD should hold, which bounds the registers of each to 512 /
 // waves: the most that fit without spilling (the build refuses spills).
 constexpr int waves_per(int dt, int D, int MT) {
-  if (D == 256) return 2;
-  if (MT == 1) return D == 64 ? 4 : 3;
+  if (D == 256) return dt == SPECV_F32 ? 1 : 2;
+  if (MT == 1) return D == 64 ? 4 : D == 128 && dt == SPECV_F32 ? 2 : 3;
   if (MT == 2) return D == 64 && dt == SPECV_BF16 ? 3 : 2;
   return 2;
 }
@@ -168,19 +167,19 @@ constexpr int waves_per(int dt, int D, int MT) {
 // One workgroup: MT x 16 queries of one (sequence, cached head) over one of
 // the parts of the sequence's tokens; its waves take the part's tiles in turn.
 template <int DT, int FMT, int D, int MT>
-__global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn p) {
+__global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn p) {
   constexpr int NP = kPieces<DT>, NF = D / 32, ND = D / 16, NC = D / 64;
   const KvView& c = p.c;
   // workgroups of one part and head that differ only in their queries read
   // the same cache: eight apart, they run on the same XCD and share its L2
-  const int per = 8 * p.mb;
-  const long outer = static_cast<long>(blockIdx.x / per) * 8 + blockIdx.x % 8;
+  const unsigned per = 8 * p.mb, outer = blockIdx.x / per * 8 + blockIdx.x % 8;
   const int mblk = blockIdx.x % per / 8;
-  const int part = static_cast<int>(outer % p.splits);
-  const long pair = outer / p.splits;
-  if (pair >= static_cast<long>(p.B) * c.H) return;
-  const int h = static_cast<int>(pair % c.H);
-  const long b = pair / c.H;
+  const unsigned pair = outer / static_cast<unsigned>(p.splits);
+  const int part = static_cast<int>(outer - pair * p.splits);
+  const unsigned seq = pair / static_cast<unsigned>(c.H);
+  if (seq >= static_cast<unsigned>(p.B)) return;
+  const int h = static_cast<int>(pair - seq * c.H);
+  const long b = seq;
   const int len = kv_len(c, p.lengths, b);
   const int ntile = (len >> 6) + ((len & 63) != 0);
   const int parts = kv_parts(ntile, p.granule);
@@ -190,36 +189,32 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
   const int nn = p.nodes ? min(max(p.nodes[b], 0), p.N) : p.N;
   const int rows = nn * p.G;           // queries that exist
   const int row0 = mblk * MT * 16;
+  // r / G: exact, (r + 1/2) / G is at least 2^-11 from an integer and off by 2^-17 at most
+  auto node_of = [&](int r) { return static_cast<int>((r + 0.5f) * p.inv_g); };
 
   // one buffer in LDS: the queries' fragments during the loop (where they
   // would take too many registers), the waves' sums at the join
   constexpr bool QL = q_in_lds(DT, D, MT);
-  constexpr int kJoinBytes = kWaves * 16 * kJoinRow * 4, kQBytes = QL ? MT * NF * NP * kWave * 16 : 0;
+  constexpr int DC = D < 128 ? D : 128, kJoinRow = DC + 4;  // channels per round of the join, its padded row
+  constexpr int kJoinBytes = kAWaves * 16 * kJoinRow * 4, kQBytes = QL ? MT * NF * NP * kWave * 16 : 0;
   __shared__ __align__(16) char lds[kJoinBytes > kQBytes ? kJoinBytes : kQBytes];
   bf16x8* const lq = reinterpret_cast<bf16x8*>(lds);
 
   // ---- queries: B operands, negated where the scale is (kept >= 0) ----
   const float kscale = fabsf(p.scale) * kLog2e;
-  bf16x8 qreg[QL ? 1 : MT][QL ? 1 : NF][NP];
+  constexpr int QF = QL ? (NF + kAWaves - 1) / kAWaves : NF;  // fragments this wave loads
+  bf16x8 qreg[MT][QF][NP];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int r = row0 + mt * 16 + col;
-    const int n = min(r / p.G, p.N - 1);  // a row that exists; what others give is not written
-    const long base = (b * p.N + n) * p.q_row + static_cast<long>(h * p.G + (r < rows ? r - n * p.G : 0)) * D;
+    const int r = min(row0 + mt * 16 + col, p.N * p.G - 1);  // a row that exists; what others give is not written
+    const int n = node_of(r);
+    const long base = (b * p.N + n) * p.q_row + static_cast<long>(h * p.G + (r - n * p.G)) * D;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      if (QL && f % kWaves != w) continue;
-      bf16x8 x[NP];
-      load8<DT>(p.q, base + chan<D>(f, g), x);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (p.scale < 0.f) x[i] = -x[i];
-        if constexpr (QL) lq[((mt * NF + f) * NP + i) * kWave + lane] = x[i];
-        else qreg[mt][f][i] = x[i];
-      }
+    for (int f = 0; f < QF; ++f) {
+      const int frag = QL ? min(f * kAWaves + w, NF - 1) : f;
+      load8<DT>(p.q, base + chan<D>(frag, g), qreg[mt][f]);
     }
   }
-  if constexpr (QL) __syncthreads();
   auto query = [&](int mt, int f, int i) -> bf16x8 {
     if constexpr (QL) return lq[((mt * NF + f) * NP + i) * kWave + lane];
     else return qreg[mt][f][i];
@@ -290,14 +285,155 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
   const uint8_t* this_k = nullptr;
   if (tile < tile1) {
     pid = page_of(tile);
-    pid_next = page_of(tile + kWaves);
+    pid_next = page_of(tile + kAWaves);
     this_k = k_rows(tile, pid);
 #pragma unroll
     for (int t = 0; t < KB; ++t) load_k(this_k, t);
     load_v(tile, pid);
   }
-  for (; tile < tile1; tile += kWaves) {
-    const bool more = tile + kWaves < tile1;
+  // the queries, requested first, are here before the cached bytes
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int f = 0; f < QF; ++f)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (p.scale < 0.f) qreg[mt][f][i] = -qreg[mt][f][i];
+        if constexpr (QL)
+          if (f * kAWaves + w < NF) lq[((mt * NF + f * kAWaves + w) * NP + i) * kWave + lane] = qreg[mt][f][i];
+      }
+  if constexpr (QL) __syncthreads();
+  // ---- the nodes, 16 a wave, with the last part: while the first tile is
+  // on its way, and with every load requested before the first is needed ----
+  static_assert(SPECV_MAX_TREE <= 16 * kAWaves, "a wave has one block of 16 nodes");
+  const int j0 = 16 * w;
+  if (p.kn && part == parts - 1 && j0 < nn) {
+    constexpr int VG = ND < 8 ? ND : 8;  // blocks of 16 channels of V at a time
+    const long at0 = b * p.N * p.kv_row + static_cast<long>(h) * D;
+    float vn[VG][4];
+    auto load_vn = [&](int d0) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const long at = at0 + min(j0 + 4 * g + r, p.N - 1) * p.kv_row + col;
+#pragma unroll
+        for (int d = 0; d < VG; ++d) vn[d][r] = load1<DT>(p.vn, at + 16 * (d0 + d));
+      }
+    };
+    bf16x8 kf[NF][NP];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) load8<DT>(p.kn, at0 + min(j0 + col, p.N - 1) * p.kv_row + chan<D>(f, g), kf[f]);
+    load_vn(0);
+    uint64_t set = 0;
+    if (p.parents) {
+      bool valid;
+      int depth;
+      ancestor_sets(p.parents + b * p.N, p.N, set, valid, depth);
+    } else {
+      set = ~0ull >> (63 - lane);
+    }
+    uint32_t sees[MT];  // bit i: the query sees node j0 + i
+    f32x4 s[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int r = row0 + mt * 16 + col;
+      const uint32_t x = static_cast<uint32_t>(__shfl(static_cast<int>(set >> j0), r < rows ? node_of(r) : 0, kWave));
+      sees[mt] = r < rows ? x & 0xffffu : 0u;
+      s[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+          for (int i = 0; i <= z; ++i) s[mt] = mfma(kf[f][z - i], query(mt, f, i), s[mt]);
+    bf16x8 pf[MT][NP];
+    float keep[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float x = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool ok = (sees[mt] >> (4 * g + r)) & 1;
+        s[mt][r] = ok ? s[mt][r] * kscale : -INFINITY;
+        x = fmaxf(x, s[mt][r]);
+      }
+      raise(mt, groups_max(x));
+#pragma unroll
+      for (int i = 0; i < NP; ++i) pf[mt][i] = bf16x8{};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool ok = (sees[mt] >> (4 * g + r)) & 1;
+        const float e = ok ? ex2(s[mt][r] - m[mt]) : 0.f;
+        l[mt] += e;
+        keep[mt][r] = e;
+        __bf16 piece[3];
+        split<NP>(e, piece);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) pf[mt][i][r] = piece[i];
+      }
+    }
+    // values that are not finite must not meet a weight of 0: they stay out
+    // of the products and are added where they are seen
+    bool wild = false;
+#pragma unroll
+    for (int d0 = 0; d0 < ND; d0 += VG) {
+      if (d0) load_vn(d0);
+#pragma unroll
+      for (int d = 0; d < VG; ++d) {
+        if (d0 + d >= ND) break;
+        bf16x8 vf[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) vf[i] = bf16x8{};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = j0 + 4 * g + r < nn ? vn[d][r] : 0.f;
+          if (!isfinite(x)) {
+            wild = true;
+            x = 0.f;
+          }
+          __bf16 piece[3];
+          split<NP>(x, piece);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) vf[i][r] = piece[i];
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i <= z; ++i) o[mt][d0 + d] = mfma(vf[z - i], pf[mt][i], o[mt][d0 + d]);
+      }
+    }
+    if (__any(wild)) {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {  // nodes j0 + 4 k + i: lane group k holds their weights
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + 4 * k + i;
+          const long at = at0 + min(j, p.N - 1) * p.kv_row + 4 * g;
+          float e[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) e[mt] = __shfl(keep[mt][i], col + 16 * k, kWave);
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              // few loads at a time: this rare part's registers count for the whole kernel's occupancy
+              if (r == 0) __builtin_amdgcn_sched_barrier(0);
+              const float x = load1<DT>(p.vn, at + 16 * d + r);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                if (!isfinite(x) && ((sees[mt] >> (4 * k + i)) & 1) && j < nn) o[mt][d][r] += e[mt] * x;
+            }
+        }
+      }
+    }
+  }
+
+  for (; tile < tile1; tile += kAWaves) {
+    const bool more = tile + kAWaves < tile1;
     // tokens of this lane's 16 that exist; the bytes behind them, and scales
     // of no page, may be anything (NaN too) and are cleared
     const int have = pid < 0 ? 0 : min(max(len - tile * kTile - 16 * g, 0), 16);
@@ -315,7 +451,7 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
       }
     }
     const float kc = ks * kscale;
-    const uint8_t* next_k = more ? k_rows(tile + kWaves, pid_next) : nullptr;
+    const uint8_t* next_k = more ? k_rows(tile + kAWaves, pid_next) : nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // halves of the tile: 8 of each lane's 16 tokens
       // the queries' fragments are read from LDS here, not kept across the loop
@@ -383,137 +519,14 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
           for (int i = NP - 1; i >= 0; --i) o[mt][d] = mfma(vf, pf[mt][i], o[mt][d]);
       }
     }
-    if (more) load_v(tile + kWaves, pid_next);
+    if (more) load_v(tile + kAWaves, pid_next);
     this_k = next_k;
     pid = pid_next;
-    pid_next = page_of(tile + 2 * kWaves);
-  }
-
-  // ---- the nodes, 16 at a time, by the last part's waves in turn ----
-  if (p.kn && part == parts - 1 && 16 * w < nn) {
-    uint64_t set = 0;
-    if (p.parents) {
-      bool valid;
-      int depth;
-      ancestor_sets(p.parents + b * p.N, p.N, set, valid, depth);
-    } else {
-      set = ~0ull >> (63 - lane);
-    }
-    uint64_t sees[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int r = row0 + mt * 16 + col;
-      const int n = r < rows ? r / p.G : 0;
-      const uint64_t x = (static_cast<uint64_t>(static_cast<uint32_t>(__shfl(static_cast<int>(set >> 32), n, kWave))) << 32) |
-                         static_cast<uint32_t>(__shfl(static_cast<int>(set), n, kWave));
-      sees[mt] = r < rows ? x : 0;
-    }
-    for (int j0 = 16 * w; j0 < nn; j0 += 16 * kWaves) {
-      f32x4 s[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) s[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const long krow = (b * p.N + min(j0 + col, p.N - 1)) * p.kv_row + static_cast<long>(h) * D;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        bf16x8 kf[NP];
-        load8<DT>(p.kn, krow + chan<D>(f, g), kf);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int z = 2 * (NP - 1) > 2 ? 2 : 2 * (NP - 1); z >= 0; --z)
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-              if (z - i >= 0 && z - i < NP) s[mt] = mfma(kf[z - i], query(mt, f, i), s[mt]);
-      }
-      bf16x8 pf[MT][NP];
-      float keep[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool ok = (sees[mt] >> (j0 + 4 * g + r)) & 1;
-          s[mt][r] = ok ? s[mt][r] * kscale : -INFINITY;
-          x = fmaxf(x, s[mt][r]);
-        }
-        raise(mt, groups_max(x));
-        pf[mt][0] = bf16x8{};
-        if constexpr (NP == 3) pf[mt][1] = pf[mt][2] = bf16x8{};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool ok = (sees[mt] >> (j0 + 4 * g + r)) & 1;
-          const float e = ok ? ex2(s[mt][r] - m[mt]) : 0.f;
-          l[mt] += e;
-          keep[mt][r] = e;
-          __bf16 piece[3];
-          split<NP>(e, piece);
-#pragma unroll
-          for (int i = 0; i < NP; ++i) pf[mt][i][r] = piece[i];
-        }
-      }
-      // values that are not finite must not meet a weight of 0: they stay out
-      // of the products and are added where they are seen
-      bool wild = false;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        // few loads at a time: this part's registers count for the whole kernel's occupancy
-        if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
-        bf16x8 vf[NP];
-        vf[0] = bf16x8{};
-        if constexpr (NP == 3) vf[1] = vf[2] = bf16x8{};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = j0 + 4 * g + r;
-          float x = load1<DT>(p.vn, (b * p.N + min(j, p.N - 1)) * p.kv_row + static_cast<long>(h) * D + 16 * d + col);
-          if (j >= nn) x = 0.f;
-          if (!isfinite(x)) {
-            wild = true;
-            x = 0.f;
-          }
-          __bf16 piece[3];
-          split<NP>(x, piece);
-#pragma unroll
-          for (int i = 0; i < NP; ++i) vf[i][r] = piece[i];
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int z = NP == 3 ? 2 : 0; z >= 0; --z)
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-              if (z - i >= 0 && z - i < NP) o[mt][d] = mfma(vf[z - i], pf[mt][i], o[mt][d]);
-      }
-      if (__any(wild)) {
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {  // nodes j0 + 4 k + i: lane group k holds their weights
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 4 * k + i;
-            const long at = (b * p.N + min(j, p.N - 1)) * p.kv_row + static_cast<long>(h) * D + 4 * g;
-            float e[MT];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const float t = __shfl(keep[mt][i], col + 16 * k, kWave);
-              e[mt] = j < nn && ((sees[mt] >> (j & 63)) & 1) ? t : 0.f;
-            }
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                if (r == 0) __builtin_amdgcn_sched_barrier(0);
-                const float x = load1<DT>(p.vn, at + 16 * d + r);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                  if (!isfinite(x) && ((sees[mt] >> (j & 63)) & 1) && j < nn) o[mt][d][r] += e[mt] * x;
-              }
-          }
-        }
-      }
-    }
+    pid_next = page_of(tile + 2 * kAWaves);
   }
 
   // ---- join the waves: 16 queries and at most 128 channels a round ----
-  __shared__ float sm[kWaves][MT * 16], sl[kWaves][MT * 16];
+  __shared__ float sm[kAWaves][MT * 16], sl[kAWaves][MT * 16];
   float(*const so)[16 * kJoinRow] = reinterpret_cast<float(*)[16 * kJoinRow]>(lds);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -524,12 +537,11 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
     }
   }
   __syncthreads();
-  constexpr int DC = D < kDc ? D : kDc;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     float top = sm[0][mt * 16 + col];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, sm[i][mt * 16 + col]);
+    for (int i = 1; i < kAWaves; ++i) top = fmaxf(top, sm[i][mt * 16 + col]);
     const float f = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DC) {
@@ -538,21 +550,21 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
       for (int d = 0; d < DC / 16; ++d)
         *reinterpret_cast<f32x4*>(&so[w][col * kJoinRow + 16 * d + 4 * g]) = o[mt][d0 / 16 + d] * f;
       __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (DC / 4); i += kBlock) {
+      for (int i = threadIdx.x; i < 16 * (DC / 4); i += kABlock) {
         const int q = i / (DC / 4), d = i % (DC / 4) * 4;
         const int r = row0 + mt * 16 + q;
         if (r >= p.N * p.G) continue;
         float mx = sm[0][mt * 16 + q], lt = 0.f;
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k) mx = fmaxf(mx, sm[k][mt * 16 + q]);
+        for (int k = 1; k < kAWaves; ++k) mx = fmaxf(mx, sm[k][mt * 16 + q]);
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k)
+        for (int k = 0; k < kAWaves; ++k)
           lt += sm[k][mt * 16 + q] == -INFINITY ? sl[k][mt * 16 + q] : sl[k][mt * 16 + q] * ex2(sm[k][mt * 16 + q] - mx);
         f32x4 acc = *reinterpret_cast<const f32x4*>(&so[0][q * kJoinRow + d]);
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k) acc += *reinterpret_cast<const f32x4*>(&so[k][q * kJoinRow + d]);
+        for (int k = 1; k < kAWaves; ++k) acc += *reinterpret_cast<const f32x4*>(&so[k][q * kJoinRow + d]);
         const float y[4] = {acc[0], acc[1], acc[2], acc[3]};
-        const int n = r / p.G;
+        const int n = node_of(r);
         const long orow = (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
         if (parts == 1) {
           kv_finish<DT>(p, orow, d0 + d, y, mx, lt, r < rows);
@@ -569,7 +581,7 @@ __global__ __launch_bounds__(kBlock, waves_per(DT, D, MT)) void k_kv_attn(KvAttn
 template <int DT, int FMT, int D, int MT>
 hipError_t launch_one(const KvAttn& p, hipStream_t st) {
   const long outer = (static_cast<long>(p.B) * p.c.H * p.splits + 7) / 8 * 8;
-  hipLaunchKernelGGL((k_kv_attn<DT, FMT, D, MT>), dim3(static_cast<unsigned>(outer * p.mb)), dim3(kBlock), 0, st, p);
+  hipLaunchKernelGGL((k_kv_attn<DT, FMT, D, MT>), dim3(static_cast<unsigned>(outer * p.mb)), dim3(kABlock), 0, st, p);
   return hipGetLastError();
 }
 

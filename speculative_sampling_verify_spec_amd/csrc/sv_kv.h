@@ -54,6 +54,7 @@ struct KvAttn {
   const int32_t* parents; // or null: a chain
   float scale;
   int B, N, Hq, G;        // G = Hq / H query heads share a cached head
+  float inv_g;            // 1 / G
   void* out;              // [B][N][Hq][D]
   float* lse;             // [B][N][Hq] or null
   // plan (kv_plan) and workspace

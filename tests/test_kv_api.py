@@ -102,7 +102,7 @@ def test_read_refusals(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=7), -3), (dict(q=None), -1), (dict(lengths=None), -1), (dict(out=None), -1), (dict(k=None), -1),
     (dict(v=None), -1), (dict(B=0), -2), (dict(B=65536), -2), (dict(N=0), -2), (dict(N=65), -2), (dict(Hq=0), -2),
-    (dict(Hq=12), -2), (dict(Hq=1 << 15), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2),
+    (dict(Hq=12), -2), (dict(Hq=1 << 15), -2), (dict(Hq=8 * 1025), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2),
     (dict(qs=100), -2), (dict(qs=32 * 128 + 4), -6), (dict(ks=8 * 128 + 1), -6), (dict(q=BASE + 2), -6),
     (dict(k=BASE + 8), -6), (dict(v=BASE + 8), -6), (dict(out=BASE + 8), -6), (dict(ws=None), -5),
     (dict(ws=BASE + 16), -5), (dict(wsb=8), -5)])
@@ -119,7 +119,7 @@ def test_null_descriptor(lib):
 def test_workspace_sizes(lib):
     """Every valid shape has a size, and it does not overflow at the largest ones."""
     for B, N, Hq, c in ((1, 1, 8, kv()), (256, 9, 32, kv()), (4096, 64, 64, kv(heads=8, dim=256)), (65535, 1, 8, kv()),
-                        (1, 64, 32760, kv(heads=8, dim=256, max_pages=(1 << 24) - 1))):
+                        (1, 64, 8192, kv(heads=8, dim=256, max_pages=(1 << 24) - 1))):
         n = lib.spec_kv_attention_workspace_size(ctypes.byref(c), B, N, Hq)
         assert 0 < n < 1 << 46 and n % 256 == 0, (B, N, Hq, n)
     for B, N, Hq in ((0, 1, 8), (1, 0, 8), (1, 65, 8), (1, 1, 0), (1, 1, 9), (65536, 1, 8)):
