@@ -62,7 +62,12 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(KvAttn p) {
       l += sl[threadIdx.x + i * tpr];
     }
   }
-  kv_finish<DT>(p, row, d, y, top, l, exists);
+  const bool some = exists && !(l == 0.f);  // a query that exists and sees something
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = some ? y[j] * inv : 0.f;
+  kv_store4<DT>(p.out, row * p.c.D + d, y);
+  if (d == 0 && p.lse) p.lse[row] = kv_lse(top, l, some);
 }
 
 // More parts than this: a workgroup per row.

@@ -120,6 +120,14 @@ __device__ inline float load1(const void* base, long i) {
   else return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
 }
 
+// A barrier that orders LDS only: __syncthreads would also wait for every
+// global load and store in flight, the next tile's among them.
+__device__ inline void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // First channel of the 8 that lane group g holds of fragment f: fragments 2c
 // and 2c + 1 are the halves of the 16 bytes a lane loads of 64 channels; a
 // last odd fragment is an 8-byte load of 32.
@@ -302,7 +310,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         if constexpr (QL)
           if (f * kAWaves + w < NF) lq[((mt * NF + f * kAWaves + w) * NP + i) * kWave + lane] = qreg[mt][f][i];
       }
-  if constexpr (QL) __syncthreads();
+  if constexpr (QL) lds_barrier();
   // ---- the nodes, 16 a wave, with the last part: while the first tile is
   // on its way, and with every load requested before the first is needed ----
   static_assert(SPECV_MAX_TREE <= 16 * kAWaves, "a wave has one block of 16 nodes");
@@ -526,7 +534,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
   }
 
   // ---- join the waves: 16 queries and at most 128 channels a round ----
-  __shared__ float sm[kAWaves][MT * 16], sl[kAWaves][MT * 16];
+  __shared__ float sm[kAWaves][MT * 16], sl[kAWaves][MT * 16], sinv[MT * 16];
   float(*const so)[16 * kJoinRow] = reinterpret_cast<float(*)[16 * kJoinRow]>(lds);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -536,7 +544,28 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
       sl[w][mt * 16 + col] = t;
     }
   }
-  __syncthreads();
+  lds_barrier();
+  // a row's place in the output (and, with `part`, among the parts)
+  auto out_row = [&](int r) -> long {
+    const int n = node_of(r);
+    return (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
+  };
+  if (threadIdx.x < MT * 16) {  // the rows' statistics
+    const int q = threadIdx.x, r = row0 + q;
+    float mx = sm[0][q], lt = 0.f;
+#pragma unroll
+    for (int k = 1; k < kAWaves; ++k) mx = fmaxf(mx, sm[k][q]);
+#pragma unroll
+    for (int k = 0; k < kAWaves; ++k) lt += sm[k][q] == -INFINITY ? sl[k][q] : sl[k][q] * ex2(sm[k][q] - mx);
+    if (parts > 1) {
+      sinv[q] = 1.f;
+      if (r < p.N * p.G) p.part_ml[out_row(r) * p.splits + part] = make_float2(mx, lt);
+    } else {
+      const bool some = r < rows && !(lt == 0.f);  // a query that exists and sees something
+      sinv[q] = some ? 1.f / lt : 0.f;
+      if (r < p.N * p.G && p.lse) p.lse[out_row(r)] = kv_lse(mx, lt, some);
+    }
+  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     float top = sm[0][mt * 16 + col];
@@ -545,33 +574,28 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     const float f = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top);
 #pragma unroll
     for (int d0 = 0; d0 < D; d0 += DC) {
-      if (mt || d0) __syncthreads();
+      if (mt || d0) lds_barrier();
 #pragma unroll
       for (int d = 0; d < DC / 16; ++d)
         *reinterpret_cast<f32x4*>(&so[w][col * kJoinRow + 16 * d + 4 * g]) = o[mt][d0 / 16 + d] * f;
-      __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (DC / 4); i += kABlock) {
+      lds_barrier();
+#pragma unroll
+      for (int i0 = 0; i0 < 16 * (DC / 4); i0 += kABlock) {
+        const int i = i0 + threadIdx.x;
         const int q = i / (DC / 4), d = i % (DC / 4) * 4;
         const int r = row0 + mt * 16 + q;
-        if (r >= p.N * p.G) continue;
-        float mx = sm[0][mt * 16 + q], lt = 0.f;
-#pragma unroll
-        for (int k = 1; k < kAWaves; ++k) mx = fmaxf(mx, sm[k][mt * 16 + q]);
-#pragma unroll
-        for (int k = 0; k < kAWaves; ++k)
-          lt += sm[k][mt * 16 + q] == -INFINITY ? sl[k][mt * 16 + q] : sl[k][mt * 16 + q] * ex2(sm[k][mt * 16 + q] - mx);
+        if (i >= 16 * (DC / 4) || r >= p.N * p.G) continue;
         f32x4 acc = *reinterpret_cast<const f32x4*>(&so[0][q * kJoinRow + d]);
 #pragma unroll
         for (int k = 1; k < kAWaves; ++k) acc += *reinterpret_cast<const f32x4*>(&so[k][q * kJoinRow + d]);
-        const float y[4] = {acc[0], acc[1], acc[2], acc[3]};
-        const int n = node_of(r);
-        const long orow = (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
-        if (parts == 1) {
-          kv_finish<DT>(p, orow, d0 + d, y, mx, lt, r < rows);
+        if (parts > 1) {
+          *reinterpret_cast<f32x4*>(p.part_o + (out_row(r) * p.splits + part) * D + d0 + d) = acc;
         } else {
-          const long at = orow * p.splits + part;
-          *reinterpret_cast<f32x4*>(p.part_o + at * D + d0 + d) = acc;
-          if (d0 + d == 0) p.part_ml[at] = make_float2(mx, lt);
+          const float inv = sinv[mt * 16 + q];
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = inv == 0.f ? 0.f : acc[e] * inv;  // 0 also where the sums are not finite
+          kv_store4<DT>(p.out, out_row(r) * D + d0 + d, y);
         }
       }
     }

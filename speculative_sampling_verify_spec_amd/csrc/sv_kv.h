@@ -182,20 +182,9 @@ __device__ inline void kv_store16(void* base, long i, const float* f) {
   }
 }
 
-// Channels d .. d + 3 of an output row from its sums y of weight * value and
-// its softmax statistics; with channel 0 the row's lse.  A query that sees
-// nothing (l = 0) or does not exist gets 0 and -infinity.
-template <int DT>
-__device__ inline void kv_finish(const KvAttn& p, long row, int d, const float* y, float m, float l, bool exists) {
-  const bool some = exists && !(l == 0.f);
-  const float inv = 1.f / l;
-  float f[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = some ? y[j] * inv : 0.f;
-  kv_store4<DT>(p.out, row * p.c.D + d, f);
-  if (d == 0 && p.lse)
-    p.lse[row] = some ? static_cast<float>(0.6931471805599453 * (static_cast<double>(m) + __builtin_amdgcn_logf(l)))
-                      : -INFINITY;
+// ln of a row's sum of weights from its statistics (scores in log2).
+__device__ inline float kv_lse(float m, float l, bool some) {
+  return some ? static_cast<float>(0.6931471805599453 * (static_cast<double>(m) + __builtin_amdgcn_logf(l))) : -INFINITY;
 }
 
 #endif  // __HIPCC__
