@@ -237,12 +237,13 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[mt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // moves the held maximum of a query to x, its maximum so far, where x
-  // exceeds it by too much; each query decides for itself, so that its bits do
-  // not depend on what the queries beside it see
+  // moves the held maximum of a query to the largest x of its four lanes where
+  // one exceeds it by too much; each query decides for itself, so that its
+  // bits do not depend on what the queries beside it see
   auto raise = [&](int mt, float x) {
-    const bool need = x > m[mt] + kLazyMax;  // true for the first finite x
-    if (!__any(need)) return;
+    if (!__any(x > m[mt] + kLazyMax)) return;  // true for the first finite x
+    x = groups_max(x);
+    const bool need = x > m[mt] + kLazyMax;
     const float a = need ? ex2(m[mt] - x) : 1.f;
     m[mt] = need ? x : m[mt];
     l[mt] *= a;
@@ -367,7 +368,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         s[mt][r] = ok ? s[mt][r] * kscale : -INFINITY;
         x = fmaxf(x, s[mt][r]);
       }
-      raise(mt, groups_max(x));
+      raise(mt, x);
 #pragma unroll
       for (int i = 0; i < NP; ++i) pf[mt][i] = bf16x8{};
 #pragma unroll
@@ -447,7 +448,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     const int have = pid < 0 ? 0 : min(max(len - tile * kTile - 16 * g, 0), 16);
     const bool whole = __all(have == 16);
     if (!whole) {
-      if (have == 0) ks = vs = 0.f;
+      if (have == 0) ks = vs = 1.f;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
         uint32_t* x = reinterpret_cast<uint32_t*>(&vraw[d]);
@@ -458,7 +459,10 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         }
       }
     }
-    const float kc = ks * kscale;
+    // > 0 also for a scale of 0, so that a masked score of -inf stays -inf
+    const float kc = fmaxf(ks * kscale, FLT_MIN);
+    // bf16: the V scale enters as its logarithm (exact for a power of two)
+    const float lvs = NP == 1 ? __builtin_amdgcn_logf(vs) : 0.f, per_vs = NP == 1 ? 1.f / vs : 1.f;
     const uint8_t* next_k = more ? k_rows(tile + kAWaves, pid_next) : nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // halves of the tile: 8 of each lane's 16 tokens
@@ -491,25 +495,28 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
       bf16x8 pf[MT][NP];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float x = -FLT_MAX;
+        if (!whole) {
+          m[mt] = fmaxf(m[mt], -FLT_MAX);  // finite, also while the query has seen nothing
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (!whole && 8 * j + e >= have) s[mt][e / 4][e % 4] = -FLT_MAX;
-          x = fmaxf(x, s[mt][e / 4][e % 4]);
+          for (int e = 0; e < 8; ++e)
+            if (8 * j + e >= have) s[mt][e / 4][e % 4] = -INFINITY;
         }
-        raise(mt, groups_max(x * kc));
+        float x = s[mt][0][0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) x = fmaxf(x, s[mt][e / 4][e % 4]);
+        raise(mt, x * kc);
+        const float shift = lvs - m[mt];
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float y = ex2(fmaf(s[mt][e / 4][e % 4], kc, -m[mt]));
-          if (!whole && 8 * j + e >= have) y = 0.f;  // also where the maximum is still -inf
+          const float y = ex2(fmaf(s[mt][e / 4][e % 4], kc, shift));
           sum += y;
           __bf16 piece[3];
-          split<NP>(y * vs, piece);
+          split<NP>(NP == 1 ? y : y * vs, piece);
 #pragma unroll
           for (int i = 0; i < NP; ++i) pf[mt][i][e] = piece[i];
         }
-        l[mt] += sum;
+        l[mt] += sum * per_vs;
       }
       if (KB == 2 && j == 0) {
         load_k(this_k, 2);
