@@ -144,7 +144,7 @@ def _check_rows(cache: KVCache, name: str, t, B: int, N: int, heads: int) -> int
 def _call(device, fn, *args) -> None:
     """One library call on the device's current stream (the last argument)."""
     import torch
-    st = torch.cuda.current_stream(device).cuda_stream
+    st = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream(device), without its object
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             rc = fn(*args, st)

@@ -61,7 +61,7 @@ struct KvPlan {
 };
 
 constexpr long kTargetGroups = 512;   // workgroups to aim at: two on each of 256 CUs
-constexpr int kMinGranule = 4;        // tiles per part, at least one for each wave
+constexpr int kMinGranule = 16;       // tiles per part, four for each wave: a second launch costs more than they take
 
 KvPlan kv_plan(const KvView& c, int B, int N, int Hq, int dtype) {
   KvPlan pl;

@@ -28,7 +28,6 @@ namespace {
 
 __device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
   v = wave_min_i32(v);
-  __syncthreads();
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
   int t = lds[0];
@@ -48,149 +47,188 @@ __device__ inline void item_of(const KvView& c, int isv, int i, int vpr, int& a,
   }
 }
 
-// One workgroup per (page the call may touch, K or V of a head, sequence);
-// NI items per thread, whose values stay in registers between the search for
-// the largest magnitude and the quantisation.
-template <int DT, int FMT, int NI>
+// A workgroup takes K and V (BOTH) or one of them of one head of one
+// sequence, in every gridDim.x-th page that the call may touch.  NI items per
+// thread of each; their values stay in registers between the search for the
+// largest magnitude and the quantisation.
+template <int DT, int FMT, int NI, bool BOTH>
 __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
-  constexpr int E = Elt<DT>::kPerVec;
+  constexpr int E = Elt<DT>::kPerVec, NX = BOTH ? 2 : 1;
   const KvView& c = p.c;
-  const int slot = blockIdx.x, h = blockIdx.y >> 1, isv = blockIdx.y & 1;
+  const int h = BOTH ? blockIdx.y : blockIdx.y >> 1;
   const long b = blockIdx.z;
   const int tid = threadIdx.x;
-  __shared__ float ldsf[kWaves];
+  __shared__ float ldsf[NX][kWaves];
   __shared__ int ldsi[kWaves];
 
   const int len = kv_len(c, p.lengths, b);
   const int room = (c.width << c.pshift) - len;
   int n = min(p.counts ? min(max(p.counts[b], 0), p.N) : p.N, room);
   // the tokens end at the first index outside [0, N), and at the first page
-  // the table does not have; every page before this workgroup's counts (and
-  // every page, where the new length is written)
-  const bool reports = slot == 0 && blockIdx.y == 0 && p.out_lengths;
+  // the table does not have; every page up to this workgroup's last counts
+  // (every page at all, where the new length is written)
+  const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && p.out_lengths;
   const int col0 = len >> c.pshift;
   int stop = n;
-  if (p.index)
-    for (int i = tid; i < n; i += kBlock) {
-      const int ix = p.index[b * p.N + i];
-      if (ix < 0 || ix >= p.N) stop = min(stop, i);
-    }
   if (n > 0) {
     const int end = (len + n - 1) >> c.pshift;
-    const int last = reports || slot > end - col0 ? end : col0 + slot;
-    for (int col = col0 + tid; col <= last; col += kBlock)
+    const int last = reports || gridDim.x == 1 || static_cast<int>(blockIdx.x) > end - col0 ? end : col0 + blockIdx.x;
+    const int i0 = min(tid, n - 1), c0 = min(col0 + tid, last);  // both loads before either test
+    const int ix0 = p.index ? p.index[b * p.N + i0] : 0, id0 = c.table[b * c.width + c0];
+    if (ix0 < 0 || ix0 >= p.N) stop = min(stop, i0);
+    if (id0 < 0 || id0 >= c.pages) stop = min(stop, max((c0 << c.pshift) - len, 0));
+    if (p.index)
+      for (int i = tid + kBlock; i < n; i += kBlock) {
+        const int ix = p.index[b * p.N + i];
+        if (ix < 0 || ix >= p.N) stop = min(stop, i);
+      }
+    for (int col = col0 + tid + kBlock; col <= last; col += kBlock)
       if (kv_page(c, b, col) < 0) stop = min(stop, max((col << c.pshift) - len, 0));
   }
   n = block_min_i32(stop, ldsi);
   if (reports && tid == 0) p.out_lengths[b] = len + n;
 
-  const long p0 = (static_cast<long>(col0) + slot) << c.pshift;               // the page's first position
-  const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
-  const int t1 = static_cast<int>(min(len + n - p0, static_cast<long>(c.P)));  // and after
-  if (t1 <= t0) return;
-  const int id = kv_page(c, b, p0 >> c.pshift);      // a page: n ends before the first that is not
-  const long blk = static_cast<long>(id) * c.H + h;
-  float* sp = (isv ? c.vs : c.ks) + blk;
-  const float s_old = *sp;
-  const char* src = static_cast<const char*>(isv ? p.v : p.k) + static_cast<long>(h) * c.D * Elt<DT>::kBytes;
   const int vpr = c.D / E, items = (c.P / 4) * vpr;
+  for (long col = static_cast<long>(col0) + blockIdx.x; (col << c.pshift) < static_cast<long>(len) + n; col += gridDim.x) {
+    const long p0 = col << c.pshift;                                            // the page's first position
+    const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
+    const int t1 = static_cast<int>(min(len + n - p0, static_cast<long>(c.P)));  // and after
+    const long blk = static_cast<long>(kv_page(c, b, col)) * c.H + h;  // a page: n ends before the first that is not
+    // byte masks of a word of tokens 4 a .. 4 a + 3: those this call writes,
+    // and those cached before
+    auto fresh_mask = [&](int a) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m |= 4 * a + r >= t0 && 4 * a + r < t1 ? 0xffu << (8 * r) : 0u;
+      return m;
+    };
+    auto old_mask = [&](int a) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m |= 4 * a + r < t0 ? 0xffu << (8 * r) : 0u;
+      return m;
+    };
 
-  uint4 raw[NI][4];
-  float amax = 0.f;
+    uint4 raw[NX][NI][4];
+    uint32_t cur[NI][E];  // V: words that get some new bytes, as they are
+    float s_old[NX], amax[NX];
 #pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + k * kBlock;
-    int a, v;
-    item_of(c, isv, i, vpr, a, v);
+    for (int x = 0; x < NX; ++x) {
+      const int isv = BOTH ? x : blockIdx.y & 1;
+      s_old[x] = (isv ? c.vs : c.ks)[blk];
+      amax[x] = 0.f;
+      const char* src = static_cast<const char*>(isv ? p.v : p.k) + static_cast<long>(h) * c.D * Elt<DT>::kBytes;
+      const uint8_t* page = c.vp + blk * c.P * c.D;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 4 * a + r;
-      raw[k][r] = make_uint4(0, 0, 0, 0);
-      if (i < items && t >= t0 && t < t1) {
-        const long at = p0 + t - len;
-        const long row = b * p.N + (p.index ? p.index[b * p.N + at] : at);
-        raw[k][r] = load16(src + row * p.row * Elt<DT>::kBytes, v);
-      }
-    }
-  }
+      for (int k = 0; k < NI; ++k) {
+        const int i = tid + k * kBlock;
+        int a, v;
+        item_of(c, isv, i, vpr, a, v);
 #pragma unroll
-  for (int k = 0; k < NI; ++k)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float f[E];
-      Elt<DT>::unpack(raw[k][r], f);
-#pragma unroll
-      for (int j = 0; j < E; ++j) amax = fmaxf(amax, isfinite(f[j]) ? fabsf(f[j]) : 0.f);
-    }
-  amax = block_max(amax, ldsf);
-  float s = kv_scale<FMT>(amax);
-  if (t0 > 0) s = fmaxf(s, s_old);
-  const bool grow = t0 > 0 && s > s_old;  // the tokens that were there go to the grown scale
-  const float inv = 1.f / s, ratio = s_old * inv;
-  uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
-#pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int i = tid + k * kBlock;
-    if (i >= items) break;
-    int a, v;
-    item_of(c, isv, i, vpr, a, v);
-    float f[4][E];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      Elt<DT>::unpack(raw[k][r], f[r]);
-#pragma unroll
-      for (int j = 0; j < E; ++j) f[r][j] *= inv;
-    }
-    if (!isv) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 4 * a + r;
-        uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(t) * c.D + v * E);
-        const bool fresh = t >= t0 && t < t1;
-        if (!fresh && !(grow && t < t0)) continue;
-        uint32_t w[E / 4];
-#pragma unroll
-        for (int j = 0; j < E / 4; ++j) {
-          float g[4];
-          if (!fresh) {
-            kv_decode4<FMT>(at[j], g);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[e] *= ratio;
+        for (int r = 0; r < 4; ++r) {
+          const int t = 4 * a + r;
+          raw[x][k][r] = make_uint4(0, 0, 0, 0);
+          if (i < items && t >= t0 && t < t1) {
+            const long at = p0 + t - len;
+            const long row = b * p.N + (p.index ? p.index[b * p.N + at] : at);
+            raw[x][k][r] = load16(src + row * p.row * Elt<DT>::kBytes, v);
           }
-          w[j] = kv_encode4<FMT>(fresh ? &f[r][4 * j] : g);
         }
-        if constexpr (E == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-        else *at = w[0];
-      }
-    } else {
-      // byte masks of the word's new tokens and of those to round again; the
-      // other bytes of a word are kept
-      uint32_t fresh = 0, again = 0;
+        if (isv && i < items) {
+          const uint32_t fresh = fresh_mask(a);
+          if (fresh && fresh != ~0u)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 4 * a + r;
-        if (t >= t0 && t < t1) fresh |= 0xffu << (8 * r);
-        else if (grow && t < t0) again |= 0xffu << (8 * r);
-      }
-      if (!(fresh | again)) continue;
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(v * E + j) * c.P + 4 * a);
-        const float x[4] = {f[0][j], f[1][j], f[2][j], f[3][j]};
-        uint32_t w = kv_encode4<FMT>(x);
-        if (fresh != ~0u) {
-          const uint32_t cur = *at;
-          float g[4];
-          kv_decode4<FMT>(cur, g);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) g[e] *= ratio;
-          w = (w & fresh) | (kv_encode4<FMT>(g) & again) | (cur & ~(fresh | again));
+            for (int j = 0; j < E; ++j)
+              cur[k][j] = *reinterpret_cast<const uint32_t*>(page + static_cast<long>(v * E + j) * c.P + 4 * a);
         }
-        *at = w;
       }
     }
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+#pragma unroll
+      for (int k = 0; k < NI; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float f[E];
+          Elt<DT>::unpack(raw[x][k][r], f);
+#pragma unroll
+          for (int j = 0; j < E; ++j) amax[x] = fmaxf(amax[x], isfinite(f[j]) ? fabsf(f[j]) : 0.f);
+        }
+      amax[x] = wave_max(amax[x]);
+    }
+    __syncthreads();  // also: nobody reads the LDS of the page before any more
+    if (tid % kWave == 0)
+#pragma unroll
+      for (int x = 0; x < NX; ++x) ldsf[x][tid / kWave] = amax[x];
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const int isv = BOTH ? x : blockIdx.y & 1;
+      float top = ldsf[x][0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) top = fmaxf(top, ldsf[x][i]);
+      float s = kv_scale<FMT>(top);
+      if (t0 > 0) s = fmaxf(s, s_old[x]);
+      const bool grow = t0 > 0 && s > s_old[x];  // the tokens that were there go to the grown scale
+      const float inv = 1.f / s, ratio = s_old[x] * inv;
+      uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int i = tid + k * kBlock;
+        if (i >= items) break;
+        int a, v;
+        item_of(c, isv, i, vpr, a, v);
+        float f[4][E];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          Elt<DT>::unpack(raw[x][k][r], f[r]);
+#pragma unroll
+          for (int j = 0; j < E; ++j) f[r][j] *= inv;
+        }
+        if (!isv) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int t = 4 * a + r;
+            uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(t) * c.D + v * E);
+            const bool fresh = t >= t0 && t < t1;
+            if (!fresh && !(grow && t < t0)) continue;
+            uint32_t w[E / 4];
+            if (fresh) {
+#pragma unroll
+              for (int j = 0; j < E / 4; ++j) w[j] = kv_encode4<FMT>(&f[r][4 * j]);
+            } else {
+              uint32_t had[E / 4];
+#pragma unroll
+              for (int j = 0; j < E / 4; ++j) had[j] = at[j];
+#pragma unroll
+              for (int j = 0; j < E / 4; ++j) w[j] = kv_rescale4<FMT>(had[j], ratio);
+            }
+            if constexpr (E == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+            else *at = w[0];
+          }
+        } else {
+          const uint32_t fresh = fresh_mask(a), again = grow ? old_mask(a) : 0;
+          if (!(fresh | again)) continue;
+          uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(v * E) * c.P + 4 * a);
+          const int step = c.P / 4;
+          if (!fresh)  // all loads before the first store
+#pragma unroll
+            for (int j = 0; j < E; ++j) cur[k][j] = at[j * step];
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            const float y[4] = {f[0][j], f[1][j], f[2][j], f[3][j]};
+            uint32_t w = kv_encode4<FMT>(y);
+            if (fresh != ~0u) {
+              w = (w & fresh) | (cur[k][j] & ~fresh);
+              if (again) w = (w & ~again) | (kv_rescale4<FMT>(cur[k][j], ratio) & again);
+            }
+            at[j * step] = w;
+          }
+        }
+      }
+      if (tid == 0) (isv ? c.vs : c.ks)[blk] = s;
+    }
   }
-  if (tid == 0) *sp = s;
 }
 
 // One workgroup per (page the range may touch, K or V of a head, sequence).
@@ -279,12 +317,17 @@ unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P 
 
 template <int DT, int FMT>
 hipError_t append(const KvAppend& p, hipStream_t st) {
-  const dim3 grid(kv_slots(p.N, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
-  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);  // at most 8 kBlock
-  if (items <= kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 1>), grid, block, 0, st, p);
-  else if (items <= 2 * kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 2>), grid, block, 0, st, p);
-  else if (items <= 4 * kBlock) hipLaunchKernelGGL((k_kv_append<DT, FMT, 4>), grid, block, 0, st, p);
-  else if constexpr (DT == SPECV_F32) hipLaunchKernelGGL((k_kv_append<DT, FMT, 8>), grid, block, 0, st, p);
+  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);  // at most 2048
+  const unsigned slots = kv_slots(p.N, p.c.P), H = static_cast<unsigned>(p.c.H), B = static_cast<unsigned>(p.B);
+  // a few tokens rarely cross into a second page: one workgroup takes both
+  const unsigned gx = slots <= 2 ? 1 : slots;
+#define LAUNCH(ni, both) \
+  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, both>), dim3(gx, both ? H : 2 * H, B), dim3(kBlock), 0, st, p)
+  if (items <= kBlock) LAUNCH(1, true);
+  else if (items <= 2 * kBlock) LAUNCH(2, true);
+  else if (items <= 4 * kBlock) LAUNCH(4, false);
+  else if constexpr (DT == SPECV_F32) LAUNCH(8, false);
+#undef LAUNCH
   return hipGetLastError();
 }
 

@@ -127,6 +127,16 @@ __device__ inline uint32_t kv_encode4(const float* x) {
   }
 }
 
+// Four codes to the codes of ratio times their values.
+template <int FMT>
+__device__ inline uint32_t kv_rescale4(uint32_t w, float ratio) {
+  float f[4];
+  kv_decode4<FMT>(w, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] *= ratio;
+  return kv_encode4<FMT>(f);
+}
+
 // The smallest power of two s with amax <= top * s, at least 2^-126 (the
 // smallest normal number, also for amax = 0).  amax is finite, so s <= 2^121.
 template <int FMT>
