@@ -14,7 +14,7 @@
 // reads V along the tokens.
 //
 // Both kernels give one workgroup to the K or V of one block.  Its items are
-// 4 tokens x 16 bytes of a value row.  For K, neighbouring lanes take
+// 4 tokens x 16 bytes of a value row, of the tokens the call touches.  For K, neighbouring lanes take
 // neighbouring channels (whole rows on both sides); for V neighbouring lanes
 // take neighbouring tokens, so that the four codes of a channel, one word,
 // meet their neighbours in the transposed page and the rows are still touched
@@ -36,15 +36,12 @@ __device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
   return t;
 }
 
-// Item i of a block: tokens 4 a .. 4 a + 3, vector v of the row.
-__device__ inline void item_of(const KvView& c, int isv, int i, int vpr, int& a, int& v) {
-  if (isv) {
-    a = i & (c.P / 4 - 1);
-    v = i >> (c.pshift - 2);
-  } else {
-    a = i / vpr;
-    v = i - a * vpr;
-  }
+// Item i of a block's tokens 4 a0 .. 4 (a0 + na) - 1: tokens 4 a .. 4 a + 3,
+// vector v of their rows of vpr.
+__device__ inline void item_of(int isv, unsigned i, int a0, unsigned na, unsigned vpr, int& a, int& v) {
+  const unsigned per = isv ? na : vpr, q = i / per, r = i - q * per;
+  a = a0 + static_cast<int>(isv ? r : q);
+  v = static_cast<int>(isv ? q : r);
 }
 
 // A workgroup takes K and V (BOTH) or one of them of one head of one
@@ -87,13 +84,16 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
   }
   n = block_min_i32(stop, ldsi);
   if (reports && tid == 0) p.out_lengths[b] = len + n;
+  if (n <= 0) return;  // below, every page visited gets at least one token
 
-  const int vpr = c.D / E, items = (c.P / 4) * vpr;
+  const int vpr = c.D / E;
   for (long col = static_cast<long>(col0) + blockIdx.x; (col << c.pshift) < static_cast<long>(len) + n; col += gridDim.x) {
     const long p0 = col << c.pshift;                                            // the page's first position
     const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
     const int t1 = static_cast<int>(min(len + n - p0, static_cast<long>(c.P)));  // and after
     const long blk = static_cast<long>(kv_page(c, b, col)) * c.H + h;  // a page: n ends before the first that is not
+    // only the groups of four tokens that get new ones
+    const int a0 = t0 / 4, na = (t1 + 3) / 4 - a0, items = na * vpr;
     // byte masks of a word of tokens 4 a .. 4 a + 3: those this call writes,
     // and those cached before
     auto fresh_mask = [&](int a) {
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
       for (int k = 0; k < NI; ++k) {
         const int i = tid + k * kBlock;
         int a, v;
-        item_of(c, isv, i, vpr, a, v);
+        item_of(isv, i, a0, na, vpr, a, v);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = 4 * a + r;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
         const int i = tid + k * kBlock;
         if (i >= items) break;
         int a, v;
-        item_of(c, isv, i, vpr, a, v);
+        item_of(isv, i, a0, na, vpr, a, v);
         float f[4][E];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -208,12 +208,8 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
           }
         } else {
           const uint32_t fresh = fresh_mask(a), again = grow ? old_mask(a) : 0;
-          if (!(fresh | again)) continue;
           uint32_t* at = reinterpret_cast<uint32_t*>(page + static_cast<long>(v * E) * c.P + 4 * a);
           const int step = c.P / 4;
-          if (!fresh)  // all loads before the first store
-#pragma unroll
-            for (int j = 0; j < E; ++j) cur[k][j] = at[j * step];
 #pragma unroll
           for (int j = 0; j < E; ++j) {
             const float y[4] = {f[0][j], f[1][j], f[2][j], f[3][j]};
@@ -226,6 +222,21 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
           }
         }
       }
+      if (grow)  // the groups before, of old tokens only
+        for (int i = tid; i < a0 * vpr; i += kBlock) {
+          int a, v;
+          item_of(isv, i, 0, a0, vpr, a, v);
+          // K: 4 rows of E codes; V: E rows of 4
+          uint32_t* at = reinterpret_cast<uint32_t*>(page + (isv ? static_cast<long>(v * E) * c.P + 4 * a
+                                                                : static_cast<long>(4 * a) * c.D + v * E));
+          const int step = (isv ? c.P : c.D) / 4;
+          uint32_t had[E];
+#pragma unroll
+          for (int j = 0; j < E; ++j) had[j] = at[isv ? j * step : j / (E / 4) * step + j % (E / 4)];
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            at[isv ? j * step : j / (E / 4) * step + j % (E / 4)] = kv_rescale4<FMT>(had[j], ratio);
+        }
       if (tid == 0) (isv ? c.vs : c.ks)[blk] = s;
     }
   }
@@ -252,7 +263,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   const long blk = static_cast<long>(max(id, 0)) * c.H + h;
   const float s = (isv ? c.vs : c.ks)[blk];
   const uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
-  const int vpr = c.D / E, items = (c.P / 4) * vpr;
+  const int a0 = t0 / 4, na = (t1 + 3) / 4 - a0, vpr = c.D / E, items = na * vpr;
   // row t's place in the output: token p0 + t - start
   const long row0 = b * p.T + (p0 - start);
 
@@ -261,7 +272,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   for (int k = 0; k < NI; ++k) {
     const int i = static_cast<int>(threadIdx.x) + k * kBlock;
     int a, v;
-    item_of(c, isv, i < items ? i : 0, vpr, a, v);
+    item_of(isv, i < items ? i : 0, a0, na, vpr, a, v);
     if (!isv) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -285,7 +296,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
     const int i = static_cast<int>(threadIdx.x) + k * kBlock;
     if (i >= items) break;
     int a, v;
-    item_of(c, isv, i, vpr, a, v);
+    item_of(isv, i, a0, na, vpr, a, v);
     float f[4][E];
     if (!isv) {
 #pragma unroll
