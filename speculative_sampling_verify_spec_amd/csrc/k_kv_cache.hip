@@ -87,6 +87,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
   if (n <= 0) return;  // below, every page visited gets at least one token
 
   const int vpr = c.D / E;
+  const int wave0 = __builtin_amdgcn_readfirstlane(tid) & ~(kWave - 1);  // the wave's first item
   for (long col = static_cast<long>(col0) + blockIdx.x; (col << c.pshift) < static_cast<long>(len) + n; col += gridDim.x) {
     const long p0 = col << c.pshift;                                            // the page's first position
     const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
@@ -112,11 +113,11 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
     uint4 raw[NX][NI][4];
     uint32_t cur[NI][E];  // V: words that get some new bytes, as they are
     float s_old[NX], amax[NX];
+    bool wild[NX];  // this lane holds a value that is not finite
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
       const int isv = BOTH ? x : blockIdx.y & 1;
       s_old[x] = (isv ? c.vs : c.ks)[blk];
-      amax[x] = 0.f;
       const char* src = static_cast<const char*>(isv ? p.v : p.k) + static_cast<long>(h) * c.D * Elt<DT>::kBytes;
       const uint8_t* page = c.vp + blk * c.P * c.D;
 #pragma unroll
@@ -145,16 +146,14 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
     }
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
+      MaxBits<DT> top;
 #pragma unroll
       for (int k = 0; k < NI; ++k)
+        if (wave0 + k * kBlock < items)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float f[E];
-          Elt<DT>::unpack(raw[x][k][r], f);
-#pragma unroll
-          for (int j = 0; j < E; ++j) amax[x] = fmaxf(amax[x], isfinite(f[j]) ? fabsf(f[j]) : 0.f);
-        }
-      amax[x] = wave_max(amax[x]);
+          for (int r = 0; r < 4; ++r) top.add(raw[x][k][r]);
+      wild[x] = top.wild();
+      amax[x] = wave_max(top.value());
     }
     __syncthreads();  // also: nobody reads the LDS of the page before any more
     if (tid % kWave == 0)
@@ -195,7 +194,8 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
             uint32_t w[E / 4];
             if (fresh) {
 #pragma unroll
-              for (int j = 0; j < E / 4; ++j) w[j] = kv_encode4<FMT>(&f[r][4 * j]);
+              for (int j = 0; j < E / 4; ++j)
+                w[j] = wild[x] ? kv_encode4<FMT>(&f[r][4 * j]) : kv_encode4_finite<FMT>(&f[r][4 * j]);
             } else {
               uint32_t had[E / 4];
 #pragma unroll
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
 #pragma unroll
           for (int j = 0; j < E; ++j) {
             const float y[4] = {f[0][j], f[1][j], f[2][j], f[3][j]};
-            uint32_t w = kv_encode4<FMT>(y);
+            uint32_t w = wild[x] ? kv_encode4<FMT>(y) : kv_encode4_finite<FMT>(y);
             if (fresh != ~0u) {
               w = (w & fresh) | (cur[k][j] & ~fresh);
               if (again) w = (w & ~again) | (kv_rescale4<FMT>(cur[k][j], ratio) & again);

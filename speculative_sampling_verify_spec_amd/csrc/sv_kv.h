@@ -127,6 +127,61 @@ __device__ inline uint32_t kv_encode4(const float* x) {
   }
 }
 
+// As kv_encode4 for values known to be finite and in the format's range.  int8:
+// adding 1.5 * 2^23 leaves the value, rounded to the nearest integer (ties to
+// even), in the low byte.
+template <int FMT>
+__device__ inline uint32_t kv_encode4_finite(const float* x) {
+  if constexpr (FMT == SPECV_E4M3) {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true));
+  } else {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(x[i] + 12582912.f);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400),
+                                 0x05040100);
+  }
+}
+
+// Running maximum of the finite magnitudes of 16-byte vectors, on their bits:
+// magnitudes order like integers, and adding the smallest exponent step makes
+// infinities and NaN negative.
+template <int DT> struct MaxBits;
+template <> struct MaxBits<SPECV_F32> {
+  int m = 0x00800000, any = 0;
+  __device__ void add(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = static_cast<int>((w[i] & 0x7fffffffu) + 0x00800000u);
+      any |= t;
+      m = max(m, t);
+    }
+  }
+  __device__ float value() const { return __int_as_float(m - 0x00800000); }
+  __device__ bool wild() const { return any < 0; }  // an infinity or a NaN was among them
+};
+template <> struct MaxBits<SPECV_BF16> {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  s16x2 m = {0x0080, 0x0080};
+  uint32_t any = 0;
+  __device__ void add(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const s16x2 t = __builtin_bit_cast(s16x2, w[i] & 0x7fff7fffu) + s16x2{0x0080, 0x0080};
+      any |= __builtin_bit_cast(uint32_t, t);
+      m = __builtin_elementwise_max(m, t);
+    }
+  }
+  __device__ float value() const {
+    const int top = max(static_cast<int>(m.x), static_cast<int>(m.y)) - 0x0080;
+    return __int_as_float(top << 16);
+  }
+  __device__ bool wild() const { return (any & 0x80008000u) != 0; }
+};
+
 // Four codes to the codes of ratio times their values.
 template <int FMT>
 __device__ inline uint32_t kv_rescale4(uint32_t w, float ratio) {
