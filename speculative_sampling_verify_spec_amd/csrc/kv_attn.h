@@ -167,7 +167,7 @@ constexpr bool k_half(int D, int MT) { return D == 256 || MT == 4; }
 // waves: the most that fit without spilling (the build refuses spills).
 constexpr int waves_per(int dt, int D, int MT) {
   if (D == 256) return dt == SPECV_F32 ? 1 : 2;
-  if (MT == 1) return D == 64 ? 4 : D == 128 && dt == SPECV_F32 ? 2 : 3;
+  if (MT == 1) return D == 64 ? 4 : dt == SPECV_F32 ? 2 : 3;
   if (MT == 2) return D == 64 && dt == SPECV_BF16 ? 3 : 2;
   return 2;
 }
@@ -188,12 +188,20 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
   if (seq >= static_cast<unsigned>(p.B)) return;
   const int h = static_cast<int>(pair - seq * c.H);
   const long b = seq;
+  const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int col = lane % 16, g = lane / 16;
+  // page of this lane's 16 tokens (group g) of a tile, -1: none
+  auto page_of = [&](int tile) {
+    const unsigned tok = static_cast<unsigned>(tile) * kTile + 16 * g;
+    return kv_page(c, b, tok >> c.pshift);
+  };
+  // the first pages are looked up beside the length, not after it
+  int tile = part * p.granule + w;
+  int pid = page_of(tile), pid_next = page_of(tile + kAWaves);
   const int len = kv_len(c, p.lengths, b);
   const int ntile = (len >> 6) + ((len & 63) != 0);
   const int parts = kv_parts(ntile, p.granule);
   if (part >= parts) return;
-  const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int col = lane % 16, g = lane / 16;
   const int nn = p.nodes ? min(max(p.nodes[b], 0), p.N) : p.N;
   const int rows = nn * p.G;           // queries that exist
   const int row0 = mblk * MT * 16;
@@ -203,8 +211,8 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
   // one buffer in LDS: the queries' fragments during the loop (where they
   // would take too many registers), the waves' sums at the join
   constexpr bool QL = q_in_lds(DT, D, MT);
-  constexpr int DC = D < 128 ? D : 128, kJoinRow = DC + 4;  // channels per round of the join, its padded row
-  constexpr int kJoinBytes = kAWaves * 16 * kJoinRow * 4, kQBytes = QL ? MT * NF * NP * kWave * 16 : 0;
+  constexpr int TV = (ND + kAWaves - 1) / kAWaves;  // blocks of 16 channels that a wave finishes
+  constexpr int kJoinBytes = kAWaves * (kAWaves - 1) * MT * TV * kWave * 16, kQBytes = QL ? MT * NF * NP * kWave * 16 : 0;
   __shared__ __align__(16) char lds[kJoinBytes > kQBytes ? kJoinBytes : kQBytes];
   bf16x8* const lq = reinterpret_cast<bf16x8*>(lds);
 
@@ -252,18 +260,12 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
   };
 
   // ---- cached tokens ----
-  const int tile0 = static_cast<int>(static_cast<long>(ntile) * part / parts);
-  const int tile1 = static_cast<int>(static_cast<long>(ntile) * (part + 1) / parts);
+  const int tile1 = min((part + 1) * p.granule, ntile);
   // K is kept a tile ahead, or half a tile where registers are short
   constexpr int KB = k_half(D, MT) ? 2 : 4;
   uint4 kraw[KB][NC], vraw[ND];
   uint2 ktail[KB];
   const size_t blkbytes = static_cast<size_t>(c.P) * D;
-  // page of this lane's 16 tokens (group g) of a tile, -1: none
-  auto page_of = [&](int tile) {
-    const unsigned tok = static_cast<unsigned>(tile) * kTile + 16 * g;
-    return kv_page(c, b, tok >> c.pshift);
-  };
   // this lane's row of K: token 16 (col / 4) + col % 4 of a tile
   auto k_rows = [&](int tile, int pid) -> const uint8_t* {
     const int grp = col >> 2;
@@ -289,12 +291,8 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     ks = c.ks[blk];
     vs = c.vs[blk];
   };
-  int tile = tile0 + w;
-  int pid = -1, pid_next = -1;
   const uint8_t* this_k = nullptr;
   if (tile < tile1) {
-    pid = page_of(tile);
-    pid_next = page_of(tile + kAWaves);
     this_k = k_rows(tile, pid);
 #pragma unroll
     for (int t = 0; t < KB; ++t) load_k(this_k, t);
@@ -540,70 +538,67 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     pid_next = page_of(tile + 2 * kAWaves);
   }
 
-  // ---- join the waves: 16 queries and at most 128 channels a round ----
-  __shared__ float sm[kAWaves][MT * 16], sl[kAWaves][MT * 16], sinv[MT * 16];
-  float(*const so)[16 * kJoinRow] = reinterpret_cast<float(*)[16 * kJoinRow]>(lds);
+  // ---- join the waves: each finishes TV blocks of channels, to which the
+  // others hand their sums, all scaled to the queries' largest maximum ----
+  // the lane's number again, so that nothing of it is kept across the loop
+  const int jl = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)), jc = jl % 16, jg = jl / 16;
+  __shared__ float sm[kAWaves][MT * 16], sl[kAWaves][MT * 16];
+  f32x4* const so = reinterpret_cast<f32x4*>(lds);
+  auto slot = [&](int to, int from, int mt, int t) {
+    return (((to * (kAWaves - 1) + from - (from > to)) * MT + mt) * TV + t) * kWave + jl;
+  };
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const float t = groups_sum(l[mt]);
-    if (g == 0) {
-      sm[w][mt * 16 + col] = m[mt];
-      sl[w][mt * 16 + col] = t;
+    l[mt] = groups_sum(l[mt]);
+    if (jg == 0) {
+      sm[w][mt * 16 + jc] = m[mt];
+      sl[w][mt * 16 + jc] = l[mt];
     }
+  }
+  lds_barrier();  // also: the queries' fragments are no longer read
+  float scale[MT], top[MT];  // what this wave's sums are multiplied by
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    top[mt] = sm[0][mt * 16 + jc];
+#pragma unroll
+    for (int k = 1; k < kAWaves; ++k) top[mt] = fmaxf(top[mt], sm[k][mt * 16 + jc]);
+    scale[mt] = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top[mt]);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      if (d / TV != w) so[slot(d / TV, w, mt, d % TV)] = o[mt][d] * scale[mt];
   }
   lds_barrier();
-  // a row's place in the output (and, with `part`, among the parts)
-  auto out_row = [&](int r) -> long {
-    const int n = node_of(r);
-    return (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
-  };
-  if (threadIdx.x < MT * 16) {  // the rows' statistics
-    const int q = threadIdx.x, r = row0 + q;
-    float mx = sm[0][q], lt = 0.f;
-#pragma unroll
-    for (int k = 1; k < kAWaves; ++k) mx = fmaxf(mx, sm[k][q]);
-#pragma unroll
-    for (int k = 0; k < kAWaves; ++k) lt += sm[k][q] == -INFINITY ? sl[k][q] : sl[k][q] * ex2(sm[k][q] - mx);
-    if (parts > 1) {
-      sinv[q] = 1.f;
-      if (r < p.N * p.G) p.part_ml[out_row(r) * p.splits + part] = make_float2(mx, lt);
-    } else {
-      const bool some = r < rows && !(lt == 0.f);  // a query that exists and sees something
-      sinv[q] = some ? 1.f / lt : 0.f;
-      if (r < p.N * p.G && p.lse) p.lse[out_row(r)] = kv_lse(mx, lt, some);
-    }
-  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    float top = sm[0][mt * 16 + col];
+    const int r = row0 + mt * 16 + jc;
+    if (r >= p.N * p.G) continue;
+    float lt = 0.f;
 #pragma unroll
-    for (int i = 1; i < kAWaves; ++i) top = fmaxf(top, sm[i][mt * 16 + col]);
-    const float f = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top);
+    for (int k = 0; k < kAWaves; ++k) {
+      const float mk = sm[k][mt * 16 + jc], lk = sl[k][mt * 16 + jc];
+      lt += mk == -INFINITY ? lk : lk * ex2(mk - top[mt]);  // 0, or NaN of a wave that saw only NaN
+    }
+    const int n = node_of(r);
+    const long row = (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
+    const bool some = r < rows && !(lt == 0.f);  // a query that exists and sees something
+    if (w == 0 && jg == 0) {
+      if (parts > 1) p.part_ml[row * p.splits + part] = make_float2(top[mt], lt);
+      else if (p.lse) p.lse[row] = kv_lse(top[mt], lt, some);
+    }
+    const float inv = 1.f / lt;
 #pragma unroll
-    for (int d0 = 0; d0 < D; d0 += DC) {
-      if (mt || d0) lds_barrier();
+    for (int d = 0; d < ND; ++d) {
+      if (d / TV != w) continue;
+      f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int d = 0; d < DC / 16; ++d)
-        *reinterpret_cast<f32x4*>(&so[w][col * kJoinRow + 16 * d + 4 * g]) = o[mt][d0 / 16 + d] * f;
-      lds_barrier();
+      for (int k = 0; k < kAWaves; ++k) acc += k == w ? o[mt][d] * scale[mt] : so[slot(d / TV, k == d / TV ? 0 : k, mt, d % TV)];
+      if (parts > 1) {
+        *reinterpret_cast<f32x4*>(p.part_o + (row * p.splits + part) * D + 16 * d + 4 * jg) = acc;
+      } else {
+        float y[4];
 #pragma unroll
-      for (int i0 = 0; i0 < 16 * (DC / 4); i0 += kABlock) {
-        const int i = i0 + threadIdx.x;
-        const int q = i / (DC / 4), d = i % (DC / 4) * 4;
-        const int r = row0 + mt * 16 + q;
-        if (i >= 16 * (DC / 4) || r >= p.N * p.G) continue;
-        f32x4 acc = *reinterpret_cast<const f32x4*>(&so[0][q * kJoinRow + d]);
-#pragma unroll
-        for (int k = 1; k < kAWaves; ++k) acc += *reinterpret_cast<const f32x4*>(&so[k][q * kJoinRow + d]);
-        if (parts > 1) {
-          *reinterpret_cast<f32x4*>(p.part_o + (out_row(r) * p.splits + part) * D + d0 + d) = acc;
-        } else {
-          const float inv = sinv[mt * 16 + q];
-          float y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = inv == 0.f ? 0.f : acc[e] * inv;  // 0 also where the sums are not finite
-          kv_store4<DT>(p.out, out_row(r) * D + d0 + d, y);
-        }
+        for (int e = 0; e < 4; ++e) y[e] = some ? acc[e] * inv : 0.f;
+        kv_store4<DT>(p.out, row * D + 16 * d + 4 * jg, y);
       }
     }
   }

@@ -67,7 +67,7 @@ struct KvAttn {
 // Largest number of 16-query blocks a workgroup's registers hold.
 constexpr int kv_max_mt(int dtype, int D) {
   if (D == 256) return 1;
-  return dtype == SPECV_F32 ? 2 : D == 128 ? 3 : 4;
+  return dtype == SPECV_F32 ? 2 : D == 64 ? 4 : 3;
 }
 
 // Parts of a sequence of `ntile` tiles.
