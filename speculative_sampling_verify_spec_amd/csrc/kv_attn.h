@@ -556,52 +556,67 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     }
   }
   lds_barrier();  // also: the queries' fragments are no longer read
-  float scale[MT], top[MT];  // what this wave's sums are multiplied by
+  float scale[MT], inv[MT];  // what this wave's sums, and the whole sums, are multiplied by
+  long orow[MT];             // the queries' output rows, -1: no such row
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    top[mt] = sm[0][mt * 16 + jc];
-#pragma unroll
-    for (int k = 1; k < kAWaves; ++k) top[mt] = fmaxf(top[mt], sm[k][mt * 16 + jc]);
-    scale[mt] = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top[mt]);
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-      if (d / TV != w) so[slot(d / TV, w, mt, d % TV)] = o[mt][d] * scale[mt];
-  }
-  lds_barrier();
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r = row0 + mt * 16 + jc;
-    if (r >= p.N * p.G) continue;
-    float lt = 0.f;
+    float mk[kAWaves], lk[kAWaves];
 #pragma unroll
     for (int k = 0; k < kAWaves; ++k) {
-      const float mk = sm[k][mt * 16 + jc], lk = sl[k][mt * 16 + jc];
-      lt += mk == -INFINITY ? lk : lk * ex2(mk - top[mt]);  // 0, or NaN of a wave that saw only NaN
+      mk[k] = sm[k][mt * 16 + jc];
+      lk[k] = sl[k][mt * 16 + jc];
     }
-    const int n = node_of(r);
-    const long row = (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G);
-    const bool some = r < rows && !(lt == 0.f);  // a query that exists and sees something
-    if (w == 0 && jg == 0) {
-      if (parts > 1) p.part_ml[row * p.splits + part] = make_float2(top[mt], lt);
-      else if (p.lse) p.lse[row] = kv_lse(top[mt], lt, some);
-    }
-    const float inv = 1.f / lt;
+    float top = mk[0], lt = 0.f;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      if (d / TV != w) continue;
+    for (int k = 1; k < kAWaves; ++k) top = fmaxf(top, mk[k]);
+#pragma unroll
+    for (int k = 0; k < kAWaves; ++k)
+      lt += mk[k] == -INFINITY ? lk[k] : lk[k] * ex2(mk[k] - top);  // 0, or NaN of a wave that saw only NaN
+    scale[mt] = m[mt] == -INFINITY ? 0.f : ex2(m[mt] - top);
+    const int r = row0 + mt * 16 + jc;
+    const int n = node_of(r);
+    const bool there = r < p.N * p.G;
+    orow[mt] = there ? (b * p.N + n) * p.Hq + h * p.G + (r - n * p.G) : -1;
+    const bool some = r < rows && !(lt == 0.f);  // a query that exists and sees something
+    inv[mt] = parts > 1 ? 1.f : some ? 1.f / lt : 0.f;
+    if (there && w == 0 && jg == 0) {
+      if (parts > 1) p.part_ml[orow[mt] * p.splits + part] = make_float2(top, lt);
+      else if (p.lse) p.lse[orow[mt]] = kv_lse(top, lt, some);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+    if (d / TV != w)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) so[slot(d / TV, w, mt, d % TV)] = o[mt][d] * scale[mt];
+  lds_barrier();
+  if (w * TV >= ND) return;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int t = 0; t < TV; ++t) {
+      f32x4 mine = o[mt][t];  // o[mt][w * TV + t]
+#pragma unroll
+      for (int k = 1; k < kAWaves; ++k)
+        if (k * TV + t < ND) mine = w == k ? o[mt][k * TV + t] : mine;
+      mine *= scale[mt];
       f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < kAWaves; ++k) acc += k == w ? o[mt][d] * scale[mt] : so[slot(d / TV, k == d / TV ? 0 : k, mt, d % TV)];
+      for (int k = 0; k < kAWaves; ++k) {  // in the waves' order
+        const f32x4 x = so[slot(w, k == w ? (w ? 0 : 1) : k, mt, t)];
+        acc += k == w ? mine : x;
+      }
+      if (orow[mt] < 0) continue;
+      const int d = 16 * (w * TV + t) + 4 * jg;
       if (parts > 1) {
-        *reinterpret_cast<f32x4*>(p.part_o + (row * p.splits + part) * D + 16 * d + 4 * jg) = acc;
+        *reinterpret_cast<f32x4*>(p.part_o + (orow[mt] * p.splits + part) * D + d) = acc;
       } else {
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = some ? acc[e] * inv : 0.f;
-        kv_store4<DT>(p.out, row * D + 16 * d + 4 * jg, y);
+        for (int e = 0; e < 4; ++e) y[e] = inv[mt] == 0.f ? 0.f : acc[e] * inv[mt];  // 0 whatever the sums are
+        kv_store4<DT>(p.out, orow[mt] * D + d, y);
       }
     }
-  }
 }
 
 template <int DT, int FMT, int D, int MT>
