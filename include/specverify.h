@@ -426,11 +426,12 @@ typedef struct {
  *   lengths     [B] int32 (device): tokens cached before, clamped to [0,
  *               max_pages * page_size]
  *   counts      [B] int32 (device) or NULL;  index [B][N] int32 (device) or NULL
- *   out_lengths [B] int32 or NULL: tokens cached after the call (must not be
- *               `lengths` itself)
+ *   out_lengths [B] int32 or NULL: tokens cached after the call (must not
+ *               overlap `lengths`)
  *   B <= 65535;  1 <= N <= SPECV_KV_MAX_APPEND
- * A page that the call writes may belong to one sequence only; pages that
- * are only read may be shared.  Needs no workspace; nothing synchronises.
+ * A page that the call writes may stand in one place of one sequence's table
+ * row only; pages that are only read may be shared.  Needs no workspace;
+ * nothing synchronises.
  */
 int spec_kv_append(const specv_kv_t* kv, const void* k, const void* v, int64_t row_stride, const int32_t* lengths,
                    const int32_t* counts, const int32_t* index, int B, int N, int32_t* out_lengths, int dtype,
@@ -468,14 +469,15 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   num_nodes   [B] int32 (device) or NULL: nodes of sequence b, clamped to
  *               [0, N] (NULL: N); the outputs of further nodes are 0 and -infinity
  *   parents     [B][N] int32 (device) or NULL: a chain; read when k_new is given
- *   scale       finite
+ *   scale       any sign; finite, also when multiplied by 1.5
  *   out         [B][N][Hq][dim] (dtype);  out_lse [B][N][Hq] float or NULL
  *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq a multiple of heads, at
  *               most SPECV_KV_MAX_GROUP times as many
  *   q, k_new, v_new and out 16-byte aligned
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
- * Sums and softmax statistics are in 32 bits.  The same call gives the same
- * bits.  Returns the SPECV_* codes of spec_verify; nothing synchronises.
+ * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights
+ * are rounded to bf16 for the product with the values.  The same call gives
+ * the same bits.  Returns the SPECV_* codes of spec_verify; nothing synchronises.
  */
 size_t spec_kv_attention_workspace_size(const specv_kv_t* kv, int B, int N, int Hq);
 

@@ -182,8 +182,8 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
         out_lengths = torch.empty_like(lengths)
     else:
         _check_ints(cache, (B,), "out_lengths", out_lengths)
-        if out_lengths.data_ptr() == lengths.data_ptr():
-            raise ValueError("out_lengths must not be lengths itself")
+        if abs(out_lengths.data_ptr() - lengths.data_ptr()) < 4 * B:
+            raise ValueError("out_lengths must not overlap lengths")
     _call(cache._device, load().spec_kv_append, _descriptor(cache, page_table.data_ptr(), width), k.data_ptr(),
           v.data_ptr(), row, lengths.data_ptr(), _ptr(counts), _ptr(index), B, N, out_lengths.data_ptr(),
           _dtype_code(k.dtype))

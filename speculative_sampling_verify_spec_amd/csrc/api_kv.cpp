@@ -60,8 +60,15 @@ struct KvPlan {
   int mt, mb, granule, splits;
 };
 
-constexpr long kTargetGroups = 512;   // workgroups to aim at: two on each of 256 CUs
-constexpr int kMinGranule = 16;       // tiles per part, four for each wave: a second launch costs more than they take
+// Workgroups to aim at: two on each of 256 CUs.  More parts mean more of the
+// parts' own cost, their queries and their sums: 2 x 5 positions over 131072
+// tokens take 123 us at 512, 155 at 2048; 64 x 6 over 301-2111 tokens 46 and
+// 67 us; 512 x 1 with heads of 256 240 and 268.
+constexpr long kTargetGroups = 512;
+// Tiles per part: four for each wave.  Fewer would need a second launch for
+// the join: 1 x 1 over 1000 tokens takes 12.4 us in one part of 16 tiles and
+// 11.5 us in four of 4, but 14.8 and 18.5 us a call with the launches' cost.
+constexpr int kMinGranule = 16;
 
 KvPlan kv_plan(const KvView& c, int B, int N, int Hq, int dtype) {
   KvPlan pl;
@@ -161,7 +168,7 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
   if (const int rc = check_cache(kv, &p.c)) return rc;
   if (!q || !lengths || !out || !k_new != !v_new) return SPECV_E_NULL;
   if (!valid_attention(p.c, B, N, Hq)) return SPECV_E_SHAPE;
-  if (!std::isfinite(scale)) return SPECV_E_SHAPE;
+  if (!std::isfinite(scale * 1.5f)) return SPECV_E_SHAPE;  // times log2(e), as the kernels use it
   if (const int rc = check_row(&q_stride, Hq, p.c.D, dtype)) return rc;
   if (k_new)
     if (const int rc = check_row(&kv_stride, p.c.H, p.c.D, dtype)) return rc;

@@ -229,6 +229,20 @@ def test_attention(gpu_lib, fmt, dtype, P, H, G, D, N, lens, tree):
             assert (got[b] == 0).all() and (lse[b] == -np.inf).all()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_attention_every_block_of_queries(gpu_lib, D, dtype, fmt):
+    """1 to 64 queries of a cached head: each kernel variant, full and partly
+    filled blocks of 16, and every block of 16 nodes."""
+    rng = np.random.default_rng(D)
+    P, lens = 32, [150, 0, 64]
+    c, table = kh.make_cache(rng, fmt, lens, P, 1, D)
+    for N in (2, 16, 17, 32, 41, 48, 64):
+        q, k, v = (_rand(rng, (3, N, 1, D), dtype) for _ in range(3))
+        _check_attention(gpu_lib, c, table, lens, q, k, v, D ** -0.5, dtype, _tree(rng, 3, N) if N % 2 else None)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_long_and_split(gpu_lib, dtype):
     """Few sequences with long caches next to short and empty ones: the
@@ -385,6 +399,126 @@ def test_other_stream_and_graph(gpu_lib):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
         assert all(torch.equal(a, b) for a, b in zip(eager, want))
+
+
+def test_graph_owns_its_workspace(gpu_lib):
+    """A captured call that allocates its own workspace, parts joined by a
+    second launch, two graphs replayed in turn."""
+    import torch
+    rng = np.random.default_rng(20)
+    lens, P, H, D, N = [5000, 3], 32, 1, 64, 2
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32(lens)
+    qs = [_rand(rng, (2, N, 4, D), "f32")[0] for _ in range(2)]
+    want = [gpu_lib.kv_attention(dev, tab, q, ln) for q in qs]
+    assert gpu_lib.kv_attention_workspace_size(dev, 2, N, 4, table.shape[1]) > 256
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gpu_lib.kv_attention(dev, tab, q, ln))
+        graphs.append(g)
+    for _ in range(3):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            assert torch.equal(gpu_lib.kv_attention(dev, tab, qs[0], ln), want[0])
+            torch.cuda.synchronize()
+            assert torch.equal(o, w)
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Two calls in flight together on two streams, each with its own workspace."""
+    import torch
+    rng = np.random.default_rng(21)
+    lens, P, H, D, N = [9000, 2000, 0], 64, 2, 128, 4
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32(lens)
+    qs = [_rand(rng, (3, N, 8, D), "bf16")[0] for _ in range(2)]
+    want = [gpu_lib.kv_attention(dev, tab, q, ln) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(gpu_lib.kv_attention(dev, tab, qs[i], ln))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_largest_batch(gpu_lib):
+    """65535 sequences: the first and the last give what small batches give."""
+    import torch
+    B, P, H, D = 65535, 16, 1, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    cache = gpu_lib.KVCache.empty(B, P, H, D, dtype=torch.int8)
+    for t in (cache.k_pages, cache.v_pages):
+        t.zero_()
+    cache.k_scales.fill_(1), cache.v_scales.fill_(1)
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    lens = (torch.arange(B, device="cuda") % 14).int()
+    k, v, q = (torch.randn((B, 2, h, D), generator=g, device="cuda") for h in (H, H, 2))
+    after = gpu_lib.kv_append(cache, table, k, v, lens)
+    assert torch.equal(after, lens + 2)
+    rk, rv = gpu_lib.kv_read(cache, table, after, P, dtype=torch.float32)
+    out = gpu_lib.kv_attention(cache, table, q, after, k, v)
+    for s in (slice(0, 50), slice(B - 50, B)):
+        a, b = gpu_lib.kv_read(cache, table[s].contiguous(), after[s].contiguous(), P, dtype=torch.float32)
+        assert torch.equal(a, rk[s]) and torch.equal(b, rv[s])
+        o = gpu_lib.kv_attention(cache, table[s].contiguous(), q[s].contiguous(), after[s].contiguous(),
+                                 k[s].contiguous(), v[s].contiguous())
+        assert torch.equal(o, out[s])
+        n = lens[s].long()[:, None] + torch.arange(2, device="cuda")
+        got = rk[s].gather(1, n[:, :, None, None].expand(-1, -1, H, D))
+        # an int8 code is off by half a step of its block's scale: a begun block keeps its scale of 1 here, since
+        # 127 exceeds every value, and a fresh one has the smallest power of two from its largest value over 127 up
+        step = cache.k_scales[s][:, None, :, None]
+        assert ((got - k[s]).abs() <= step / 2).all()
+        top = k[s].abs().amax((1, 2, 3))
+        assert (torch.where(lens[s] > 0, cache.k_scales[s, 0] == 1,
+                            (top <= 127 * cache.k_scales[s, 0]) & (top > 63.5 * cache.k_scales[s, 0]))).all()
+
+
+def test_pool_past_32_bits(gpu_lib):
+    """Pages more than 4 GiB into the pool hold and give what pages at its start do."""
+    import torch
+    rng = np.random.default_rng(22)
+    P, H, D, N = 128, 8, 256, 300
+    pages = (5 << 30) // (P * H * D)
+    big = gpu_lib.KVCache.empty(pages, P, H, D)
+    small = gpu_lib.KVCache.empty(3, P, H, D)
+    (k, _), (v, _), (q, _) = (_rand(rng, (1, N, h, D), "bf16") for h in (H, H, 16))
+    res = []
+    for cache, table in ((big, [[pages - 1, pages - 3, pages - 2]]), (small, [[0, 2, 1]])):
+        tab = _i32(table)
+        n = gpu_lib.kv_append(cache, tab, k, v, _i32([0]))
+        res.append((n,) + gpu_lib.kv_read(cache, tab, n, N) +
+                   (gpu_lib.kv_attention(cache, tab, q[:, :4].contiguous(), n, k[:, :4].contiguous(),
+                                         v[:, :4].contiguous()),))
+    assert int(res[0][0]) == N and all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_misaligned_rows_are_refused(gpu_lib):
+    import torch
+    rng = np.random.default_rng(23)
+    c, table = kh.make_cache(rng, "int8", [4], 16, 1, 64, extra=4)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32([4])
+    flat = torch.zeros(2 * 64 + 4, device="cuda", dtype=torch.bfloat16)
+    x = flat[4:].view(1, 2, 1, 64)
+    for call in (lambda: gpu_lib.kv_append(dev, tab, x, x, ln), lambda: gpu_lib.kv_attention(dev, tab, x, ln, x, x)):
+        with pytest.raises(gpu_lib.SpecVerifyError) as e:
+            call()
+        assert e.value.code == -6
+    both = _i32([4, 0])
+    with pytest.raises(ValueError):
+        gpu_lib.kv_append(dev, tab, x.clone(), x.clone(), ln, out_lengths=ln)
+    with pytest.raises(ValueError):
+        gpu_lib.kv_append(dev, torch.cat((tab, tab)), torch.zeros(2, 1, 1, 64, device="cuda"),
+                          torch.zeros(2, 1, 1, 64, device="cuda"), _i32([0, 0, 0])[:2], out_lengths=both.new_zeros(2)[1:])
 
 
 def test_verify_round_with_trees(gpu_lib):

@@ -102,7 +102,7 @@ def test_read_refusals(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=7), -3), (dict(q=None), -1), (dict(lengths=None), -1), (dict(out=None), -1), (dict(k=None), -1),
     (dict(v=None), -1), (dict(B=0), -2), (dict(B=65536), -2), (dict(N=0), -2), (dict(N=65), -2), (dict(Hq=0), -2),
-    (dict(Hq=12), -2), (dict(Hq=1 << 15), -2), (dict(Hq=8 * 1025), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2),
+    (dict(Hq=12), -2), (dict(Hq=1 << 15), -2), (dict(Hq=8 * 1025), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2), (dict(scale=-3.2e38), -2),
     (dict(qs=100), -2), (dict(qs=32 * 128 + 4), -6), (dict(ks=8 * 128 + 1), -6), (dict(q=BASE + 2), -6),
     (dict(k=BASE + 8), -6), (dict(v=BASE + 8), -6), (dict(out=BASE + 8), -6), (dict(ws=None), -5),
     (dict(ws=BASE + 16), -5), (dict(wsb=8), -5)])
@@ -173,6 +173,14 @@ def test_token_strides():
                 x[:1, :1].expand(3, 1, 10, 64)):
         with pytest.raises(ValueError):
             f("x", bad, bad.shape[2], bad.shape[3])
+
+
+def test_build_finds_spills():
+    from speculative_sampling_verify_spec_amd.build import _spills
+    line = "k.hip:3:1: remark: {} [-Rpass-analysis=kernel-resource-usage]\n"
+    text = line.format("Function Name: _Za") + line.format("    VGPRs: 12") + line.format("    VGPRs Spill: 0") + \
+        line.format("Function Name: _Zb") + line.format("    SGPRs Spill: 4") + line.format("    VGPRs Spill: 7")
+    assert _spills(text) == ["_Zb: 7 VGPRs"] and _spills("") == []
 
 
 STUBS = """
