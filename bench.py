@@ -346,6 +346,68 @@ def tree_bench(args):
     print(json.dumps(line), flush=True)
 
 
+def cache_bench(args):
+    """A verify round's work on the 8-bit cache in one layer: the attention of
+    B sequences' N nodes over their cached tokens, and the append of the
+    accepted paths (32 query heads, 8 cached heads of 128, pages of 64)."""
+    import numpy as np
+    import torch
+
+    import speculative_sampling_verify_spec_amd as sv
+    B, N, Hq, H, D, P = 256, 9, 32, 8, 128, 64
+    rng = np.random.default_rng(0)
+    lens = rng.integers(1001, 4098, B)
+    need = (lens + N + P - 1) // P
+    table = np.full((B, int(need.max())), -1, np.int32)
+    perm = rng.permutation(int(need.sum())).astype(np.int32)
+    for b, e in enumerate(np.cumsum(need)):
+        table[b, :need[b]] = perm[e - need[b]:e]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    cache = sv.KVCache.empty(len(perm), P, H, D)
+    tab = torch.from_numpy(table).cuda()
+    ln = torch.from_numpy(lens.astype(np.int32)).cuda()
+    fill = torch.zeros_like(ln)
+    for t in range(0, int(lens.max()), 512):  # the cached tokens, written as a prompt is
+        k, v = (torch.randn((B, 512, H, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+        fill = sv.kv_append(cache, tab, k, v, fill, counts=(ln - t).clamp(0, 512))
+    q = torch.randn((B, N, Hq, D), generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn((B, N, H, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    counts = torch.from_numpy(rng.integers(1, N + 1, B).astype(np.int32)).cuda()
+    after = torch.empty_like(ln)
+    ws = torch.empty(sv.kv_attention_workspace_size(cache, B, N, Hq, table.shape[1]), dtype=torch.uint8, device="cuda")
+
+    def attend():
+        sv.kv_attention(cache, tab, q, ln, k, v, workspace=ws)
+
+    def append():
+        sv.kv_append(cache, tab, k, v, ln, counts=counts, out_lengths=after)
+
+    def step():
+        attend()
+        append()
+    ramp_steps, _, _ = warm_up(step, args.warmup, args.ramp_seconds)
+    us = {}
+    for name, f in (("step", step), ("attention", attend), ("append", append)):
+        t0 = time.perf_counter()
+        for _ in range(args.steps):
+            f()
+        torch.cuda.synchronize()
+        us[name] = (time.perf_counter() - t0) / args.steps * 1e6
+    # what the attention cannot do without: cached codes and scales once, q, k, v and the output
+    read = int(lens.sum()) * 2 * H * D + int(need.sum()) * 8 * H + B * N * 2 * D * (2 * Hq + 2 * H)
+    line = {"metric": "positions/s + HBM GB/s (% peak), 8-bit cache attention and append of one layer",
+            "value": B * N / us["step"] * 1e6, "unit": "positions/s", "n_gpus": 1, "steps": args.steps,
+            "warmup": args.warmup, "ramp_steps": ramp_steps, "ms_per_step": us["step"] / 1e3,
+            "attention_us": us["attention"], "append_us": us["append"], "higher_is_better": True, "scaling": "weak",
+            "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {"workload": f"cache-e4m3: {B} sequences of {N} positions over 1001-4097 cached tokens",
+                       "B": B, "N": N, "query_heads": Hq, "heads": H, "dim": D, "page_size": P},
+            "hbm_gbps": read / us["attention"] / 1e3, "hbm_frac_of_peak": read / us["attention"] / 1e3 / PEAK_HBM_GBS,
+            "bytes_per_attention": read, "roofline": None, "cpu_baseline": None}
+    print(json.dumps(line), flush=True)
+
+
 def ngram_bench(args):
     """Prompt-lookup proposals for B histories (every history token read once)."""
     import numpy as np
@@ -512,6 +574,8 @@ def main():
     ap.add_argument("--copy-calibration", type=int, default=0, metavar="BYTES")
     ap.add_argument("--tree", action="store_true",
                     help="greedy token-tree verification: 128 trees of 32 nodes, V=128256 bf16")
+    ap.add_argument("--cache", action="store_true",
+                    help="8-bit cache: attention of 256 x 9 positions over 1001-4097 tokens, append of accepted paths")
     ap.add_argument("--ngram", action="store_true",
                     help="prompt-lookup proposer: 1024 histories of up to 16384 tokens, n = 1..4, K = 5")
     ap.add_argument("--ngram-map", action="store_true",
@@ -535,6 +599,9 @@ def main():
     import workloads
 
     sv.load()
+    if args.cache:
+        cache_bench(args)
+        return
     if args.tree:
         tree_bench(args)
         return

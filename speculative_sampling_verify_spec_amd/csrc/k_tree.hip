@@ -17,6 +17,7 @@
 // A node whose parent is not in [0, v) has an empty chain: it sees only
 // itself, has depth 0 and is never accepted (its edge test fails).
 #include "sv_device.h"
+#include "sv_tree.h"
 #include "specverify.h"
 
 namespace sv {

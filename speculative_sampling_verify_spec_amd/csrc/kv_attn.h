@@ -32,6 +32,7 @@
 
 #include "sv_device.h"
 #include "sv_kv.h"
+#include "sv_tree.h"
 
 namespace sv {
 
