@@ -381,7 +381,7 @@ int spec_ngram_map_update(void* tables, int capacity, const int32_t* history, co
  * one head has one scale for K and one for V; an entry stands for
  * code * scale.  spec_kv_append writes scales that are powers of two, the
  * smallest that brings the block's largest magnitude into the format's
- * range; spec_kv_read and spec_kv_attention take any finite positive scale.
+ * range; spec_kv_read and spec_kv_attention take any finite scale >= 0.
  */
 typedef enum {
   SPECV_E4M3 = 0, /* 8-bit float, 4 exponent and 3 fraction bits, no infinities, largest value 448 */
@@ -476,8 +476,9 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   q, k_new, v_new and out 16-byte aligned
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
  * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights
- * are rounded to bf16 for the product with the values.  The same call gives
- * the same bits.  Returns the SPECV_* codes of spec_verify; nothing synchronises.
+ * are rounded to bf16 for the product with the values, and blocks whose V
+ * scale is below 2^-86 count as zeros.  Values are to stay below 2^100.  The
+ * same call gives the same bits.  Returns the SPECV_* codes of spec_verify; nothing synchronises.
  */
 size_t spec_kv_attention_workspace_size(const specv_kv_t* kv, int B, int N, int Hq);
 

@@ -108,6 +108,24 @@ def test_append_special_values(gpu_lib, fmt):
     _same_cache(kh.to_host(dev, fmt), c)
 
 
+def test_append_long_index(gpu_lib):
+    """An index of hundreds of tokens over many pages: any order, repeats, an
+    end past the first 256, a missing page in the middle."""
+    rng = np.random.default_rng(6)
+    B, N, P, H, D = 4, 600, 16, 1, 64
+    lens = [0, 7, 100, 31]
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D, extra=N)
+    table[2, 30] = -1
+    index = rng.integers(0, N, (B, N))
+    index[0, 431], index[1, 599], index[3, 0] = -1, N, -5
+    (k, k64), (v, v64) = _rand(rng, (B, N, H, D), "bf16"), _rand(rng, (B, N, H, D), "bf16")
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k, v, _i32(lens), index=_i32(index))
+    want = okv.append(c, table, k64, v64, lens, index=index)
+    assert got.cpu().numpy().tolist() == want.tolist() == [431, 606, 480, 31]
+    _same_cache(kh.to_host(dev, "int8"), c)
+
+
 def test_append_without_pages(gpu_lib):
     """A missing or foreign page ends the tokens there; a full table, a
     negative and a too large length write nothing out of place."""
@@ -341,6 +359,29 @@ def test_attention_arbitrary_scales_and_shared_pages(gpu_lib):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_attention_blocks_of_zeros(gpu_lib, fmt, dtype):
+    """Blocks of zeros, which have the smallest scale, keep their weight in
+    the sums: next to other blocks, alone, as keys and as values; so do scales
+    of 0 and tiny ones."""
+    rng = np.random.default_rng(24)
+    lens, P, H, D, N = [300, 200, 64, 130], 32, 2, 64, 3
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D)
+    zero = [table[0, 1], table[0, 4], table[0, 9], *table[1, :7], table[2, 0]]
+    for name in ("k", "v"):
+        c[name + "_pages"][zero] = 0
+        c[name + "_scales"][zero] = 2.0 ** -126
+    c["v_scales"][table[2, 1]] = 0.0
+    c["k_scales"][table[3, 0]] = 0.0
+    c["v_scales"][table[3, 2]] = 2.0 ** -80
+    q, k, v = (_rand(rng, (4, N, h, D), dtype) for h in (8, H, H))
+    _check_attention(gpu_lib, c, table, lens, q, k, v, D ** -0.5, dtype)
+    out, lse = _check_attention(gpu_lib, c, table, lens, q, (None, None), (None, None), D ** -0.5, dtype)
+    assert (out[1] == 0).all()
+    np.testing.assert_allclose(lse[1].cpu().numpy(), np.log(200.0), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_fused_rows_and_repeatability(gpu_lib, dtype):
     """q, k and v as slices of one projection's rows give the bits of
     contiguous copies, twice."""
@@ -500,6 +541,23 @@ def test_pool_past_32_bits(gpu_lib):
                    (gpu_lib.kv_attention(cache, tab, q[:, :4].contiguous(), n, k[:, :4].contiguous(),
                                          v[:, :4].contiguous()),))
     assert int(res[0][0]) == N and all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.mark.parametrize("G", [1000, 1024])
+def test_largest_group_of_heads(gpu_lib, G):
+    """Up to 65536 queries share a cached head: each gives what it gives alone."""
+    import torch
+    rng = np.random.default_rng(25)
+    P, D, N = 32, 64, 64
+    c, table = kh.make_cache(rng, "e4m3", [100], P, 1, D)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32([100])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    q = torch.randn((1, N, G, D), generator=g, device="cuda").bfloat16()
+    (k, _), (v, _) = _rand(rng, (1, N, 1, D), "bf16"), _rand(rng, (1, N, 1, D), "bf16")
+    out = gpu_lib.kv_attention(dev, tab, q, ln, k, v)
+    for h in (0, G // 2, G - 8):
+        assert torch.equal(gpu_lib.kv_attention(dev, tab, q[:, :, h:h + 8], ln, k, v), out[:, :, h:h + 8])
 
 
 def test_misaligned_rows_are_refused(gpu_lib):
