@@ -14,6 +14,16 @@ KV_PAGE_SIZES = (16, 32, 64, 128)
 KV_DIMS = (64, 96, 128, 256)
 
 
+torch = None  # bound by the first cache: the package imports without it, and every call here has a cache
+
+
+def _bind_torch() -> None:
+    global torch
+    if torch is None:
+        import torch as t
+        torch = t
+
+
 class KVCache:
     """The pages and scales of an 8-bit cache.
 
@@ -25,7 +35,7 @@ class KVCache:
     __slots__ = ("_k", "_v", "_ks", "_vs", "_device", "_type")
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales):
-        import torch
+        _bind_torch()
         if k_pages.dim() != 4:
             raise ValueError("k_pages must be [num_pages, heads, page_size, dim]")
         n, h, p, d = k_pages.shape
@@ -49,7 +59,7 @@ class KVCache:
     @classmethod
     def empty(cls, num_pages: int, page_size: int, heads: int, dim: int, dtype=None, device="cuda") -> "KVCache":
         """A cache of num_pages pages (dtype: torch.float8_e4m3fn, the default, or torch.int8)."""
-        import torch
+        _bind_torch()
         dtype = torch.float8_e4m3fn if dtype is None else dtype
         return cls(torch.empty((num_pages, heads, page_size, dim), dtype=dtype, device=device),
                    torch.empty((num_pages, heads, dim, page_size), dtype=dtype, device=device),
@@ -98,26 +108,23 @@ def _descriptor(cache: KVCache, table_ptr: int, max_pages: int) -> bytes:
 
 
 def _dtype_code(dtype) -> int:
-    import torch
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return SPECV_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return SPECV_F32
     raise TypeError(f"queries, keys and values must be torch.bfloat16 or torch.float32, got {dtype}")
 
 
 def _check_table(cache: KVCache, page_table) -> None:
-    import torch
     if cache._device.type != "cuda":
         raise ValueError("the cache must be on a GPU")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.device != cache._device or \
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != cache._device or \
             not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
 
 
 def _check_ints(cache: KVCache, shape, name: str, t) -> None:
-    import torch
-    if t.dtype != torch.int32 or t.shape != shape or t.device != cache._device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != cache._device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor on the cache's device")
 
 
@@ -125,7 +132,7 @@ def _token_stride(name: str, t, heads: int, dim: int) -> int:
     """Elements between the token rows of t [B, N, heads, dim]: heads and
     channels contiguous, one stride for all tokens (a slice of a fused
     projection's rows will do)."""
-    B, N = t.shape[:2]
+    B, N, _, _ = t.shape
     sb, sn, sh, sd = t.stride()
     if sd != 1 or (heads > 1 and sh != dim):
         raise ValueError(f"{name}: heads and channels must be contiguous")
@@ -143,7 +150,6 @@ def _check_rows(cache: KVCache, name: str, t, B: int, N: int, heads: int) -> int
 
 def _call(device, fn, *args) -> None:
     """One library call on the device's current stream (the last argument)."""
-    import torch
     st = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream(device), without its object
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
@@ -164,7 +170,6 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
     the first entry outside [0, N): the path of verify_tree_greedy), int32.
     Returns the tokens cached after the call, [B] int32 (out_lengths if given;
     lengths itself is left as it is, so every layer can pass it)."""
-    import torch
     _check_table(cache, page_table)
     B, width = page_table.shape
     if k.dim() != 4:
@@ -195,7 +200,6 @@ def kv_read(cache: KVCache, page_table, lengths, T: int, *, starts=None, dtype=N
     starts[b] + T - 1 (from 0 without starts) of every sequence.  Returns (k,
     v), each [B, T, heads, dim] in dtype (torch.bfloat16, the default, or
     torch.float32), 0 at and behind lengths[b]."""
-    import torch
     _check_table(cache, page_table)
     B, width = page_table.shape
     if T < 1:
@@ -229,7 +233,6 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
     parents [B, N] the nodes' tree (None: a chain), num_nodes [B] the nodes of
     each sequence, int32; scale defaults to dim ** -0.5.  Returns out [B, N,
     Hq, dim] and, when asked, lse [B, N, Hq] float32."""
-    import torch
     _check_table(cache, page_table)
     B, width = page_table.shape
     if q.dim() != 4:
