@@ -11,6 +11,8 @@ namespace {
 // sums meet in LDS in their order, so the same call gives the same bits.
 // WIDE: a workgroup per row, GR = 1024 / D; else GR = 1 and several rows per
 // workgroup, for few parts.  Rows of sequences in one part are already written.
+// Bound by the latency of length, maxima and sums in turn, all from the caches
+// the attention just wrote: 640 rows of up to 121 parts take 6 us.
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kBlock) void k_kv_join(KvAttn p) {
   __shared__ float4 sy[kBlock];
@@ -70,7 +72,10 @@ __global__ __launch_bounds__(kBlock) void k_kv_join(KvAttn p) {
   if (d == 0 && p.lse) p.lse[row] = kv_lse(top, l, some);
 }
 
-// More parts than this: a workgroup per row.
+// More parts than this: a workgroup per row.  A whole call of 2 x 5 positions
+// (G = 4, D = 128) over 20000 tokens, 20 parts, takes 29.1 us wide and 31.4
+// with a row's parts in series (121 parts: the join alone 6 us and 74); 8 x 5 over
+// 8000, 8 parts, 33.7 either way; 16 x 5 over 8000, 4 parts, 54.0 and 52.1.
 constexpr int kWideParts = 8;
 
 template <int DT>

@@ -169,8 +169,11 @@ __device__ inline float groups_sum(float v) {
 constexpr int kAWaves = 4, kABlock = kAWaves * kWave;  // waves and threads per workgroup
 constexpr int kTile = 64;                       // cached tokens a wave takes at a time
 
-// The queries' fragments stay in registers if they take fewer than 16.
-constexpr bool q_in_lds(int dt, int D, int MT) { return MT * (dt == SPECV_F32 ? 3 : 1) * D / 8 >= 16; }
+// The queries' fragments stay in registers if they take at most 16: 2 x 8
+// positions (G = 4, D = 64) over 900 tokens take 12.7 us, through LDS 13.2; 2 x 2
+// with D = 96 11.7 and 12.1; long caches differ by 1 %.  24 would spill
+// (32-bit, D = 64: 128 registers for four waves; 36.0 us against 37.8).
+constexpr bool q_in_lds(int dt, int D, int MT) { return MT * (dt == SPECV_F32 ? 3 : 1) * D / 8 > 16; }
 
 // Waves a SIMD should hold, which bounds the registers of each to 512 /
 // waves: the most that fit without spilling (the build refuses spills).

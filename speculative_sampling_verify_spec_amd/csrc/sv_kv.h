@@ -64,7 +64,10 @@ struct KvAttn {
   float2* part_ml;        // [B][N][Hq][splits] (maximum, sum of weights), scores in log2
 };
 
-// Largest number of 16-query blocks a workgroup's registers hold.
+// Largest number of 16-query blocks a workgroup's registers hold at two waves
+// a SIMD (32-bit, D = 256: one).  A fourth block at D = 128 leaves one wave:
+// 128 trees of 32 nodes (128 queries a cached head) took 395 us so, against 267
+// in workgroups of 48, though those read the cache three times and not twice.
 constexpr int kv_max_mt(int dtype, int D) {
   if (D == 256) return 1;
   return dtype == SPECV_F32 ? 2 : D == 64 ? 4 : 3;
