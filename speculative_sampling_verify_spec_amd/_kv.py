@@ -32,7 +32,7 @@ class KVCache:
     k_scales and v_scales [num_pages, heads] float32, all contiguous on one
     device.  KVCache.empty() allocates them."""
 
-    __slots__ = ("_k", "_v", "_ks", "_vs", "_device", "_type")
+    __slots__ = ("_k", "_v", "_ks", "_vs", "_device", "_type", "_pages", "_heads", "_page", "_dim")
 
     def __init__(self, k_pages, v_pages, k_scales, v_scales):
         _bind_torch()
@@ -54,6 +54,7 @@ class KVCache:
                 raise ValueError("pages and scales must be contiguous tensors on the same device")
         self._k, self._v, self._ks, self._vs = k_pages, v_pages, k_scales, v_scales
         self._device = k_pages.device
+        self._pages, self._heads, self._page, self._dim = n, h, p, d
         self._type = SPECV_I8 if k_pages.dtype == torch.int8 else SPECV_E4M3
 
     @classmethod
@@ -88,23 +89,23 @@ class KVCache:
 
     @property
     def page_size(self) -> int:
-        return self._k.shape[2]
+        return self._page
 
     @property
     def heads(self) -> int:
-        return self._k.shape[1]
+        return self._heads
 
     @property
     def dim(self) -> int:
-        return self._k.shape[3]
+        return self._dim
 
 
 _pack = struct.Struct("@5P6i").pack  # specv_kv_t, read by the library during the call
 
 
 def _descriptor(cache: KVCache, table_ptr: int, max_pages: int) -> bytes:
-    n, h, p, d = cache._k.shape
-    return _pack(cache._k.data_ptr(), cache._v.data_ptr(), cache._ks.data_ptr(), cache._vs.data_ptr(), table_ptr, n, max_pages, p, h, d, cache._type)
+    return _pack(cache._k.data_ptr(), cache._v.data_ptr(), cache._ks.data_ptr(), cache._vs.data_ptr(), table_ptr,
+                 cache._pages, max_pages, cache._page, cache._heads, cache._dim, cache._type)
 
 
 def _dtype_code(dtype) -> int:
@@ -132,6 +133,8 @@ def _token_stride(name: str, t, heads: int, dim: int) -> int:
     """Elements between the token rows of t [B, N, heads, dim]: heads and
     channels contiguous, one stride for all tokens (a slice of a fused
     projection's rows will do)."""
+    if t.is_contiguous():
+        return heads * dim
     B, N, _, _ = t.shape
     sb, sn, sh, sd = t.stride()
     if sd != 1 or (heads > 1 and sh != dim):
@@ -143,15 +146,15 @@ def _token_stride(name: str, t, heads: int, dim: int) -> int:
 
 
 def _check_rows(cache: KVCache, name: str, t, B: int, N: int, heads: int) -> int:
-    if t.shape != (B, N, heads, cache._k.shape[3]) or t.device != cache._device:
-        raise ValueError(f"{name} must be [{B}, {N}, {heads}, {cache.dim}] on the cache's device")
-    return _token_stride(name, t, heads, t.shape[3])
+    if t.shape != (B, N, heads, cache._dim) or t.device != cache._device:
+        raise ValueError(f"{name} must be [{B}, {N}, {heads}, {cache._dim}] on the cache's device")
+    return _token_stride(name, t, heads, cache._dim)
 
 
 def _call(device, fn, *args) -> None:
     """One library call on the device's current stream (the last argument)."""
     st = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream(device), without its object
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             rc = fn(*args, st)
     else:
@@ -174,7 +177,7 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
     B, width = page_table.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, N, heads, dim]")
-    N, heads = k.shape[1], cache._k.shape[1]
+    N, heads = k.shape[1], cache._heads
     row = _check_rows(cache, "k", k, B, N, heads)
     if _check_rows(cache, "v", v, B, N, heads) != row or v.dtype != k.dtype:
         raise ValueError("k and v must have the same dtype and strides")
@@ -207,10 +210,9 @@ def kv_read(cache: KVCache, page_table, lengths, T: int, *, starts=None, dtype=N
     _check_ints(cache, (B,), "lengths", lengths)
     if starts is not None:
         _check_ints(cache, (B,), "starts", starts)
-    _, heads, _, dim = cache._k.shape
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _dtype_code(dtype)
-    k = torch.empty((B, T, heads, dim), dtype=dtype, device=cache._device)
+    k = torch.empty((B, T, cache._heads, cache._dim), dtype=dtype, device=cache._device)
     v = torch.empty_like(k)
     _call(cache._device, load().spec_kv_read, _descriptor(cache, page_table.data_ptr(), width), _ptr(starts),
           lengths.data_ptr(), B, T, k.data_ptr(), v.data_ptr(), code)
@@ -243,7 +245,7 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
         raise ValueError("k_new and v_new go together")
     kv_row = 0
     if k_new is not None:
-        heads = cache._k.shape[1]
+        heads = cache._heads
         kv_row = _check_rows(cache, "k_new", k_new, B, N, heads)
         if _check_rows(cache, "v_new", v_new, B, N, heads) != kv_row or k_new.dtype != q.dtype or \
                 v_new.dtype != q.dtype:
