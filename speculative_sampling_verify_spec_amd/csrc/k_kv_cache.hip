@@ -24,9 +24,10 @@
 // 128) moves 201 MB in 44 us, 4.6 TB/s, and reading 64 x 1500-4096 back as
 // bf16 1.45 GB in 293 us, 4.9 TB/s; a large copy reaches 4.75 TB/s.  Short
 // appends are a chain of dependent loads (length; table and index; rows; the
-// words shared with older tokens): 256 paths of up to 32 nodes take 20 us and
-// one token of 8 sequences 6 us.  A workgroup of one wave per block was slower
-// there (paths 89 us with their read, against 70), as its rows queue up.
+// words shared with older tokens): 256 paths of up to 32 nodes take 20 us, 256 x
+// 9 tokens 10 us and one token of 8 sequences 6 us.
+#include <algorithm>
+
 #include "sv_device.h"
 #include "sv_kv.h"
 
@@ -34,13 +35,15 @@ namespace sv {
 
 namespace {
 
-__device__ inline int block_min_i32(int v, int* lds /* >= kWaves */) {
+// The smallest v of a workgroup of NW waves.
+template <int NW>
+__device__ inline int block_min_i32(int v, int* lds /* >= NW */) {
   v = wave_min_i32(v);
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
   int t = lds[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) t = min(t, lds[i]);
+  for (int i = 1; i < NW; ++i) t = min(t, lds[i]);
   return t;
 }
 
@@ -52,19 +55,22 @@ __device__ inline void item_of(int isv, unsigned i, int a0, unsigned na, unsigne
   v = static_cast<int>(isv ? q : r);
 }
 
-// A workgroup takes K and V (BOTH) or one of them of one head of one
-// sequence, in every gridDim.x-th page that the call may touch.  NI items per
+// A workgroup of NW waves takes K and V (BOTH) or one of them of one head of
+// one sequence, in every gridDim.x-th page that the call may touch.  NI items per
 // thread of each; their values stay in registers between the search for the
 // largest magnitude and the quantisation.
-template <int DT, int FMT, int NI, bool BOTH>
-__global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
-  constexpr int E = Elt<DT>::kPerVec, NX = BOTH ? 2 : 1;
+//
+// Five waves a SIMD with one item a thread: 95 registers; left to itself the
+// compiler takes 120 (256 x 32 tokens 23.2 us against 24.5), six waves spill.
+template <int DT, int FMT, int NI, bool BOTH, int NW>
+__global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvAppend p) {
+  constexpr int E = Elt<DT>::kPerVec, NX = BOTH ? 2 : 1, kThreads = NW * kWave;
   const KvView& c = p.c;
   const int h = BOTH ? blockIdx.y : blockIdx.y >> 1;
   const long b = blockIdx.z;
   const int tid = threadIdx.x;
-  __shared__ float ldsf[NX][kWaves];
-  __shared__ int ldsi[kWaves];
+  __shared__ float ldsf[NX][NW];
+  __shared__ int ldsi[NW];
 
   const int len = kv_len(c, p.lengths, b);
   const int room = (c.width << c.pshift) - len;
@@ -82,15 +88,21 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
     const int ix0 = p.index ? p.index[b * p.N + i0] : 0, id0 = c.table[b * c.width + c0];
     if (ix0 < 0 || ix0 >= p.N) stop = min(stop, i0);
     if (id0 < 0 || id0 >= c.pages) stop = min(stop, max((c0 << c.pshift) - len, 0));
+    // long calls: the loads of several turns go out together (131072 tokens
+    // of 8 heads of 64 in pages of 16: 203 us, one by one 328)
     if (p.index)
-      for (int i = tid + kBlock; i < n; i += kBlock) {
+#pragma unroll 8
+      for (int i = tid + kThreads; i < n; i += kThreads) {
         const int ix = p.index[b * p.N + i];
-        if (ix < 0 || ix >= p.N) stop = min(stop, i);
+        stop = ix < 0 || ix >= p.N ? min(stop, i) : stop;
       }
-    for (int col = col0 + tid + kBlock; col <= last; col += kBlock)
-      if (kv_page(c, b, col) < 0) stop = min(stop, max((col << c.pshift) - len, 0));
+#pragma unroll 8
+    for (int col = col0 + tid + kThreads; col <= last; col += kThreads) {
+      const int id = c.table[b * c.width + col];
+      stop = id < 0 || id >= c.pages ? min(stop, max((col << c.pshift) - len, 0)) : stop;
+    }
   }
-  n = block_min_i32(stop, ldsi);
+  n = block_min_i32<NW>(stop, ldsi);
   if (reports && tid == 0) p.out_lengths[b] = len + n;
   if (n <= 0) return;  // below, every page visited gets at least one token
 
@@ -130,7 +142,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
       const uint8_t* page = c.vp + blk * c.P * c.D;
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
-        const int i = tid + k * kBlock;
+        const int i = tid + k * kThreads;
         int a, v;
         item_of(isv, i, a0, na, vpr, a, v);
 #pragma unroll
@@ -157,7 +169,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
       MaxBits<DT> top;
 #pragma unroll
       for (int k = 0; k < NI; ++k)
-        if (wave0 + k * kBlock < items)
+        if (wave0 + k * kThreads < items)
 #pragma unroll
           for (int r = 0; r < 4; ++r) top.add(raw[x][k][r]);
       wild[x] = top.wild();
@@ -173,7 +185,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
       const int isv = BOTH ? x : blockIdx.y & 1;
       float top = ldsf[x][0];
 #pragma unroll
-      for (int i = 1; i < kWaves; ++i) top = fmaxf(top, ldsf[x][i]);
+      for (int i = 1; i < NW; ++i) top = fmaxf(top, ldsf[x][i]);
       float s = kv_scale<FMT>(top);
       if (t0 > 0) s = fmaxf(s, s_old[x]);
       const bool grow = t0 > 0 && s > s_old[x];  // the tokens that were there go to the grown scale
@@ -181,7 +193,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
       uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
-        const int i = tid + k * kBlock;
+        const int i = tid + k * kThreads;
         if (i >= items) break;
         int a, v;
         item_of(isv, i, a0, na, vpr, a, v);
@@ -231,7 +243,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_append(KvAppend p) {
         }
       }
       if (grow)  // the groups before, of old tokens only
-        for (int i = tid; i < a0 * vpr; i += kBlock) {
+        for (int i = tid; i < a0 * vpr; i += kThreads) {
           int a, v;
           item_of(isv, i, 0, a0, vpr, a, v);
           // K: 4 rows of E codes; V: E rows of 4
@@ -336,21 +348,27 @@ unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P 
 
 template <int DT, int FMT>
 hipError_t append(const KvAppend& p, hipStream_t st) {
-  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);  // at most 2048
+  // items of a page that N tokens can touch, wherever they begin: at most 2048
+  const int items = std::min(p.c.P / 4, (std::min(p.N, p.c.P) + 6) / 4) * (p.c.D / Elt<DT>::kPerVec);
   const unsigned slots = kv_slots(p.N, p.c.P), H = static_cast<unsigned>(p.c.H), B = static_cast<unsigned>(p.B);
   // a few tokens rarely cross into a second page: one workgroup takes both
-  // (256 x 6 tokens, P = 64, 8 heads of 128: 13.9 us, with one per page 21.6)
+  // (256 x 6 tokens by four waves: 13.9 us, with one per page 21.6)
   const unsigned gx = slots <= 2 ? 1 : slots;
   // K and V in one workgroup share the table, index and length reads: 256 x 6
-  // tokens 13.9 us, apart 17.3 (D = 128, P = 64; P = 128 20.2 and 23.4).  With
+  // tokens by four waves 13.9 us, apart 17.3 (D = 128, P = 64; P = 128 20.2 and 23.4).  With
   // four items a thread the registers halve the waves: 24.8 us apart, 28.0
   // together (D = 256, P = 128), 4 x 4096 tokens 26.7 and 32.
-#define LAUNCH(ni, both) \
-  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, both>), dim3(gx, both ? H : 2 * H, B), dim3(kBlock), 0, st, p)
-  if (items <= kBlock) LAUNCH(1, true);
-  else if (items <= 2 * kBlock) LAUNCH(2, true);
-  else if (items <= 4 * kBlock) LAUNCH(4, false);
-  else if constexpr (DT == SPECV_F32) LAUNCH(8, false);
+#define LAUNCH(ni, both, nw) \
+  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, both, nw>), dim3(gx, both ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
+  // One wave's items, one wave: 256 x 9 tokens (P = 64, 8 heads of 128) 10.4 us, by
+  // four waves 13.8; 256 x 1 9.7 and 13.2; 64 x 9 7.0 and 7.5, but 14.4 and 12.6
+  // if every block's scale grows.  More in turns of one wave queue up: 256
+  // paths of up to 32 nodes and their read 89 us against 70.
+  if (items <= kWave) LAUNCH(1, true, 1);
+  else if (items <= kBlock) LAUNCH(1, true, kWaves);
+  else if (items <= 2 * kBlock) LAUNCH(2, true, kWaves);
+  else if (items <= 4 * kBlock) LAUNCH(4, false, kWaves);
+  else if constexpr (DT == SPECV_F32) LAUNCH(8, false, kWaves);
 #undef LAUNCH
   return hipGetLastError();
 }

@@ -108,6 +108,28 @@ def test_append_special_values(gpu_lib, fmt):
     _same_cache(kh.to_host(dev, fmt), c)
 
 
+@pytest.mark.parametrize("fmt,dtype,P,D", [("e4m3", "bf16", 128, 128), ("int8", "f32", 128, 128), ("e4m3", "f32", 64, 256),
+                                           ("int8", "bf16", 32, 96), ("e4m3", "bf16", 64, 256)])
+@pytest.mark.parametrize("N", [1, 2, 4, 5, 9, 13, 14, 22])
+def test_append_few_tokens(gpu_lib, fmt, dtype, P, D, N):
+    """Calls around the size up to which one wave does a block, at every
+    offset in a group of four, across a page's end, with and without growth
+    of a block that is all but full."""
+    rng = np.random.default_rng(P + D + N)
+    lens, H = [0, 1, 2, 3, P - 1, P - 2, P - 3, P, P - N // 2 - 1, P - 1, 2 * P - 2], 2
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D, extra=N)
+    x = rng.normal(size=(2, len(lens), N, H, D)).astype(np.float32)
+    x[:, 4:7] *= 300.0  # these blocks' scales grow
+    x[:, 9] *= 2.0 ** 60
+    import torch
+    k, v = (torch.from_numpy(t).to(_dt(dtype)) for t in x)
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k.cuda(), v.cuda(), _i32(lens))
+    want = okv.append(c, table, k.double().numpy(), v.double().numpy(), lens)
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    _same_cache(kh.to_host(dev, fmt), c)
+
+
 def test_append_long_index(gpu_lib):
     """An index of hundreds of tokens over many pages: any order, repeats, an
     end past the first 256, a missing page in the middle."""
