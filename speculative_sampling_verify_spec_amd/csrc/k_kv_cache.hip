@@ -262,12 +262,15 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
   }
 }
 
-// One workgroup per (page the range may touch, K or V of a head, sequence).
-template <int DT, int FMT, int NI>
+// One workgroup per (page the range may touch, K or V of a head, sequence),
+// NI items per thread; SPREAD: one item per thread, p.chunks workgroups per
+// page.
+template <int DT, int FMT, int NI, bool SPREAD>
 __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   constexpr int E = Elt<DT>::kPerVec;
   const KvView& c = p.c;
-  const int slot = blockIdx.x, h = blockIdx.y >> 1, isv = blockIdx.y & 1;
+  const int slot = SPREAD ? blockIdx.x / p.chunks : blockIdx.x, first = SPREAD ? (blockIdx.x - slot * p.chunks) * kBlock : 0;
+  const int h = blockIdx.y >> 1, isv = blockIdx.y & 1;
   const long b = blockIdx.z;
   void* out = isv ? p.out_v : p.out_k;
   if (!out) return;
@@ -284,13 +287,14 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   const float s = (isv ? c.vs : c.ks)[blk];
   const uint8_t* page = (isv ? c.vp : c.kp) + blk * c.P * c.D;
   const int a0 = t0 / 4, na = (t1 + 3) / 4 - a0, vpr = c.D / E, items = na * vpr;
+  if (SPREAD && first + static_cast<int>(threadIdx.x) >= items) return;
   // row t's place in the output: token p0 + t - start
   const long row0 = b * p.T + (p0 - start);
 
   uint32_t raw[NI][E];  // K: words of 4 channels, [token][E / 4]; V: words of 4 tokens, [channel]
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int i = static_cast<int>(threadIdx.x) + k * kBlock;
+    const int i = first + static_cast<int>(threadIdx.x) + k * kBlock;
     int a, v;
     item_of(isv, i < items ? i : 0, a0, na, vpr, a, v);
     if (!isv) {
@@ -313,7 +317,7 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   }
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int i = static_cast<int>(threadIdx.x) + k * kBlock;
+    const int i = first + static_cast<int>(threadIdx.x) + k * kBlock;
     if (i >= items) break;
     int a, v;
     item_of(isv, i, a0, na, vpr, a, v);
@@ -360,11 +364,14 @@ hipError_t append(const KvAppend& p, hipStream_t st) {
   // together (D = 256, P = 128), 4 x 4096 tokens 26.7 and 32.
 #define LAUNCH(ni, both, nw) \
   hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, both, nw>), dim3(gx, both ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
-  // One wave's items, one wave: 256 x 9 tokens (P = 64, 8 heads of 128) 10.4 us, by
+  // No more waves than items.  One wave: 256 x 9 tokens (P = 64, 8 heads of 128) 10.4 us, by
   // four waves 13.8; 256 x 1 9.7 and 13.2; 64 x 9 7.0 and 7.5, but 14.4 and 12.6
   // if every block's scale grows.  More in turns of one wave queue up: 256
-  // paths of up to 32 nodes and their read 89 us against 70.
+  // paths of up to 32 nodes and their read 89 us against 70.  Three waves: the
+  // same paths and read 40.4 us, by four 41.5.
   if (items <= kWave) LAUNCH(1, true, 1);
+  else if (items <= 2 * kWave) LAUNCH(1, true, 2);
+  else if (items <= 3 * kWave) LAUNCH(1, true, 3);
   else if (items <= kBlock) LAUNCH(1, true, kWaves);
   else if (items <= 2 * kBlock) LAUNCH(2, true, kWaves);
   else if (items <= 4 * kBlock) LAUNCH(4, false, kWaves);
@@ -374,13 +381,24 @@ hipError_t append(const KvAppend& p, hipStream_t st) {
 }
 
 template <int DT, int FMT>
-hipError_t read(const KvRead& p, hipStream_t st) {
-  const dim3 grid(kv_slots(p.T, p.c.P), static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B)), block(kBlock);
-  const int items = p.c.P / 4 * (p.c.D / Elt<DT>::kPerVec);
-  if (items <= kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 1>), grid, block, 0, st, p);
-  else if (items <= 2 * kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 2>), grid, block, 0, st, p);
-  else if (items <= 4 * kBlock) hipLaunchKernelGGL((k_kv_read<DT, FMT, 4>), grid, block, 0, st, p);
-  else if constexpr (DT == SPECV_F32) hipLaunchKernelGGL((k_kv_read<DT, FMT, 8>), grid, block, 0, st, p);
+hipError_t read(KvRead p, hipStream_t st) {
+  // items of a page that T tokens can touch, wherever they begin
+  const int items = std::min(p.c.P / 4, (std::min(p.T, p.c.P) + 6) / 4) * (p.c.D / Elt<DT>::kPerVec);
+  // Calls over whole pages spread a page's items over workgroups: 16 x 4096
+  // tokens (P = 128) 98 us, with several items a thread 102 (bf16, D = 128), 173 and
+  // 196 (fp32, D = 256).  In short calls the workgroups that find nothing to do
+  // count: 256 x 33 tokens in fp32 (P = 64, D = 128) 43 us spread and 28 not.
+  p.chunks = p.T >= 4 * p.c.P ? (items + kBlock - 1) / kBlock : 1;
+  const dim3 grid(kv_slots(p.T, p.c.P) * p.chunks, static_cast<unsigned>(2 * p.c.H), static_cast<unsigned>(p.B));
+  // no more waves than items: 64 x 100 tokens (P = 16, D = 64) 9.0 us, four waves each 12.4
+  const dim3 block(std::min((items + kWave - 1) / kWave * kWave, kBlock));
+#define LAUNCH(ni, spread) hipLaunchKernelGGL((k_kv_read<DT, FMT, ni, spread>), grid, block, 0, st, p)
+  if (p.chunks > 1) LAUNCH(1, true);
+  else if (items <= kBlock) LAUNCH(1, false);
+  else if (items <= 2 * kBlock) LAUNCH(2, false);
+  else if (items <= 4 * kBlock) LAUNCH(4, false);
+  else if constexpr (DT == SPECV_F32) LAUNCH(8, false);
+#undef LAUNCH
   return hipGetLastError();
 }
 

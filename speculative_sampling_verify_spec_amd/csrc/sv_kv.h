@@ -41,6 +41,7 @@ struct KvRead {
   int B, T;
   void* out_k;            // [B][T][H][D], or null
   void* out_v;
+  int chunks;             // workgroups that share a page (the launcher sets it)
 };
 
 struct KvAttn {

@@ -199,6 +199,23 @@ def test_read_is_exact(gpu_lib, fmt, P, H, D, dtype):
         np.testing.assert_array_equal(v.double().cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,P,D", [("e4m3", 128, 256), ("int8", 128, 96), ("e4m3", 64, 256), ("int8", 32, 128)])
+def test_read_short_and_long(gpu_lib, fmt, P, D, dtype):
+    """A few tokens, and ranges of whole pages on both sides of the length
+    from which workgroups share a page, at every offset in a group of four."""
+    rng = np.random.default_rng(P + D)
+    lens = [0, 5 * P, 4 * P + 3, P + 1, 6 * P - 1]
+    c, table = kh.make_cache(rng, fmt, lens, P, 2, D)
+    dev = kh.to_device(gpu_lib, c)
+    for T, starts in ((1, [0, 5, P - 1, P, 6 * P - 2]), (3, [0, P - 2, 2, 1, P - 1]), (10, [1, P - 5, 2, P - 9, 3]),
+                      (4 * P - 1, [0, 1, 2, 3, P - 1]), (4 * P, [3, 0, 2, 1, 2 * P - 1]), (5 * P + 2, [0, 1, 2, 3, P + 2])):
+        k, v = gpu_lib.kv_read(dev, _i32(table), _i32(lens), T, starts=_i32(starts), dtype=_dt(dtype))
+        want = okv.read(c, table, lens, T, starts)
+        np.testing.assert_array_equal(k.double().cpu().numpy(), want[0])
+        np.testing.assert_array_equal(v.double().cpu().numpy(), want[1])
+
+
 def test_read_without_pages(gpu_lib):
     rng = np.random.default_rng(8)
     c, table = kh.make_cache(rng, "e4m3", [40, 40], 16, 2, 64)
