@@ -21,7 +21,7 @@
 // them.
 //
 // Bound by reading the cache once: 256 x 9 positions (G = 4, D = 128, e4m3)
-// over 1001-4097 tokens take 283 us, 5.0 TB/s; 512 x 1 (G = 8, D = 256, int8)
+// over 1001-4097 tokens take 280 us, 5.0 TB/s; 512 x 1 (G = 8, D = 256, int8)
 // 215 us, 4.8 TB/s; equal lengths of 2560 with one position 6.1 TB/s.  Many
 // queries are bound by instruction issue instead: 128 trees of 32 nodes 223 us
 // for 90 GFLOP, 61 % of it VALU (conversions, exponentials) and 21 % MFMA.
