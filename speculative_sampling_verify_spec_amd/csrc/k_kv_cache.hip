@@ -13,8 +13,8 @@
 // K pages are [P][D], V pages are [D][P]: the attention's second product
 // reads V along the tokens.
 //
-// Both kernels give one workgroup to the K or V of one block.  Its items are
-// 4 tokens x 16 bytes of a value row, of the tokens the call touches.  For K, neighbouring lanes take
+// A workgroup has the K or V of a block, or both, or a share of it.  Its items
+// are 4 tokens x 16 bytes of a value row, of the tokens the call touches.  For K, neighbouring lanes take
 // neighbouring channels (whole rows on both sides); for V neighbouring lanes
 // take neighbouring tokens, so that the four codes of a channel, one word,
 // meet their neighbours in the transposed page and the rows are still touched
@@ -55,15 +55,16 @@ __device__ inline void item_of(int isv, unsigned i, int a0, unsigned na, unsigne
   v = static_cast<int>(isv ? q : r);
 }
 
-// A workgroup of NW waves takes K and V (BOTH) or one of them of one head of
-// one sequence, in every gridDim.x-th page that the call may touch.  NI items per
-// thread of each; their values stay in registers between the search for the
-// largest magnitude and the quantisation.
+// A workgroup of NW waves takes one head of one sequence, in every
+// gridDim.x-th page that the call may touch: its K and V with one item per
+// thread, one of them with NI items.  The values stay in registers between the
+// search for the largest magnitude and the quantisation.
 //
 // Five waves a SIMD with one item a thread: 95 registers; left to itself the
 // compiler takes 120 (256 x 32 tokens 23.2 us against 24.5), six waves spill.
-template <int DT, int FMT, int NI, bool BOTH, int NW>
+template <int DT, int FMT, int NI, int NW>
 __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvAppend p) {
+  constexpr bool BOTH = NI == 1;
   constexpr int E = Elt<DT>::kPerVec, NX = BOTH ? 2 : 1, kThreads = NW * kWave;
   const KvView& c = p.c;
   const int h = BOTH ? blockIdx.y : blockIdx.y >> 1;
@@ -359,23 +360,23 @@ hipError_t append(const KvAppend& p, hipStream_t st) {
   // (256 x 6 tokens by four waves: 13.9 us, with one per page 21.6)
   const unsigned gx = slots <= 2 ? 1 : slots;
   // K and V in one workgroup share the table, index and length reads: 256 x 6
-  // tokens by four waves 13.9 us, apart 17.3 (D = 128, P = 64; P = 128 20.2 and 23.4).  With
-  // four items a thread the registers halve the waves: 24.8 us apart, 28.0
-  // together (D = 256, P = 128), 4 x 4096 tokens 26.7 and 32.
-#define LAUNCH(ni, both, nw) \
-  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, both, nw>), dim3(gx, both ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
+  // tokens by four waves 13.9 us, apart 17.3 (D = 128, P = 64).  With two items a
+  // thread the registers count for more: 64 x 100 tokens (D = 128, P = 128) 16.0 us
+  // together, 14.3 apart, 4 x 4096 23.8 and 22.4, but 256 x 64 34.2 and 37.0.
+#define LAUNCH(ni, nw) \
+  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, nw>), dim3(gx, ni == 1 ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
   // No more waves than items.  One wave: 256 x 9 tokens (P = 64, 8 heads of 128) 10.4 us, by
   // four waves 13.8; 256 x 1 9.7 and 13.2; 64 x 9 7.0 and 7.5, but 14.4 and 12.6
   // if every block's scale grows.  More in turns of one wave queue up: 256
   // paths of up to 32 nodes and their read 89 us against 70.  Three waves: the
   // same paths and read 40.4 us, by four 41.5.
-  if (items <= kWave) LAUNCH(1, true, 1);
-  else if (items <= 2 * kWave) LAUNCH(1, true, 2);
-  else if (items <= 3 * kWave) LAUNCH(1, true, 3);
-  else if (items <= kBlock) LAUNCH(1, true, kWaves);
-  else if (items <= 2 * kBlock) LAUNCH(2, true, kWaves);
-  else if (items <= 4 * kBlock) LAUNCH(4, false, kWaves);
-  else if constexpr (DT == SPECV_F32) LAUNCH(8, false, kWaves);
+  if (items <= kWave) LAUNCH(1, 1);
+  else if (items <= 2 * kWave) LAUNCH(1, 2);
+  else if (items <= 3 * kWave) LAUNCH(1, 3);
+  else if (items <= kBlock) LAUNCH(1, kWaves);
+  else if (items <= 2 * kBlock) LAUNCH(2, kWaves);
+  else if (items <= 4 * kBlock) LAUNCH(4, kWaves);
+  else if constexpr (DT == SPECV_F32) LAUNCH(8, kWaves);
 #undef LAUNCH
   return hipGetLastError();
 }
