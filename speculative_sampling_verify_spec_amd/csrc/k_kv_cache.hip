@@ -55,8 +55,8 @@ __device__ inline void item_of(int isv, unsigned i, int a0, unsigned na, unsigne
   v = static_cast<int>(isv ? q : r);
 }
 
-// A workgroup of NW waves takes one head of one sequence, in every
-// gridDim.x-th page that the call may touch: its K and V with one item per
+// A workgroup of NW waves takes one head of one sequence, in p.per
+// consecutive pages that the call may touch: its K and V with one item per
 // thread, one of them with NI items.  The values stay in registers between the
 // search for the largest magnitude and the quantisation.
 //
@@ -77,23 +77,26 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
   const int room = (c.width << c.pshift) - len;
   int n = min(p.counts ? min(max(p.counts[b], 0), p.N) : p.N, room);
   // the tokens end at the first index outside [0, N), and at the first page
-  // the table does not have; every page up to this workgroup's last counts
-  // (every page at all, where the new length is written)
+  // the table does not have; what counts is every page and token up to this
+  // workgroup's last (all of them, where the new length is written)
   const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && p.out_lengths;
   const int col0 = len >> c.pshift;
+  const int first = static_cast<int>(blockIdx.x) * p.per;  // this workgroup's first page, from col0 on
   int stop = n;
   if (n > 0) {
     const int end = (len + n - 1) >> c.pshift;
-    const int last = reports || gridDim.x == 1 || static_cast<int>(blockIdx.x) > end - col0 ? end : col0 + blockIdx.x;
-    const int i0 = min(tid, n - 1), c0 = min(col0 + tid, last);  // both loads before either test
+    if (!reports && first > end - col0) return;
+    const int last = reports ? end : min(end, col0 + first + p.per - 1);
+    const int upto = last == end ? n : ((last + 1) << c.pshift) - len;  // tokens up to there
+    const int i0 = min(tid, upto - 1), c0 = min(col0 + tid, last);  // both loads before either test
     const int ix0 = p.index ? p.index[b * p.N + i0] : 0, id0 = c.table[b * c.width + c0];
     if (ix0 < 0 || ix0 >= p.N) stop = min(stop, i0);
     if (id0 < 0 || id0 >= c.pages) stop = min(stop, max((c0 << c.pshift) - len, 0));
     // long calls: the loads of several turns go out together (131072 tokens
-    // of 8 heads of 64 in pages of 16: 203 us, one by one 328)
+    // of 8 heads of 64 in pages of 16: 131 us, one by one 163; by index 350 and 947)
     if (p.index)
 #pragma unroll 8
-      for (int i = tid + kThreads; i < n; i += kThreads) {
+      for (int i = tid + kThreads; i < upto; i += kThreads) {
         const int ix = p.index[b * p.N + i];
         stop = ix < 0 || ix >= p.N ? min(stop, i) : stop;
       }
@@ -109,7 +112,8 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
 
   const int vpr = c.D / E;
   const int wave0 = __builtin_amdgcn_readfirstlane(tid) & ~(kWave - 1);  // the wave's first item
-  for (long col = static_cast<long>(col0) + blockIdx.x; (col << c.pshift) < static_cast<long>(len) + n; col += gridDim.x) {
+  const long col1 = static_cast<long>(col0) + first + p.per;
+  for (long col = col1 - p.per; col < col1 && (col << c.pshift) < static_cast<long>(len) + n; ++col) {
     const long p0 = col << c.pshift;                                            // the page's first position
     const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
     const int t1 = static_cast<int>(min(len + n - p0, static_cast<long>(c.P)));  // and after
@@ -348,17 +352,12 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   }
 }
 
-// Pages that n consecutive tokens can touch, whatever position they start at.
-unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P + 1); }
-
 template <int DT, int FMT>
 hipError_t append(const KvAppend& p, hipStream_t st) {
   // items of a page that N tokens can touch, wherever they begin: at most 2048
   const int items = std::min(p.c.P / 4, (std::min(p.N, p.c.P) + 6) / 4) * (p.c.D / Elt<DT>::kPerVec);
-  const unsigned slots = kv_slots(p.N, p.c.P), H = static_cast<unsigned>(p.c.H), B = static_cast<unsigned>(p.B);
-  // a few tokens rarely cross into a second page: one workgroup takes both
-  // (256 x 6 tokens by four waves: 13.9 us, with one per page 21.6)
-  const unsigned gx = slots <= 2 ? 1 : slots;
+  const unsigned H = static_cast<unsigned>(p.c.H), B = static_cast<unsigned>(p.B);
+  const unsigned gx = (kv_slots(p.N, p.c.P) + p.per - 1) / p.per;
   // K and V in one workgroup share the table, index and length reads: 256 x 6
   // tokens by four waves 13.9 us, apart 17.3 (D = 128, P = 64).  With two items a
   // thread the registers count for more: 64 x 100 tokens (D = 128, P = 128) 16.0 us

@@ -148,6 +148,51 @@ def test_append_long_index(gpu_lib):
     _same_cache(kh.to_host(dev, "int8"), c)
 
 
+@pytest.mark.parametrize("indexed", [False, True])
+def test_append_several_pages_a_workgroup(gpu_lib, indexed):
+    """More pages than a head has workgroups (1024): ends and missing pages
+    before, in and behind a workgroup's three pages, and a short sequence."""
+    rng = np.random.default_rng(26)
+    B, N, P, H, D = 7, 40000, 16, 1, 64
+    lens = [0, 7, 0, 33, 5, 0, 16]
+    counts = np.array([N, N, 17001, N, N, 20, 0])
+    c, table = kh.make_cache(rng, "int8", [n + k for n, k in zip(lens, counts)], P, H, D, poison=False)
+    table[0, 1000], table[3, 48], table[4, 50] = -1, 10 ** 9, -7
+    index = rng.integers(0, N, (B, N))
+    index[1, 31000], index[2, 17000], index[3, 40], index[5, 3] = -1, N, -1, N
+    (k, k64), (v, v64) = _rand(rng, (B, N, H, D), "bf16"), _rand(rng, (B, N, H, D), "bf16")
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k, v, _i32(lens), counts=_i32(counts),
+                            index=_i32(index) if indexed else None)
+    want = okv.append(c, table, k64, v64, lens, counts, index if indexed else None)
+    ends = [16000, 31007, 17000, 73, 800, 3, 16] if indexed else [16000, 40007, 17001, 768, 800, 20, 16]
+    assert got.cpu().numpy().tolist() == want.tolist() == ends
+    _same_cache(kh.to_host(dev, "int8"), c)
+
+
+def test_longest_append(gpu_lib):
+    """2^24 tokens by index in the smallest pages, against the same tokens in
+    order and in sixteen calls."""
+    import torch
+    N, P, D = 1 << 24, 16, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    k = torch.randn((1, N, 1, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    v = k.roll(1, 3)
+    table = torch.randperm(N // P, generator=g, device="cuda").int().view(1, -1)
+    whole, pieces = (gpu_lib.KVCache.empty(N // P, P, 1, D, dtype=torch.int8) for _ in range(2))
+    index = torch.arange(N - 1, -1, -1, dtype=torch.int32, device="cuda").view(1, N)
+    after = gpu_lib.kv_append(whole, table, k, v, _i32([0]), index=index)
+    assert int(after[0]) == N
+    at = _i32([0])
+    for i in range(0, N, N // 16):
+        src = slice(N - i - N // 16, N - i)
+        at = gpu_lib.kv_append(pieces, table, k[:, src].flip(1), v[:, src].flip(1), at)
+    assert int(at[0]) == N
+    for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+        assert torch.equal(getattr(whole, name), getattr(pieces, name)), name
+
+
 def test_append_without_pages(gpu_lib):
     """A missing or foreign page ends the tokens there; a full table, a
     negative and a too large length write nothing out of place."""

@@ -194,6 +194,52 @@ hipError_t launch_kv_attention(const KvAttn&, int, int, hipStream_t) { return hi
 """
 
 
+PLAN_STUBS = """
+#include "specverify.h"
+#include "sv_kv.h"
+namespace sv {
+static KvAppend seen;
+hipError_t launch_kv_append(const KvAppend& p, int, int, hipStream_t) { seen = p; return hipSuccess; }
+hipError_t launch_kv_read(const KvRead&, int, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_kv_attention(const KvAttn&, int, int, hipStream_t) { return hipSuccess; }
+}
+extern "C" int pages_per_group() { return sv::seen.per; }
+extern "C" unsigned page_slots() { return sv::kv_slots(sv::seen.N, sv::seen.c.P); }
+"""
+
+
+def test_append_work_is_linear_in_the_tokens(tmp_path):
+    """A workgroup of the append looks through the call's pages and indexes up
+    to its own last one.  Its pages cover the call, and a head's workgroups
+    look at no more than 1024 entries for each token, up to the longest call
+    (with a workgroup for every page: 2^39 pages and 2^43 indexes)."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("g++ not found")
+    stubs, so = tmp_path / "plan.cpp", tmp_path / "libkv_plan.so"
+    stubs.write_text(PLAN_STUBS)
+    r = subprocess.run([gxx, "-std=c++17", "-shared", "-fPIC", "-O1", "-D__HIP_PLATFORM_AMD__",
+                        "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", "/opt/rocm/include",
+                        os.path.join(CSRC, "api_kv.cpp"), str(stubs), "-o", str(so)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
+    plan = ctypes.CDLL(str(so))
+    plan.spec_kv_append.argtypes = sv.load().spec_kv_append.argtypes
+    for P in (16, 32, 64, 128):
+        for N in (1, 2, P, P + 1, P + 2, 8191, 1 << 14, (1 << 14) + 17, 131072, 999999, 1 << 24):
+            c = kv(page_size=P, max_pages=(1 << 24) // P + 2)
+            assert plan.spec_kv_append(ctypes.byref(c), BASE, BASE, 0, BASE, None, BASE, 1, N, None, BF16, None) == 0
+            per, slots = plan.pages_per_group(), plan.page_slots()
+            assert slots == (N + P - 2) // P + 1 and per >= 1
+            groups = -(-slots // per)
+            assert groups * per >= slots
+            pages = sum(min(slots, (g + 1) * per) for g in range(groups))
+            indexes = sum(min(N, (g + 1) * per * P) for g in range(groups))
+            assert pages <= 1024 * slots and indexes <= 1024 * N
+            if 2 < slots <= 1024:
+                assert per == 1  # nothing is taken in turns that can run at once
+
+
 def test_host_checks_under_address_sanitizer(tmp_path):
     gxx = shutil.which("g++")
     asan = subprocess.run([gxx, "-print-file-name=libasan.so"], capture_output=True, text=True).stdout.strip() \
