@@ -51,6 +51,7 @@ typedef enum { SPECV_F32 = 0, SPECV_BF16 = 1 } specv_dtype_t;
 #define SPECV_E_ALIGN      -6   /* a logits pointer is not aligned to its element size, or a cache array or stride to 16 bytes */
 #define SPECV_E_HIP        -7   /* a kernel launch failed */
 #define SPECV_E_SCRATCH    -8   /* spec_verify_noalloc: the shape needs more than SPECV_NOALLOC_SCRATCH bytes */
+#define SPECV_E_OVERLAP    -9   /* spec_kv_append: out_lengths overlaps an array that the call reads */
 
 #define SPECV_MAX_K        32   /* one 64-lane wave runs the acceptance scan */
 #define SPECV_MAX_TREE     64   /* token-tree nodes: one per lane of a wave */
@@ -426,8 +427,8 @@ typedef struct {
  *   lengths     [B] int32 (device): tokens cached before, clamped to [0,
  *               max_pages * page_size]
  *   counts      [B] int32 (device) or NULL;  index [B][N] int32 (device) or NULL
- *   out_lengths [B] int32 or NULL: tokens cached after the call (must not
- *               overlap `lengths`)
+ *   out_lengths [B] int32 or NULL: tokens cached after the call; overlaps
+ *               neither lengths, counts, index nor the page table
  *   B <= 65535;  1 <= N <= SPECV_KV_MAX_APPEND
  * A page that the call writes may stand in one place of one sequence's table
  * row only; pages that are only read may be shared.  Needs no workspace;

@@ -171,8 +171,9 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
     rows will do), page_table [B, max_pages], lengths [B] and optionally
     counts [B] (tokens of each sequence) and index [B, N] (which tokens, up to
     the first entry outside [0, N): the path of verify_tree_greedy), int32.
-    Returns the tokens cached after the call, [B] int32 (out_lengths if given;
-    lengths itself is left as it is, so every layer can pass it)."""
+    Returns the tokens cached after the call, [B] int32 (out_lengths if given,
+    which overlaps none of the other int32 tensors; lengths itself is left as
+    it is, so every layer can pass it)."""
     _check_table(cache, page_table)
     B, width = page_table.shape
     if k.dim() != 4:
@@ -190,8 +191,10 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
         out_lengths = torch.empty_like(lengths)
     else:
         _check_ints(cache, (B,), "out_lengths", out_lengths)
-        if abs(out_lengths.data_ptr() - lengths.data_ptr()) < 4 * B:
-            raise ValueError("out_lengths must not overlap lengths")
+        at = out_lengths.data_ptr()
+        for name, t in (("lengths", lengths), ("counts", counts), ("index", index), ("page_table", page_table)):
+            if t is not None and t.data_ptr() < at + 4 * B and at < t.data_ptr() + 4 * t.numel():
+                raise ValueError(f"out_lengths must not overlap {name}")
     _call(cache._device, load().spec_kv_append, _descriptor(cache, page_table.data_ptr(), width), k.data_ptr(),
           v.data_ptr(), row, lengths.data_ptr(), _ptr(counts), _ptr(index), B, N, out_lengths.data_ptr(),
           _dtype_code(k.dtype))

@@ -54,6 +54,12 @@ int check_row(int64_t* row, long heads, int D, int dtype) {
   return *row * (dtype == SPECV_F32 ? 4 : 2) % 16 ? SPECV_E_ALIGN : SPECV_OK;
 }
 
+// Whether a[0 .. na) and b[0 .. nb) share bytes; null arrays share none.
+bool overlap(const int32_t* a, long na, const int32_t* b, long nb) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + 4 * static_cast<uintptr_t>(nb) && y < x + 4 * static_cast<uintptr_t>(na);
+}
+
 // How an attention call is cut into workgroups; from sizes alone (the lengths
 // are on the device), so that the workspace's size is known before.
 struct KvPlan {
@@ -113,6 +119,11 @@ int spec_kv_append(const specv_kv_t* kv, const void* k, const void* v, int64_t r
   if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_KV_MAX_APPEND) return SPECV_E_SHAPE;
   if (const int rc = check_row(&row_stride, p.c.H, p.c.D, dtype)) return rc;
   if (!aligned16(k) || !aligned16(v)) return SPECV_E_ALIGN;
+  // one workgroup writes a sequence's new length while others still read these
+  if (overlap(out_lengths, B, lengths, B) || overlap(out_lengths, B, counts, B) ||
+      overlap(out_lengths, B, index, static_cast<long>(B) * N) ||
+      overlap(out_lengths, B, p.c.table, static_cast<long>(B) * p.c.width))
+    return SPECV_E_OVERLAP;
   p.k = k;
   p.v = v;
   p.row = row_stride;

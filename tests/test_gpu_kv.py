@@ -663,6 +663,25 @@ def test_misaligned_rows_are_refused(gpu_lib):
                           torch.zeros(2, 1, 1, 64, device="cuda"), _i32([0, 0, 0])[:2], out_lengths=both.new_zeros(2)[1:])
 
 
+def test_overlapping_lengths_are_refused(gpu_lib):
+    """New lengths over a part of any array the call reads; beside it they are fine."""
+    import torch
+    B, N, P, D = 2, 3, 16, 64
+    cache = gpu_lib.KVCache.empty(4, P, 1, D)
+    x = torch.zeros(B, N, 1, D, device="cuda")
+    buf = torch.zeros(64, dtype=torch.int32, device="cuda")
+    table = buf[:8].view(B, 4)
+    lengths, counts, index = buf[16:18], buf[24:26], buf[32:38].view(B, N)
+    table.copy_(_i32([[0, 1, 9, 9], [2, 3, 9, 9]])), counts.fill_(2), index.copy_(_i32([[2, 1, 0]] * 2))
+    for name, first, n in (("lengths", 16, 2), ("counts", 24, 2), ("index", 32, 6), ("page_table", 0, 8)):
+        for at in {first, first + 1, first + n - 1, max(first - 1, 0)}:
+            with pytest.raises(ValueError, match=f"overlap {name}"):
+                gpu_lib.kv_append(cache, table, x, x, lengths, counts=counts, index=index, out_lengths=buf[at:at + 2])
+        got = gpu_lib.kv_append(cache, table, x, x, lengths, counts=counts, index=index,
+                                out_lengths=buf[first + n:first + n + 2])
+        assert got.tolist() == [2, 2]
+
+
 def test_verify_round_with_trees(gpu_lib):
     """A run of them together: prompts cached, then rounds of attention over
     a token tree, greedy verification of the logits its outputs give, and the

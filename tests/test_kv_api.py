@@ -92,6 +92,21 @@ def test_append_refusals(lib, kw, code):
     assert append(lib, **kw) == code
 
 
+def test_append_overlap(lib):
+    """The new lengths may touch none of the arrays that other workgroups
+    still read; right next to them is as far as they may go."""
+    B, N, width = 4, 3, 10
+    for name, at, n in (("lengths", 8 * BASE, B), ("counts", 10 * BASE, B), ("index", 11 * BASE, B * N),
+                        ("page_table", 5 * BASE, B * width)):
+        kw = {} if name == "page_table" else {name: at}
+        for out in (at, at + 4, at - 4 * (B - 1), at + 4 * (n - 1)):
+            assert append(lib, out=out, B=B, N=N, **kw) == -9, (name, out - at)
+        for out in (at - 4 * B, at + 4 * n):
+            assert append(lib, out=out, B=B, N=N, k=None, **kw) == -1
+            assert append(lib, out=out, B=B, N=N, k=BASE + 8, **kw) == -6
+    assert sv.ERRORS[-9] == "SPECV_E_OVERLAP" and "overlap" in sv.strerror(-9)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=-1), -3), (dict(lengths=None), -1), (dict(k=None, v=None), -1), (dict(B=0), -2), (dict(T=0), -2),
     (dict(T=(1 << 24) + 1), -2), (dict(B=65536), -2), (dict(k=BASE + 8), -6), (dict(v=BASE + 8), -6)])
@@ -225,6 +240,8 @@ def test_append_work_is_linear_in_the_tokens(tmp_path):
     assert r.returncode == 0, r.stderr[-3000:]
     plan = ctypes.CDLL(str(so))
     plan.spec_kv_append.argtypes = sv.load().spec_kv_append.argtypes
+    for out in (8 * BASE - 16, 8 * BASE + 16, 5 * BASE + 160, 9 * BASE + 48):  # next to the arrays, not over them
+        assert append(plan, counts=8 * BASE, index=9 * BASE, out=out) == 0
     for P in (16, 32, 64, 128):
         for N in (1, 2, P, P + 1, P + 2, 8191, 1 << 14, (1 << 14) + 17, 131072, 999999, 1 << 24):
             c = kv(page_size=P, max_pages=(1 << 24) // P + 2)
