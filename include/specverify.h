@@ -441,8 +441,11 @@ int spec_kv_append(const specv_kv_t* kv, const void* k, const void* v, int64_t r
 /*
  * spec_kv_read - cached tokens back as values: out_k[b][t] and out_v[b][t]
  * are position starts[b] + t of sequence b (starts clamped to at least 0;
- * NULL: 0), exact in both types for scales that are powers of two; 0 at and
- * behind lengths[b] and where the page_table has no page.
+ * NULL: 0); 0 at and behind lengths[b] and where the page_table has no page.
+ * For scales that are powers of two the values are exact, but for two ends:
+ * what passes the type's largest finite value reads as that value (codes of
+ * values within half a step of it can), and bf16 rounds magnitudes below
+ * 2^-130, which e4m3 codes under a scale of 2^-126 can have.
  *   out_k, out_v  [B][T][heads][dim] (dtype), 16-byte aligned; one may be NULL
  *   B <= 65535;  1 <= T <= SPECV_KV_MAX_APPEND
  * Needs no workspace; nothing synchronises.

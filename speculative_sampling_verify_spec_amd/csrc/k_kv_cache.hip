@@ -296,6 +296,11 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
   // row t's place in the output: token p0 + t - start
   const long row0 = b * p.T + (p0 - start);
 
+  // Blocks next to the largest float: a code times the scale can pass the
+  // output type's range where the value that was appended did not.
+  constexpr float top = kLargest<DT>;
+  const bool huge = s > 0x1p119f;
+
   uint32_t raw[NI][E];  // K: words of 4 channels, [token][E / 4]; V: words of 4 tokens, [channel]
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
@@ -347,6 +352,9 @@ __global__ __launch_bounds__(kBlock) void k_kv_read(KvRead p) {
       if (t < t0 || t >= t1) continue;
 #pragma unroll
       for (int j = 0; j < E; ++j) f[r][j] = t < have ? f[r][j] * s : 0.f;
+      if (huge)
+#pragma unroll
+        for (int j = 0; j < E; ++j) f[r][j] = f[r][j] > top ? top : f[r][j] < -top ? -top : f[r][j];  // NaN stays
       kv_store16<DT>(out, ((row0 + t) * c.H + h) * c.D + v * E, f[r]);
     }
   }

@@ -113,6 +113,10 @@ hipError_t launch_kv_attn_256(const KvAttn& p, int dtype, int fmt, hipStream_t s
 constexpr float kE4m3Max = 448.f;  // largest e4m3 value: 0.875 * 2^9
 constexpr float kI8Max = 127.f;    // largest int8 code used (symmetric): 0.9921875 * 2^7
 
+// Largest finite value of an element type.
+template <int DT>
+constexpr float kLargest = DT == SPECV_F32 ? 0x1.fffffep127f : 0x1.fep127f;
+
 // Four codes of a word to float; exact for both formats.
 template <int FMT>
 __device__ inline void kv_decode4(uint32_t w, float* f) {
@@ -216,7 +220,9 @@ __device__ inline uint32_t kv_rescale4(uint32_t w, float ratio) {
 }
 
 // The smallest power of two s with amax <= top * s, at least 2^-126 (the
-// smallest normal number, also for amax = 0).  amax is finite, so s <= 2^121.
+// smallest normal number, also for amax = 0).  amax is finite, so s <= 2^120
+// (e4m3) or 2^122 (int8), and the code of a value past 248 or 63.5 times that
+// stands for 2^128, which spec_kv_read gives as the largest finite value.
 template <int FMT>
 __device__ inline float kv_scale(float amax) {
   constexpr int bits = FMT == SPECV_E4M3 ? 9 : 7;

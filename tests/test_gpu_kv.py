@@ -261,6 +261,52 @@ def test_read_short_and_long(gpu_lib, fmt, P, D, dtype):
         np.testing.assert_array_equal(v.double().cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,D,N", [("e4m3", 64, 5), ("int8", 96, 5), ("e4m3", 256, 70), ("int8", 128, 70)])
+def test_finite_values_read_back_finite(gpu_lib, fmt, D, N, dtype):
+    """Values next to the type's largest, whose code times the scale is
+    2^128, and next to its smallest: what was finite reads back finite and
+    within half a step of the code, NaN (e4m3) stays NaN, and magnitudes past
+    the range, under scales of the caller's own, are the largest value."""
+    import torch
+    rng = np.random.default_rng(27)
+    P, H = 16, 1
+    c, table = kh.make_cache(rng, fmt, [0, 0, 3], P, H, D, extra=N, poison=False)
+    dt = _dt(dtype)
+    big = float(torch.finfo(dt).max)
+    x = rng.normal(size=(2, 3, N, H, D)).astype(np.float32)
+    x[:, 0] *= 3e36
+    x[:, 0, :, :, 0], x[:, 0, :, :, 1], x[:, 0, 1, 0, 2], x[:, 0, 3, 0, 5] = big, -big, 3.38e38, np.nan
+    x[:, 1] *= 2.0 ** -130
+    k, v = (torch.from_numpy(t).to(dt) for t in x)
+    dev, tab = kh.to_device(gpu_lib, c), _i32(table)
+    after = gpu_lib.kv_append(dev, tab, k.cuda(), v.cuda(), _i32([0, 0, 3]))
+    want = okv.append(c, table, k.double().numpy(), v.double().numpy(), [0, 0, 3])
+    _same_cache(kh.to_host(dev, fmt), c)
+
+    def check(cache, c):
+        got = gpu_lib.kv_read(cache, tab, after, 3 + N, dtype=dt)
+        for g, w in zip(got, okv.read(c, table, want, 3 + N)):
+            # fp64 holds code * scale; float has it exactly once it is in range
+            w = torch.from_numpy(np.clip(w, -big, big)).float().to(dt)
+            assert torch.equal(g.cpu().isnan(), w.isnan())
+            assert torch.equal(g.cpu().nan_to_num(), w.nan_to_num())
+        return got
+    for g, w in zip(check(dev, c), (k, v)):
+        fine = w[0].isfinite()
+        assert g[0, :N].cpu()[fine].isfinite().all() and fine.sum() >= fine.numel() - 1
+        assert (g[0, :N, :, 0] == big).all() and (g[0, :N, :, 1] == -big).all()
+        if fmt == "e4m3":
+            assert g[0, 3, 0, 5].isnan()
+    for name in ("k_scales", "v_scales"):
+        c[name][:] = np.float32(1.3 * 2.0 ** 121)
+    if dtype == "f32":  # such products round once in float, and once more in bf16
+        check(kh.to_device(gpu_lib, c), c)
+    else:
+        got = gpu_lib.kv_read(kh.to_device(gpu_lib, c), tab, after, 3 + N, dtype=dt)
+        assert all(not g.isinf().any() for g in got)
+
+
 def test_read_without_pages(gpu_lib):
     rng = np.random.default_rng(8)
     c, table = kh.make_cache(rng, "e4m3", [40, 40], 16, 2, 64)
