@@ -393,6 +393,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         s[mt][r] = ok ? s[mt][r] * kscale : -INFINITY;
         x = fmaxf(x, s[mt][r]);
       }
+      m[mt] = fmaxf(m[mt], -FLT_MAX);  // finite: a node's score can be -infinity where it is seen, too
       raise(mt, x);
 #pragma unroll
       for (int i = 0; i < NP; ++i) pf[mt][i] = bf16x8{};

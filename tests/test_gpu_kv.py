@@ -462,6 +462,37 @@ def test_attention_nan_and_infinity_in_unseen_nodes(gpu_lib, dtype, N):
                 assert (got[~blind][..., 7] == val).all() and got[~blind][..., :7].isfinite().all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,N,lens", [(64, 1, [50, 7000, 16]), (128, 17, [0, 50, 5000]), (256, 40, [0, 70, 9])])
+def test_attention_nodes_with_the_lowest_score(gpu_lib, D, N, lens, dtype):
+    """A key at the type's lowest value, whose score passes 32 bits downwards,
+    has a weight of 0 where it is seen, as a key far below the others has:
+    alone in its wave's block of nodes, beside others, under a tree."""
+    import torch
+    rng = np.random.default_rng(28)
+    P, H = 32, 2
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D)
+    (q, _), (k, _), (v, v64) = (_rand(rng, (3, N, h, D), dtype) for h in (4, H, H))
+    q[..., 7] = 8.0
+    low = N - 1  # the only node of its block that the last queries see, for 17 nodes
+    par = _tree(rng, 3, N) if N == 40 else None
+    res = []
+    for val in (-20000.0, float(torch.finfo(_dt(dtype)).min)):
+        k[:, low, :, 7] = val
+        if val == -20000.0:
+            res.append(_check_attention(gpu_lib, c, table, lens, (q, q.double().cpu().numpy()),
+                                        (k, k.double().cpu().numpy()), (v, v64), 1.0, dtype, par))
+        else:
+            res.append(gpu_lib.kv_attention(kh.to_device(gpu_lib, c), _i32(table), q, _i32(lens), k, v, scale=1.0,
+                                            return_lse=True, parents=None if par is None else _i32(par)))
+    for a, b in zip(*res):
+        assert a.isfinite().all() and torch.equal(a, b)
+    # alone, nothing weighs anything: as a query that sees nothing
+    out, lse = gpu_lib.kv_attention(kh.to_device(gpu_lib, c), _i32(table), q[:, low:].contiguous(), _i32([0, 0, 0]),
+                                    k[:, low:].contiguous(), v[:, low:].contiguous(), scale=1.0, return_lse=True)
+    assert (out == 0).all() and (lse == -np.inf).all()
+
+
 def test_attention_bad_pages_and_lengths(gpu_lib):
     """Positions without a page are not seen; lengths are clamped."""
     rng = np.random.default_rng(15)
