@@ -489,8 +489,9 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         }
       }
     }
-    // > 0 also for a scale of 0, so that a masked score of -inf stays -inf
-    const float kc = fmaxf(ks * kscale, FLT_MIN);
+    // > 0 also for a scale of 0, so that a masked score of -inf stays -inf; the
+    // smallest number there is, which leaves the other scores below 2^-33
+    const float kc = fmaxf(ks * kscale, 0x1p-149f);
     // bf16: the V scale enters as its logarithm (exact for a power of two)
     const float lvs = NP == 1 ? __builtin_amdgcn_logf(vs) : 0.f, per_vs = NP == 1 ? 1.f / vs : 1.f;
     const uint8_t* next_k = more ? k_rows(tile + kAWaves, pid_next) : nullptr;

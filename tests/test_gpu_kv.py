@@ -493,6 +493,23 @@ def test_attention_nodes_with_the_lowest_score(gpu_lib, D, N, lens, dtype):
     assert (out == 0).all() and (lse == -np.inf).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,D", [("e4m3", 64), ("int8", 256)])
+def test_attention_smallest_key_scales(gpu_lib, fmt, D, dtype):
+    """Queries next to 2^100 over blocks of the smallest K scales, and a scale
+    of 0 or next to it: scores are what they are, however small their factor."""
+    rng = np.random.default_rng(29)
+    lens, P, H, N = [24, 9], 16, 1, 3
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D)
+    q, q64 = _rand(rng, (2, N, 4, D), dtype)
+    q, q64 = q * 2.0 ** 97, q64 * 2.0 ** 97
+    none = (None, None)
+    for k_scale in (2.0 ** -126, 2.0 ** -140, 0.0):
+        c["k_scales"][table[0, :2]] = c["k_scales"][table[1, 0]] = k_scale
+        for scale in (0.125, 2.0 ** -12, -(2.0 ** -14), 0.0):
+            _check_attention(gpu_lib, c, table, lens, (q, q64), none, none, scale, dtype)
+
+
 def test_attention_bad_pages_and_lengths(gpu_lib):
     """Positions without a page are not seen; lengths are clamped."""
     rng = np.random.default_rng(15)
