@@ -481,7 +481,7 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
  * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights
  * are rounded to bf16 for the product with the values, and blocks whose V
- * scale is below 2^-86 count as zeros.  Values, and 1.5 * scale times a
+ * scale is below 2^-86 count as zeros (NaN stays).  Values, and 1.5 * scale times a
  * block's K scale, are to stay below 2^100, and scores below 2^127, before
  * and after the scale; a node's score may pass that range downwards: then
  * its weight is 0.  out and out_lse overlap no input.  The same call gives

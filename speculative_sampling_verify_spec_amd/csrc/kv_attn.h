@@ -80,6 +80,13 @@ __device__ inline bf16x8 codes8(uint32_t a, uint32_t b) {
   return u.v;
 }
 
+// The bytes of a word of codes that are NaN.
+template <int FMT>
+__device__ inline uint32_t nan_bytes(uint32_t w) {
+  if constexpr (FMT == SPECV_E4M3) return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
+  else return 0;
+}
+
 __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -473,6 +480,7 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
     // of no page, may be anything (NaN too) and are cleared.  So are values
     // whose block has next to no magnitude (blocks of zeros have the smallest
     // scale): a weight times such a scale could vanish from the weights' sum.
+    // NaN has no magnitude, and stays.
     const int have = pid < 0 ? 0 : min(max(len - tile * kTile - 16 * g, 0), 16);
     const bool flat = NP == 1 && !(vs >= kFlatScale);
     const bool whole = __all(have == 16 && !flat);
@@ -484,10 +492,17 @@ __global__ __launch_bounds__(kABlock, waves_per(DT, D, MT)) void k_kv_attn(KvAtt
         uint32_t* x = reinterpret_cast<uint32_t*>(&vraw[d]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int n = (flat ? 0 : have) - 4 * i;
+          const int n = have - 4 * i;
           x[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
         }
       }
+      if (__any(flat))
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(&vraw[d]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] &= flat ? nan_bytes<FMT>(x[i]) : ~0u;
+        }
     }
     // > 0 also for a scale of 0, so that a masked score of -inf stays -inf; the
     // smallest number there is, which leaves the other scores below 2^-33

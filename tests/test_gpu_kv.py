@@ -510,6 +510,37 @@ def test_attention_smallest_key_scales(gpu_lib, fmt, D, dtype):
             _check_attention(gpu_lib, c, table, lens, (q, q64), none, none, scale, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_attention_keeps_nan_of_tiny_blocks(gpu_lib, D, dtype):
+    """NaN appended among zeros, among values next to nothing and as a whole
+    block reaches every query, in its channels only; NaN in the slots behind
+    the last token reaches none."""
+    import torch
+    rng = np.random.default_rng(30)
+    P, H, N, T = 32, 2, 3, 120
+    lens = [T, 70, 33, 1]
+    c, table = kh.make_cache(rng, "e4m3", [0] * 4, P, H, D, extra=T)
+    (k, k64), (v, _) = _rand(rng, (4, T, H, D), dtype), _rand(rng, (4, T, H, D), dtype)
+    v[0, 32:64], v[0, 64:96] = 0.0, 2.0 ** -110
+    v[0, 40, 0, 5], v[0, 47, 1, 6], v[0, 64, 1, D - 1] = np.nan, np.nan, np.nan
+    v[1, 64:], v[2, 32:], v[3] = np.nan, 0.0, 0.0
+    v[2, 32, 0, 17] = np.nan
+    v64 = v.double().cpu().numpy()
+    dev, tab = kh.to_device(gpu_lib, c), _i32(table)
+    after = gpu_lib.kv_append(dev, tab, k, v, _i32([0] * 4), counts=_i32(lens))
+    assert after.tolist() == okv.append(c, table, k64, v64, [0] * 4, lens).tolist() == lens
+    q = _rand(rng, (4, N, 8, D), dtype)
+    kn, vn = _rand(rng, (4, N, H, D), dtype), _rand(rng, (4, N, H, D), dtype)
+    for new in ((kn, vn), ((None, None), (None, None))):
+        out, _ = _check_attention(gpu_lib, c, table, lens, q, *new, D ** -0.5, dtype, dev=dev)
+        nan = out.isnan().all(1)  # [sequence, head, channel]: every node
+        assert torch.equal(nan, out.isnan().any(1))
+        want = torch.zeros_like(nan)
+        want[0, :4, 5], want[0, 4:, 6], want[0, 4:, D - 1], want[1], want[2, :4, 17] = True, True, True, True, True
+        assert torch.equal(nan, want)
+
+
 def test_attention_bad_pages_and_lengths(gpu_lib):
     """Positions without a page are not seen; lengths are clamped."""
     rng = np.random.default_rng(15)
