@@ -383,6 +383,7 @@ int spec_ngram_map_update(void* tables, int capacity, const int32_t* history, co
  * code * scale.  spec_kv_append writes scales that are powers of two, the
  * smallest that brings the block's largest magnitude into the format's
  * range; spec_kv_read and spec_kv_attention take any finite scale >= 0.
+ * All three calls are forward only: there are no gradients.
  */
 typedef enum {
   SPECV_E4M3 = 0, /* 8-bit float, 4 exponent and 3 fraction bits, no infinities, largest value 448 */

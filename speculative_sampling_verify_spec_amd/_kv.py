@@ -15,13 +15,36 @@ KV_DIMS = (64, 96, 128, 256)
 
 
 torch = None  # bound by the first cache: the package imports without it, and every call here has a cache
+_ForwardOnly = None
 
 
 def _bind_torch() -> None:
-    global torch
+    global torch, _ForwardOnly
     if torch is None:
         import torch as t
-        torch = t
+
+        class ForwardOnly(t.autograd.Function):
+            """Hands results through; a backward pass that reaches them is an error."""
+
+            @staticmethod
+            def forward(ctx, n, *tensors):
+                return tensors[:n]
+
+            @staticmethod
+            def backward(ctx, *grads):
+                raise NotImplementedError("kv_attention is forward only: it has no gradients")
+
+        torch, _ForwardOnly = t, ForwardOnly
+
+
+def _forward_only(results, inputs):
+    """The results; where autograd follows the inputs, tied to them, so that
+    gradients are refused and not left out."""
+    if torch.is_grad_enabled():
+        inputs = [t for t in inputs if t is not None and t.requires_grad]
+        if inputs:
+            return _ForwardOnly.apply(len(results), *results, *inputs)
+    return results
 
 
 class KVCache:
@@ -173,7 +196,7 @@ def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=N
     the first entry outside [0, N): the path of verify_tree_greedy), int32.
     Returns the tokens cached after the call, [B] int32 (out_lengths if given,
     which overlaps none of the other int32 tensors; lengths itself is left as
-    it is, so every layer can pass it)."""
+    it is, so every layer can pass it).  The cache holds no gradients."""
     _check_table(cache, page_table)
     B, width = page_table.shape
     if k.dim() != 4:
@@ -237,7 +260,8 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
     bf16 or fp32), Hq a multiple of heads; lengths [B] cached tokens,
     parents [B, N] the nodes' tree (None: a chain), num_nodes [B] the nodes of
     each sequence, int32; scale defaults to dim ** -0.5.  Returns out [B, N,
-    Hq, dim] and, when asked, lse [B, N, Hq] float32."""
+    Hq, dim] and, when asked, lse [B, N, Hq] float32.  Forward only: a
+    backward pass through the results raises NotImplementedError."""
     _check_table(cache, page_table)
     B, width = page_table.shape
     if q.dim() != 4:
@@ -276,4 +300,5 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
     _call(cache._device, lib.spec_kv_attention, kv, q.data_ptr(), q_row, _ptr(k_new), _ptr(v_new), kv_row,
           lengths.data_ptr(), _ptr(num_nodes), _ptr(parents), dim ** -0.5 if scale is None else float(scale), B, N,
           Hq, out.data_ptr(), _ptr(lse), code, workspace.data_ptr(), have)
-    return (out, lse) if return_lse else out
+    results = _forward_only((out, lse) if return_lse else (out,), (q, k_new, v_new))
+    return results if return_lse else results[0]

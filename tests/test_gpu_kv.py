@@ -788,6 +788,28 @@ def test_misaligned_rows_are_refused(gpu_lib):
                           torch.zeros(2, 1, 1, 64, device="cuda"), _i32([0, 0, 0])[:2], out_lengths=both.new_zeros(2)[1:])
 
 
+def test_gradients_are_refused(gpu_lib):
+    """Queries, keys or values that require gradients: the same values, and a
+    backward pass through them raises."""
+    import torch
+    rng = np.random.default_rng(31)
+    lens, P, H, D, N = [40, 5], 16, 2, 64, 3
+    c, table = kh.make_cache(rng, "int8", lens, P, H, D)
+    dev, tab, ln = kh.to_device(gpu_lib, c), _i32(table), _i32(lens)
+    x = [_rand(rng, (2, N, h, D), "f32")[0] for h in (4, H, H)]
+    want = gpu_lib.kv_attention(dev, tab, x[0], ln, *x[1:], return_lse=True)
+    assert not any(t.requires_grad for t in want)
+    for i in range(3):
+        y = [t.clone().requires_grad_(j == i) for j, t in enumerate(x)]
+        got = gpu_lib.kv_attention(dev, tab, y[0], ln, *y[1:], return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for t in (got[0], got[1], gpu_lib.kv_attention(dev, tab, y[0], ln, *y[1:])):
+            with pytest.raises(NotImplementedError, match="forward only"):
+                (t.sum() + y[i].sum()).backward()
+        with torch.no_grad():
+            assert not gpu_lib.kv_attention(dev, tab, y[0], ln, *y[1:]).requires_grad
+
+
 def test_overlapping_lengths_are_refused(gpu_lib):
     """New lengths over a part of any array the call reads; beside it they are fine."""
     import torch

@@ -190,6 +190,24 @@ def test_token_strides():
             f("x", bad, bad.shape[2], bad.shape[3])
 
 
+def test_forward_only():
+    """Results that follow inputs with gradients refuse a backward pass; their
+    values, and results without such inputs, are left as they are."""
+    _kv._bind_torch()
+    out, lse = torch.randn(3, 4), torch.randn(3)
+    a, b = torch.randn(2, requires_grad=True), torch.randn(2)
+    assert _kv._forward_only((out, lse), (b, None, b)) == (out, lse)
+    with torch.no_grad():
+        assert _kv._forward_only((out, lse), (a, None, b)) == (out, lse)
+    for inputs in ((a, None, None), (b, b, a)):
+        got = _kv._forward_only((out, lse), inputs)
+        assert all(torch.equal(g, t) and g.requires_grad for g, t in zip(got, (out, lse)))
+        for g in got:
+            with pytest.raises(NotImplementedError, match="forward only"):
+                (g.sum() + a.sum()).backward()
+    assert not out.requires_grad and a.grad is None
+
+
 def test_build_finds_spills():
     from speculative_sampling_verify_spec_amd.build import _spills
     line = "k.hip:3:1: remark: {} [-Rpass-analysis=kernel-resource-usage]\n"
