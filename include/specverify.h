@@ -399,7 +399,7 @@ typedef struct {
   int num_pages;   /* pages in k_pages and v_pages */
   int max_pages;   /* columns of page_table; max_pages * page_size < 2^31 */
   int page_size;   /* 16, 32, 64 or 128 tokens */
-  int heads;       /* cached (key and value) heads */
+  int heads;       /* cached (key and value) heads, at most 32767 */
   int dim;         /* 64, 96, 128 or 256 */
   int type;        /* specv_kvtype_t */
 } specv_kv_t;      /* read on the host during the call; the arrays are device memory */
@@ -476,8 +476,11 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   parents     [B][N] int32 (device) or NULL: a chain; read when k_new is given
  *   scale       any sign; finite, also when multiplied by 1.5
  *   out         [B][N][Hq][dim] (dtype);  out_lse [B][N][Hq] float or NULL
- *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq a multiple of heads, at
- *               most SPECV_KV_MAX_GROUP times as many
+ *   1 <= N <= SPECV_MAX_TREE;  B <= 65535;  Hq <= 32767, a multiple of
+ *               heads and at most SPECV_KV_MAX_GROUP times as many;
+ *               B * N * Hq < 2^26 and (B * heads + 7) * ceil(N * Hq / (16 *
+ *               heads)) < 2^24 (larger calls: SPECV_E_SHAPE, but for some
+ *               past the second limit)
  *   q, k_new, v_new and out 16-byte aligned
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
  * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights

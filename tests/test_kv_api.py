@@ -141,6 +141,23 @@ def test_workspace_sizes(lib):
         assert lib.spec_kv_attention_workspace_size(ctypes.byref(kv()), B, N, Hq) == 0
 
 
+def test_largest_attention_calls(lib):
+    """The limits that the header states: the last size inside has a
+    workspace size in both types' plans, whatever the table, the first outside is refused."""
+    def size(B, N, Hq, **kw):
+        return lib.spec_kv_attention_workspace_size(ctypes.byref(kv(**kw)), B, N, Hq)
+    for pages, P in ((1, 16), ((1 << 24) - 1, 128)):
+        for dim in (64, 96, 128, 256):
+            t = dict(max_pages=pages, page_size=P, dim=dim)
+            assert size(1023, 64, 1024, heads=1, **t) > 0 and size(1024, 64, 1024, heads=1, **t) == 0
+            assert size(32767, 1, 512, heads=512, **t) > 0
+            assert size(1, 64, 32767, heads=32767, **t) > 0 and size(1, 1, 32768, heads=32767, **t) == 0
+            assert size(8191, 1, 8192, heads=8, **t) > 0 and size(8192, 1, 8192, heads=8, **t) == 0
+    assert size(32768, 1, 512, heads=512) == 0  # 2^24 workgroups
+    assert attend(lib, kv(heads=1), B=1024, N=64, Hq=1024) == -2
+    assert attend(lib, kv(heads=512), B=32768, N=1, Hq=512) == -2
+
+
 def _parts(pages=4, h=2, p=16, d=64, dtype=torch.int8):
     return [torch.zeros(pages, h, p, d, dtype=dtype), torch.zeros(pages, h, d, p, dtype=dtype),
             torch.zeros(pages, h), torch.zeros(pages, h)]
