@@ -133,7 +133,7 @@ int spec_kv_append(const specv_kv_t* kv, const void* k, const void* v, int64_t r
   p.B = B;
   p.N = N;
   p.out_lengths = out_lengths;
-  p.per = kv_append_per(N, p.c.P);
+  p.groups = kv_append_groups(N, p.c.P);
   return launch_kv_append(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK
                                                                                              : SPECV_E_HIP;
 }

@@ -55,10 +55,10 @@ __device__ inline void item_of(int isv, unsigned i, int a0, unsigned na, unsigne
   v = static_cast<int>(isv ? q : r);
 }
 
-// A workgroup of NW waves takes one head of one sequence, in p.per
-// consecutive pages that the call may touch: its K and V with one item per
-// thread, one of them with NI items.  The values stay in registers between the
-// search for the largest magnitude and the quantisation.
+// A workgroup of NW waves takes one head of one sequence, in an equal share of
+// consecutive pages of those that its tokens touch: its K and V with one item
+// per thread, one of them with NI items.  The values stay in registers between
+// the search for the largest magnitude and the quantisation.
 //
 // Five waves a SIMD with one item a thread: 95 registers; left to itself the
 // compiler takes 120 (256 x 32 tokens 23.2 us against 24.5), six waves spill.
@@ -81,12 +81,16 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
   // workgroup's last (all of them, where the new length is written)
   const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && p.out_lengths;
   const int col0 = len >> c.pshift;
-  const int first = static_cast<int>(blockIdx.x) * p.per;  // this workgroup's first page, from col0 on
-  int stop = n;
+  int stop = n, first = 0, per = 1;  // this workgroup's first page, from col0 on, and how many
   if (n > 0) {
-    const int end = (len + n - 1) >> c.pshift;
-    if (!reports && first > end - col0) return;
-    const int last = reports ? end : min(end, col0 + first + p.per - 1);
+    // shares of the pages that this sequence's tokens can touch, not of the
+    // call's: a call padded to many more keeps its workgroups busy (1000 tokens
+    // of 131072, pages of 16: 9.4 us, in shares of the call's pages 30)
+    const int end = (len + n - 1) >> c.pshift, groups = gridDim.x;
+    if (end - col0 >= groups) per = (end - col0 + groups) / groups;
+    first = static_cast<int>(blockIdx.x) * per;
+    if (first > end - col0) return;
+    const int last = reports ? end : min(end, col0 + first + per - 1);
     const int upto = last == end ? n : ((last + 1) << c.pshift) - len;  // tokens up to there
     const int i0 = min(tid, upto - 1), c0 = min(col0 + tid, last);  // both loads before either test
     const int ix0 = p.index ? p.index[b * p.N + i0] : 0, id0 = c.table[b * c.width + c0];
@@ -112,11 +116,12 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
 
   const int vpr = c.D / E;
   const int wave0 = __builtin_amdgcn_readfirstlane(tid) & ~(kWave - 1);  // the wave's first item
-  const long col1 = static_cast<long>(col0) + first + p.per;
-  for (long col = col1 - p.per; col < col1 && (col << c.pshift) < static_cast<long>(len) + n; ++col) {
+  // the tokens of its pages end here
+  const long stop_at = min(static_cast<long>(len) + n, (static_cast<long>(col0) + first + per) << c.pshift);
+  for (long col = static_cast<long>(col0) + first; (col << c.pshift) < stop_at; ++col) {
     const long p0 = col << c.pshift;                                            // the page's first position
     const int t0 = static_cast<int>(max(len - p0, 0L));                         // tokens of it cached before
-    const int t1 = static_cast<int>(min(len + n - p0, static_cast<long>(c.P)));  // and after
+    const int t1 = static_cast<int>(min(stop_at - p0, static_cast<long>(c.P)));  // and after
     const long blk = static_cast<long>(kv_page(c, b, col)) * c.H + h;  // a page: n ends before the first that is not
     // only the groups of four tokens that get new ones
     const int a0 = t0 / 4, na = (t1 + 3) / 4 - a0, items = na * vpr;
@@ -365,13 +370,12 @@ hipError_t append(const KvAppend& p, hipStream_t st) {
   // items of a page that N tokens can touch, wherever they begin: at most 2048
   const int items = std::min(p.c.P / 4, (std::min(p.N, p.c.P) + 6) / 4) * (p.c.D / Elt<DT>::kPerVec);
   const unsigned H = static_cast<unsigned>(p.c.H), B = static_cast<unsigned>(p.B);
-  const unsigned gx = (kv_slots(p.N, p.c.P) + p.per - 1) / p.per;
   // K and V in one workgroup share the table, index and length reads: 256 x 6
   // tokens by four waves 13.9 us, apart 17.3 (D = 128, P = 64).  With two items a
   // thread the registers count for more: 64 x 100 tokens (D = 128, P = 128) 16.0 us
   // together, 14.3 apart, 4 x 4096 23.8 and 22.4, but 256 x 64 34.2 and 37.0.
 #define LAUNCH(ni, nw) \
-  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, nw>), dim3(gx, ni == 1 ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
+  hipLaunchKernelGGL((k_kv_append<DT, FMT, ni, nw>), dim3(p.groups, ni == 1 ? H : 2 * H, B), dim3(nw * kWave), 0, st, p)
   // No more waves than items.  One wave: 256 x 9 tokens (P = 64, 8 heads of 128) 10.4 us, by
   // four waves 13.8; 256 x 1 9.7 and 13.2; 64 x 9 7.0 and 7.5, but 14.4 and 12.6
   // if every block's scale grows.  More in turns of one wave queue up: 256

@@ -32,7 +32,7 @@ struct KvAppend {
   const int32_t* index;   // or null
   int B, N;
   int32_t* out_lengths;   // or null
-  int per;                // pages a workgroup takes (kv_append_per)
+  unsigned groups;        // workgroups that share a head's pages (kv_append_groups)
 };
 
 struct KvRead {
@@ -83,19 +83,17 @@ __host__ __device__ inline int kv_parts(int ntile, int granule) {
 // Pages that n consecutive tokens can touch, whatever position they start at.
 inline unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 2) / P + 1); }
 
-// Workgroups of one head of one sequence in an append, at most.  Each looks
-// through the call's pages and indexes up to its own last one, so their number
-// bounds the entries looked at for a token (131072 tokens of 8 heads of 64 in
-// pages of 16: 131 us, with a workgroup for each of the 8193 pages 186; by
-// index, every workgroup to the end of it, 350 and 1458).
+// Workgroups of one head of one sequence in an append.  Each looks through
+// the call's pages and indexes up to its own last one, so their number bounds
+// the entries looked at for a token (131072 tokens of 8 heads of 64 in pages of
+// 16: 127 us, with a workgroup for each of the 8193 pages 186; by index, every
+// workgroup to the end of it, 362 and 1458).  A few tokens rarely cross into a
+// second page: one workgroup takes both (256 x 6 tokens by four waves: 13.9 us,
+// with one per page 21.6).
 constexpr unsigned kMaxAppendGroups = 1024;
-
-// Consecutive pages that a workgroup of the append takes.  A few tokens
-// rarely cross into a second page: one workgroup takes both (256 x 6 tokens by
-// four waves: 13.9 us, with one per page 21.6).
-inline int kv_append_per(int N, int P) {
+inline unsigned kv_append_groups(int N, int P) {
   const unsigned slots = kv_slots(N, P);
-  return slots <= 2 ? 2 : static_cast<int>((slots + kMaxAppendGroups - 1) / kMaxAppendGroups);
+  return slots <= 2 ? 1 : slots < kMaxAppendGroups ? slots : kMaxAppendGroups;
 }
 
 // Launchers, next to their kernels.  dtype: SPECV_F32 or SPECV_BF16; fmt:

@@ -253,15 +253,14 @@ hipError_t launch_kv_append(const KvAppend& p, int, int, hipStream_t) { seen = p
 hipError_t launch_kv_read(const KvRead&, int, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_kv_attention(const KvAttn&, int, int, hipStream_t) { return hipSuccess; }
 }
-extern "C" int pages_per_group() { return sv::seen.per; }
+extern "C" int groups() { return sv::seen.groups; }
 extern "C" unsigned page_slots() { return sv::kv_slots(sv::seen.N, sv::seen.c.P); }
 """
 
 
 def test_append_work_is_linear_in_the_tokens(tmp_path):
     """A workgroup of the append looks through the call's pages and indexes up
-    to its own last one.  Its pages cover the call, and a head's workgroups
-    look at no more than 1024 entries for each token, up to the longest call
+    to its own last one.  A head's workgroups look at no more than 1024 entries for each token, up to the longest call
     (with a workgroup for every page: 2^39 pages and 2^43 indexes)."""
     gxx = shutil.which("g++")
     if not gxx:
@@ -281,10 +280,9 @@ def test_append_work_is_linear_in_the_tokens(tmp_path):
         for N in (1, 2, P, P + 1, P + 2, 8191, 1 << 14, (1 << 14) + 17, 131072, 999999, 1 << 24):
             c = kv(page_size=P, max_pages=(1 << 24) // P + 2)
             assert plan.spec_kv_append(ctypes.byref(c), BASE, BASE, 0, BASE, None, BASE, 1, N, None, BF16, None) == 0
-            per, slots = plan.pages_per_group(), plan.page_slots()
-            assert slots == (N + P - 2) // P + 1 and per >= 1
-            groups = -(-slots // per)
-            assert groups * per >= slots
+            groups, slots = plan.groups(), plan.page_slots()
+            assert slots == (N + P - 2) // P + 1 and 1 <= groups <= slots
+            per = -(-slots // groups)  # each takes an equal share
             pages = sum(min(slots, (g + 1) * per) for g in range(groups))
             indexes = sum(min(N, (g + 1) * per * P) for g in range(groups))
             assert pages <= 1024 * slots and indexes <= 1024 * N
