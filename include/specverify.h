@@ -484,13 +484,13 @@ int spec_kv_read(const specv_kv_t* kv, const int32_t* starts, const int32_t* len
  *   q, k_new, v_new and out 16-byte aligned
  *   workspace   spec_kv_attention_workspace_size() bytes, 256-byte aligned
  * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights
- * are rounded to bf16 for the product with the values, and blocks whose V
- * scale is below 2^-86 count as zeros (NaN stays).  Values, and 1.5 * scale times a
- * block's K scale, are to stay below 2^100, and scores below 2^127, before
- * and after the scale; a node's score may pass that range downwards: then
- * its weight is 0.  out and out_lse overlap no input.  The same call gives
- * the same bits.  Returns the SPECV_* codes of spec_verify; nothing
- * synchronises.
+ * are rounded to bf16 for the product with the values, blocks whose V scale
+ * is below 2^-86 count as zeros (NaN stays), and terms below 2^-117 may.
+ * Values, and 1.5 * scale times a block's K scale, are to stay below 2^100,
+ * and scores below 2^127, before and after the scale; a node's score may pass
+ * that range downwards: then its weight is 0.  out and out_lse overlap no
+ * input.  The same call gives the same bits.  Returns the SPECV_* codes of
+ * spec_verify; nothing synchronises.
  */
 size_t spec_kv_attention_workspace_size(const specv_kv_t* kv, int B, int N, int Hq);
 

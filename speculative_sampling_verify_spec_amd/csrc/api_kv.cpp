@@ -66,10 +66,11 @@ struct KvPlan {
   int mt, mb, granule, splits;
 };
 
-// Workgroups to aim at: two on each of 256 CUs.  More parts mean more of the
-// parts' own cost, their queries and their sums: 2 x 5 positions over 131072
-// tokens take 123 us at 512, 155 at 2048; 64 x 6 over 301-2111 tokens 46 and
-// 67 us; 512 x 1 with heads of 256 240 and 268.
+// Workgroups to aim at.  Fewer leave CUs idle, more mean more of the parts'
+// own cost, their queries and their sums (us, at 256 / 512 / 1024 / 2048): 2 x
+// 5 positions over 131072 tokens 125, 111, 121, 137; 64 x 6 over 301-2111
+// 41, 41, 54, 50; 16 x 9 in fp32 over 65-2900 29.2, 27.1, 26.8, 26.7; 512 x 1
+// with heads of 256 223, 222, 224, 276.
 constexpr long kTargetGroups = 512;
 // Tiles per part: four for each wave.  Fewer would need a second launch for
 // the join: 1 x 1 over 1000 tokens takes 12.4 us in one part of 16 tiles and
