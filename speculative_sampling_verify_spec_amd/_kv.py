@@ -28,6 +28,7 @@ def _bind_torch() -> None:
 
             @staticmethod
             def forward(ctx, n, *tensors):
+                ctx.mark_dirty(*tensors[:n])  # the tensors themselves, not views of them, which refuse in-place work
                 return tensors[:n]
 
             @staticmethod

@@ -217,12 +217,17 @@ def test_forward_only():
     with torch.no_grad():
         assert _kv._forward_only((out, lse), (a, None, b)) == (out, lse)
     for inputs in ((a, None, None), (b, b, a)):
-        got = _kv._forward_only((out, lse), inputs)
-        assert all(torch.equal(g, t) and g.requires_grad for g, t in zip(got, (out, lse)))
+        given = (out.clone(), lse.clone())
+        got = _kv._forward_only(given, inputs)
+        assert all(torch.equal(g, t) and g.requires_grad and g is x for g, t, x in zip(got, (out, lse), given))
         for g in got:
             with pytest.raises(NotImplementedError, match="forward only"):
                 (g.sum() + a.sum()).backward()
-    assert not out.requires_grad and a.grad is None
+        got[0].mul_(2.0)  # in place, as results without gradients take it
+        assert torch.equal(got[0], 2.0 * out)
+        with pytest.raises(NotImplementedError, match="forward only"):
+            got[0].sum().backward()
+    assert a.grad is None
 
 
 def test_build_finds_spills():
