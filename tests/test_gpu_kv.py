@@ -108,6 +108,33 @@ def test_append_special_values(gpu_lib, fmt):
     _same_cache(kh.to_host(dev, fmt), c)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,N,D", [("e4m3", 3, 64), ("int8", 3, 96), ("e4m3", 40, 256)])
+def test_append_keeps_nan_and_reads_no_padding(gpu_lib, fmt, N, D, dtype):
+    """NaN codes of a begun block stay NaN when its scale grows, by a little
+    and from 0 or next to nothing; tokens behind counts hold anything."""
+    import torch
+    rng = np.random.default_rng(33)
+    lens, P, H = [7, 9, 31, 5], 32, 2
+    c, table = kh.make_cache(rng, fmt, lens, P, H, D, extra=N)
+    if fmt == "e4m3":
+        for b, n in enumerate(lens):
+            c["k_pages"][table[b, 0], :, n // 2], c["v_pages"][table[b, 0], :, 3, :n] = 127, 255
+    for b, s in ((1, 0.0), (3, 2.0 ** -126)):
+        c["k_scales"][table[b, 0]] = c["v_scales"][table[b, 0]] = s
+    x = (rng.normal(size=(2, 4, N, H, D)) * 1e3).astype(np.float32)
+    counts = np.array([N, 1, N - 1, 2])
+    k, v = (torch.from_numpy(t).to(_dt(dtype)) for t in x)
+    k64, v64 = k.double().numpy(), v.double().numpy()
+    for t in (k, v):
+        t[torch.arange(N) >= torch.from_numpy(counts)[:, None]] = float("nan")
+    dev = kh.to_device(gpu_lib, c)
+    got = gpu_lib.kv_append(dev, _i32(table), k.cuda(), v.cuda(), _i32(lens), counts=_i32(counts))
+    want = okv.append(c, table, k64, v64, lens, counts)
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    _same_cache(kh.to_host(dev, fmt), c)
+
+
 @pytest.mark.parametrize("fmt,dtype,P,D", [("e4m3", "bf16", 128, 128), ("int8", "f32", 128, 128), ("e4m3", "f32", 64, 256),
                                            ("int8", "bf16", 32, 96), ("e4m3", "bf16", 64, 256)])
 @pytest.mark.parametrize("N", [1, 2, 4, 5, 9, 13, 14, 22])
@@ -786,6 +813,43 @@ def test_misaligned_rows_are_refused(gpu_lib):
     with pytest.raises(ValueError):
         gpu_lib.kv_append(dev, torch.cat((tab, tab)), torch.zeros(2, 1, 1, 64, device="cuda"),
                           torch.zeros(2, 1, 1, 64, device="cuda"), _i32([0, 0, 0])[:2], out_lengths=both.new_zeros(2)[1:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,N,G", [(64, 5, 3), (128, 20, 4), (256, 33, 1)])
+def test_padding_may_hold_anything(gpu_lib, D, N, G, dtype):
+    """A padded batch: queries, keys and values of nodes that do not exist,
+    and table columns behind a sequence's pages that name pages of NaN, reach
+    no other query; a live query of NaN reaches itself only."""
+    import torch
+    rng = np.random.default_rng(32)
+    P, H = 16, 2
+    lens, nodes = [0, 33, 5000, 17, 100], [1, N, N - 2, 0, 3]
+    c, table = kh.make_cache(rng, "e4m3", lens, P, H, D, spare=40)
+    dev, ln, nn = kh.to_device(gpu_lib, c), _i32(lens), _i32(nodes)
+    q, k, v = (_rand(rng, (5, N, h, D), dtype)[0] for h in (H * G, H, H))
+    par = _i32(_tree(rng, 5, N))
+    want = gpu_lib.kv_attention(dev, _i32(table), q, ln, k, v, parents=par, num_nodes=nn, return_lse=True)
+    wild = table.copy()
+    poisoned = np.setdiff1d(np.arange(c["k_pages"].shape[0]), table)
+    for b, n in enumerate(lens):
+        free = wild[b, (n + P - 1) // P:]
+        free[:] = rng.choice(poisoned, free.shape)
+    live = torch.arange(N, device="cuda") < nn[:, None]
+    q2, k2, v2 = (torch.where(live[..., None, None], t, float("nan")) for t in (q, k, v))
+    for val in (float("nan"), float("inf")):
+        for t in (q2, k2, v2):
+            t[~live] = val
+        got = gpu_lib.kv_attention(dev, _i32(wild), q2, ln, k2, v2, parents=par, num_nodes=nn, return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (got[0][~live] == 0).all() and (got[1][~live] == -np.inf).all()
+    q2 = q.clone()
+    q2[1, N - 1, 1], q2[2, 0, 0] = float("nan"), float("inf")
+    got = gpu_lib.kv_attention(dev, _i32(table), q2, ln, k, v, parents=par, num_nodes=nn, return_lse=True)
+    hit = torch.zeros(got[1].shape, dtype=torch.bool, device="cuda")
+    hit[1, N - 1, 1], hit[2, 0, 0] = True, True
+    assert all(torch.equal(a[~hit], b[~hit]) for a, b in zip(got, want))
+    assert got[0][hit].isnan().all()
 
 
 def test_gradients_are_refused(gpu_lib):
