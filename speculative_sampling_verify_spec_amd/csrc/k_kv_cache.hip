@@ -97,7 +97,7 @@ __global__ __launch_bounds__(NW * kWave, NI == 1 ? 5 : 1) void k_kv_append(KvApp
     if (ix0 < 0 || ix0 >= p.N) stop = min(stop, i0);
     if (id0 < 0 || id0 >= c.pages) stop = min(stop, max((c0 << c.pshift) - len, 0));
     // long calls: the loads of several turns go out together (131072 tokens
-    // of 8 heads of 64 in pages of 16: 131 us, one by one 163; by index 350 and 947)
+    // of 8 heads of 64 in pages of 16: 130 us, one by one 165; by index 362 and 928)
     if (p.index)
 #pragma unroll 8
       for (int i = tid + kThreads; i < upto; i += kThreads) {

@@ -86,7 +86,7 @@ inline unsigned kv_slots(long n, int P) { return static_cast<unsigned>((n + P - 
 // Workgroups of one head of one sequence in an append.  Each looks through
 // the call's pages and indexes up to its own last one, so their number bounds
 // the entries looked at for a token (131072 tokens of 8 heads of 64 in pages of
-// 16: 127 us, with a workgroup for each of the 8193 pages 186; by index, every
+// 16: 130 us, with a workgroup for each of the 8193 pages 186; by index, every
 // workgroup to the end of it, 362 and 1458).  A few tokens rarely cross into a
 // second page: one workgroup takes both (256 x 6 tokens by four waves: 13.9 us,
 // with one per page 21.6).
