@@ -499,6 +499,42 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
                       float scale, int B, int N, int Hq, void* out, float* out_lse, int dtype, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/*
+ * spec_prompt_attention - causal attention of whole prompts, packed: T token
+ * rows, of which sequence b has the rows starts[b] .. starts[b+1]-1 (starts
+ * are to ascend within [0, T]; whatever they hold, nothing outside the rows is
+ * read or written).  With G = Hq / heads query heads per key head, query
+ * (token i, head hq) sees the tokens j <= i of its own sequence in head hq / G:
+ *   s_j = scale * (q . k_j),  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
+ *   lse = ln sum_j e^(s_j).
+ * It is the pass of prompts whose keys and values spec_kv_append then caches
+ * ([C] 3.1: the prefix that a draft's nodes share).  Rows of no sequence get 0
+ * and -infinity.  What a query does not see never reaches it, whatever its
+ * memory holds.
+ *   q           [T] token rows of Hq*dim elements (dtype)
+ *   k, v        [T] token rows of heads*dim elements
+ *   q_stride, kv_stride  elements between token rows, multiples of 16 bytes;
+ *               0: contiguous (rows of a fused projection: their full length)
+ *   starts      [B + 1] int32 (device); sequences may be empty
+ *   scale       any sign; finite, also when multiplied by 1.5
+ *   out         [T][Hq][dim] (dtype);  out_lse [T][Hq] float or NULL
+ *   dim         64, 96, 128 or 256
+ *   1 <= T <= SPECV_KV_MAX_APPEND;  B <= 65535;  Hq <= 32767, a multiple of
+ *               heads and at most SPECV_KV_MAX_GROUP times as many;  T * Hq <
+ *               2^30 * heads and (ceil(T * Hq / (128 * heads)) + B) * heads <
+ *               2^24 (larger calls: SPECV_E_SHAPE)
+ *   q, k, v and out 16-byte aligned
+ * Sums and softmax statistics are in 32 bits; with SPECV_BF16 the weights are
+ * rounded to bf16 for the product with the values.  What a query sees is to be
+ * finite, values below 2^100 and scores below 2^127, before and after the
+ * scale.  out and out_lse overlap no input.  The same call gives the same
+ * bits.  Forward only.  Needs no workspace; nothing synchronises.  Returns
+ * the SPECV_* codes of spec_verify.
+ */
+int spec_prompt_attention(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                          const int32_t* starts, float scale, int B, int T, int heads, int Hq, int dim, void* out,
+                          float* out_lse, int dtype, void* stream);
+
 /* Device-side input validation, a debugging aid.  While it is on, every
  * spec_verify* call (spec_verify, _ex, _noalloc, _ragged, _ragged_ex) first
  * runs one more pass over the inputs it uses and adds what it finds to

@@ -14,7 +14,7 @@ KV_PAGE_SIZES = (16, 32, 64, 128)
 KV_DIMS = (64, 96, 128, 256)
 
 
-torch = None  # bound by the first cache: the package imports without it, and every call here has a cache
+torch = None  # bound by the first cache or prompt: the package imports without it
 _ForwardOnly = None
 
 
@@ -27,24 +27,25 @@ def _bind_torch() -> None:
             """Hands results through; a backward pass that reaches them is an error."""
 
             @staticmethod
-            def forward(ctx, n, *tensors):
+            def forward(ctx, name, n, *tensors):
+                ctx.name = name
                 ctx.mark_dirty(*tensors[:n])  # the tensors themselves, not views of them, which refuse in-place work
                 return tensors[:n]
 
             @staticmethod
             def backward(ctx, *grads):
-                raise NotImplementedError("kv_attention is forward only: it has no gradients")
+                raise NotImplementedError(f"{ctx.name} is forward only: it has no gradients")
 
         torch, _ForwardOnly = t, ForwardOnly
 
 
-def _forward_only(results, inputs):
+def _forward_only(results, inputs, name="kv_attention"):
     """The results; where autograd follows the inputs, tied to them, so that
     gradients are refused and not left out."""
     if torch.is_grad_enabled():
         inputs = [t for t in inputs if t is not None and t.requires_grad]
         if inputs:
-            return _ForwardOnly.apply(len(results), *results, *inputs)
+            return _ForwardOnly.apply(name, len(results), *results, *inputs)
     return results
 
 

@@ -1,0 +1,62 @@
+"""Binding of whole prompts (argument marshalling only): prompt_attention.
+Checks shapes and dtypes, allocates outputs with torch and passes device
+pointers plus torch's current stream of the tensors' device."""
+from __future__ import annotations
+
+from typing import Optional
+
+from . import _kv
+from ._kv import KV_DIMS, _bind_torch, _call, _dtype_code, _forward_only, _token_stride
+from ._lib import _ptr, load
+
+
+def _rows(name: str, t, T: int, dim: int, like) -> int:
+    """Elements between the token rows of t [T, heads, dim]."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != dim or t.device != like.device or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be [{T}, heads, {dim}], with q's dtype and on q's device")
+    return _token_stride(name, t.unsqueeze(0), t.shape[1], dim)
+
+
+def _packed(q, k, starts):
+    """Checks of packed prompts: (sequences, q's stride, k's stride, dtype's code)."""
+    if q.device.type != "cuda":
+        raise ValueError("q must be on a GPU")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, dim]")
+    T, Hq, dim = q.shape
+    if dim not in KV_DIMS:
+        raise ValueError(f"dim must be one of {KV_DIMS}, got {dim}")
+    code = _dtype_code(q.dtype)
+    q_row, kv_row = _rows("q", q, T, dim, q), _rows("k", k, T, dim, q)
+    heads = k.shape[1]
+    if Hq < 1 or heads < 1 or Hq % heads:
+        raise ValueError(f"q's {Hq} heads must be a multiple of k's {heads}")
+    if starts.dtype is not _kv.torch.int32 or starts.dim() != 1 or starts.shape[0] < 2 or starts.device != q.device or \
+            not starts.is_contiguous():
+        raise ValueError("starts must be a contiguous int32 [B + 1] tensor on q's device")
+    return starts.shape[0] - 1, q_row, kv_row, code
+
+
+def prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, return_lse: bool = False):
+    """Causal attention of whole prompts, packed (spec_prompt_attention).
+
+    q [T, Hq, dim], k and v [T, heads, dim] (bf16 or fp32; slices of a fused
+    projection's rows will do; k and v with the same strides), Hq a multiple of
+    heads; starts [B + 1] int32: sequence b has the rows starts[b] ..
+    starts[b+1]-1.  scale defaults to dim ** -0.5.  Returns out [T, Hq, dim]
+    and, when asked, lse [T, Hq] float32; rows of no sequence are 0 and
+    -infinity.  Forward only: a backward pass through the results raises
+    NotImplementedError."""
+    _bind_torch()
+    B, q_row, kv_row, code = _packed(q, k, starts)
+    T, Hq, dim = q.shape
+    if v.shape != k.shape or _rows("v", v, T, dim, q) != kv_row:
+        raise ValueError("k and v must have the same shape and strides")
+    out = _kv.torch.empty((T, Hq, dim), dtype=q.dtype, device=q.device)
+    lse = _kv.torch.empty((T, Hq), dtype=_kv.torch.float32, device=q.device) if return_lse else None
+    if T:
+        _call(q.device, load().spec_prompt_attention, q.data_ptr(), q_row, k.data_ptr(), v.data_ptr(), kv_row,
+              starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, k.shape[1], Hq, dim,
+              out.data_ptr(), _ptr(lse), code)
+    results = _forward_only((out, lse) if return_lse else (out,), (q, k, v), "prompt_attention")
+    return results if return_lse else results[0]

@@ -1,0 +1,366 @@
+// Causal attention of whole prompts (the kernel template; k_prompt_<dim>.hip
+// instantiate it).
+//
+// A workgroup takes 128 rows of one sequence and one key head; row r is query
+// head r % G of token r / G, so the G query heads that share a key head also
+// share its tiles, and a short prompt fills a block with all its heads.  A
+// wave has 32 of the rows as the columns of both products:
+//   S^T = K Q^T       A = 32 tokens x 16 channels,  B = 16 channels x 32 rows
+//   O^T += V^T P^T    A = 32 channels x 16 tokens,  B = 16 tokens x 32 rows
+// with v_mfma_f32_32x32x16_bf16.  A lane then has one row's scores, so that
+// the softmax needs one exchange between two lanes; and its scores of a tile
+// are, as they come, the B operand of the second product, for the order of
+// tokens in which the A operand is read.  That operand is V transposed, which
+// the transposing LDS read gives.
+//
+// The tiles of K and V pass through LDS, swizzled by 16 bytes so that neither
+// read meets bank conflicts; bf16 goes from memory to LDS without registers
+// between, the next tile while this one is worked on.
+//
+// Softmax: the running maximum is held per row and only moved when a tile
+// exceeds it by more than 2^8 (the weights then stay below 2^8, and the sums
+// are in 32 bits), so most tiles rescale nothing.  The weights are rounded to
+// bf16 for the product with the values, as the output is.
+//
+// 32-bit inputs: every operand is split into three bf16 pieces whose sum has
+// 24 bits; products take the six largest of nine pieces' products.
+#pragma once
+
+#include <cfloat>
+
+#include "sv_device.h"
+#include "sv_kv.h"
+#include "sv_mfma.h"
+#include "sv_prompt.h"
+
+namespace sv {
+
+namespace {
+
+using namespace frag;
+
+constexpr int kPBlock = 256;
+
+// Tokens of a tile, LDS buffers of tiles and waves a SIMD.
+template <int DT, int D> struct PromptShape {
+  static constexpr int tile = DT == SPECV_F32 || D == 256 ? 32 : 64;
+  static constexpr int buffers = DT == SPECV_F32 ? 1 : 2;
+  static constexpr int waves = DT == SPECV_F32 || D == 256 ? 1 : 2;
+};
+
+// Where the 16-byte piece c of a tile's row t stands in the row, for both
+// reads: eight rows' same piece (K), and four rows' same pair of pieces (V),
+// fall into different banks.
+template <int D>
+__device__ inline int swizzle(int t, int c) {
+  if constexpr (D == 96) return c ^ ((t >> 2) & 3);
+  else if constexpr (D == 64) return c ^ (2 * ((t >> 1) & 3));
+  else return c ^ (2 * (t & 7));
+}
+
+// 16 bytes a lane from memory straight to LDS: the wave's 1024 bytes from `to` on.
+__device__ inline void load_lds(const void* from, const void* to) {
+  typedef __attribute__((address_space(3))) const void* lds_ptr;
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)to)));
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt_attn(PromptAttn p) {
+  using Shape = PromptShape<DT, D>;
+  constexpr int NP = kPieces<DT>, NF = D / 16, ND = D / 32, BN = Shape::tile, NB = BN / 32, NC = D / 8;
+  constexpr int kPlane = BN * D;                 // elements of a tile's piece
+  constexpr int kAll = BN * NC, kLoads = (kAll + kPBlock - 1) / kPBlock;  // pieces of 8 elements of K (and of V): of the tile, of a thread
+  static_assert(DT == SPECV_F32 || kAll % kPBlock == 0, "whole loads");
+  const Packed& s = p.s;
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(s.H));
+  const unsigned place = blockIdx.x / static_cast<unsigned>(s.H);
+  const PromptBlock at = prompt_block<kPBlock>(s, place, s.G, kPromptRows);
+  const int tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int col = lane % 32, half = lane / 32;
+  if (at.block < 0) {
+    // tokens of no sequence (before the first and behind the last) see nothing
+    const int lead = min(max(s.starts[0], 0), s.T), tail = min(max(s.starts[s.B], lead), s.T);
+    const int gone = lead + s.T - tail;
+    const unsigned free = p.slots - at.used;
+    float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (long i = place - at.used; i < gone; i += free) {
+      const long tok = i < lead ? i : tail + (i - lead);
+      const long row = tok * s.Hq + static_cast<long>(h) * s.G;
+      for (int e = tid; e < s.G * D / 4; e += kPBlock) kv_store4<DT>(p.out, row * D + 4 * e, zero);
+      if (p.lse)
+        for (int e = tid; e < s.G; e += kPBlock) p.lse[row + e] = -INFINITY;
+    }
+    return;
+  }
+  const int len = at.last - at.first, rows = len * s.G;
+  const int row0 = at.block * kPromptRows, wrow = row0 + 32 * w;
+  const int r = min(wrow + col, rows - 1);  // a row that exists
+  const int tok = r / s.G, hq = h * s.G + (r - tok * s.G);
+
+  __shared__ __align__(16) __bf16 lk[Shape::buffers][NP * kPlane], lv[Shape::buffers][NP * kPlane];
+  __shared__ int wild;  // a value that is not finite was cleared
+
+  // ---- queries, negated where the scale is ----
+  const float kscale = fmaxf(fabsf(s.scale) * kLog2e, 0x1p-149f);  // > 0: a masked score stays -infinity
+  // fp32 with D = 256 keeps them whole and splits them in every tile: their
+  // pieces would take 192 registers
+  constexpr bool kWhole = DT == SPECV_F32 && D == 256;
+  bf16x8 q[kWhole ? 1 : NF][NP];
+  Raw8<DT> xq[NF];
+  {
+    const long base = (static_cast<long>(at.first) + tok) * s.q_row + static_cast<long>(hq) * D + 8 * half;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) xq[f].load(s.q, base + 16 * f);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      xq[f].negate(s.scale < 0.f);
+      if constexpr (!kWhole) xq[f].pieces(q[f]);
+    }
+  }
+
+  f32x16 o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float m = -FLT_MAX, l = 0.f;
+
+  // tokens seen by the workgroup's last and first row
+  const int last_tok = min(row0 + kPromptRows - 1, rows - 1) / s.G, first_tok = row0 / s.G;
+  const int ntile = last_tok / BN + 1;
+  const long kbase = static_cast<long>(at.first) * s.kv_row + static_cast<long>(h) * D;
+
+  auto offset = [&](int tile, int e) {
+    const int t = e / NC;
+    return kbase + static_cast<long>(min(tile * BN + t, len - 1)) * s.kv_row + 8 * swizzle<D>(t, e % NC);
+  };
+  // bf16: memory to LDS, whose rows hold the pieces in the swizzled order
+  auto request = [&](int tile, int buf) {
+    if constexpr (DT == SPECV_BF16) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const long a = offset(tile, tid + i * kPBlock);
+        const int to = 8 * (i * kPBlock + w * kWave);
+        load_lds(static_cast<const uint16_t*>(s.k) + a, &lk[buf][to]);
+        load_lds(static_cast<const uint16_t*>(s.v) + a, &lv[buf][to]);
+      }
+    }
+  };
+  // fp32: through registers, where an element becomes its pieces
+  auto fill = [&](int tile) {
+    if constexpr (DT == SPECV_F32) {
+      int thread = tid;
+      if constexpr (kWhole) asm volatile("" : "+v"(thread));
+#pragma unroll D == 256 ? 1 : kLoads
+      for (int i = 0; i < kLoads; ++i) {
+        const int e = thread + i * kPBlock;
+        if (kAll % kPBlock && e >= kAll) break;
+        const long a = offset(tile, e);
+        Raw8<DT> x, y;
+        x.load(s.k, a);
+        y.load(s.v, a);
+        bf16x8 f[NP];
+        x.pieces(f);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&lk[0][j * kPlane + 8 * e]) = f[j];
+        y.pieces(f);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&lv[0][j * kPlane + 8 * e]) = f[j];
+      }
+    }
+  };
+  // clears what is not finite among a tile's values in LDS
+  auto tame = [&](int buf) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = tid + i * kPBlock;
+      if (kAll % kPBlock && e >= kAll) break;
+      Raw8<SPECV_BF16> x;  // an element that is not finite is its own first piece
+      uint4* at = reinterpret_cast<uint4*>(&lv[buf][8 * e]);
+      x.w[0] = *at;
+      if (x.wild()) {
+        odd = true;
+        x.tame();
+        *at = x.w[0];
+      }
+    }
+    if (odd) wild = 1;
+  };
+  auto landed = [] {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  if (tid == 0) wild = 0;
+  request(0, 0);
+  if constexpr (DT == SPECV_BF16) landed();
+
+  for (int tile = 0; tile < ntile; ++tile) {
+    const int buf = Shape::buffers == 2 ? tile & 1 : 0;
+    const bool more = tile + 1 < ntile;
+    if constexpr (DT == SPECV_F32) {
+      fill(tile);
+      __syncthreads();
+    } else if (more) {
+      request(tile + 1, buf ^ 1);
+    }
+    if (tile * BN + BN - 1 > first_tok) {  // some rows do not see all of it
+      tame(buf);
+      lds_barrier();
+    }
+    // waves whose rows see nothing of the tile wait for the others
+    const int t0 = tile * BN;
+    const bool any = t0 * s.G < wrow + 32 && wrow < rows;
+    if (any) {
+      // the lane's places in LDS are computed in every tile where registers are short
+      int own = lane;
+      if constexpr (kWhole) asm volatile("" : "+v"(own));
+      // ---- scores: token 32 n + 8 (i / 4) + 4 half + i % 4 of the tile in register i ----
+      f32x16 sc[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[n][i] = 0.f;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        constexpr int kStep = kWhole ? 0 : 1;
+        if constexpr (kWhole) {
+          __builtin_amdgcn_sched_barrier(0);  // reads far ahead would not leave registers for the pieces
+          xq[f].hide();
+          xq[f].pieces(q[0]);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          bf16x8 a[NP];
+          const int t = 32 * n + own % 32;
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            a[j] = *reinterpret_cast<const bf16x8*>(&lk[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + own / 32)]);
+#pragma unroll
+          for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i <= z; ++i) sc[n] = mfma32(a[z - i], q[f * kStep][i], sc[n]);
+        }
+      }
+      if (t0 + BN - 1 > wrow / s.G) {  // some of the wave's rows do not see all of the tile
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (t0 + 32 * n + 8 * (i / 4) + 4 * half + i % 4 > tok) sc[n][i] = -INFINITY;
+      }
+      float x = sc[0][0];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x = fmaxf(x, sc[n][i]);
+      x *= kscale;
+      if (__any(x > m + 8.f)) {
+        x = halves_max(x);
+        const bool need = x > m + 8.f;  // each row decides for itself, so that its bits do not depend on its neighbours
+        const float a = need ? ex2(m - x) : 1.f;
+        m = need ? x : m;
+        l *= a;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] *= a;
+      }
+      bf16x8 pf[NB * 2][NP];
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = ex2(fmaf(sc[n][i], kscale, -m));
+          sum += e;
+          __bf16 piece[3];
+          split<NP>(e, piece);
+#pragma unroll
+          for (int j = 0; j < NP; ++j) pf[2 * n + i / 8][j][i % 8] = piece[j];
+        }
+      l += sum;
+      // ---- values: slots 0..3 of half h hold tokens 16 c + 4 h .., 4..7 those 8 further ----
+#pragma unroll
+      for (int c = 0; c < 2 * NB; ++c)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          bf16x8 a[NP];
+          const int t = 16 * c + 4 * (own / 32) + (own % 16) / 4, piece = 4 * d + 2 * ((own / 16) % 2) + (own % 4) / 2;
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+            const __bf16* lo = &lv[buf][j * kPlane + t * D + 8 * swizzle<D>(t, piece) + 4 * (own % 2)];
+            const __bf16* hi = &lv[buf][j * kPlane + (t + 8) * D + 8 * swizzle<D>(t + 8, piece) + 4 * (own % 2)];
+            const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lo));
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(hi));
+            a[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+          }
+#pragma unroll
+          for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i <= z; ++i) o[d] = mfma32(a[z - i], pf[c][i], o[d]);
+        }
+      if (wild) {
+        // values that are not finite must not meet a weight of 0: they were
+        // left out, and are added where they are seen
+#pragma unroll 1
+        for (int j = 0; j < BN && t0 + j < len; ++j) {
+          float e = 0.f;
+#pragma unroll
+          for (int c = 0; c < 2 * NB; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (16 * c + 8 * (i / 4) + 4 * half + i % 4 == j) e = static_cast<float>(pf[c][0][i]);
+          e = halves_sum(e);
+          const long a = kbase + static_cast<long>(t0 + j) * s.kv_row + 4 * half;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              // few loads at a time: this rare part's registers count for the whole kernel
+              if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+              const long k = a + 32 * d + 8 * (i / 4) + i % 4;
+              float y;
+              if constexpr (DT == SPECV_F32) y = static_cast<const float*>(s.v)[k];
+              else y = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(s.v)[k]) << 16);
+              if (!isfinite(y) && t0 + j <= tok) o[d][i] += e * y;
+            }
+        }
+      }
+    }
+    landed();
+  }
+
+  l = halves_sum(l);
+  const bool there = wrow + col < rows, some = !(l == 0.f);
+  const float inv = some ? 1.f / l : 0.f;
+  if (!there) return;
+  const long orow = (static_cast<long>(at.first) + tok) * s.Hq + hq;
+  if (p.lse && half == 0) p.lse[orow] = kv_lse(m, l, some);
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = some ? o[d][i + e] * inv : 0.f;
+      kv_store4<DT>(p.out, orow * D + 32 * d + 2 * i + 4 * half, y);
+    }
+}
+
+template <int D>
+hipError_t launch_prompt(const PromptAttn& p, int dtype, hipStream_t st) {
+  const dim3 grid(p.slots * static_cast<unsigned>(p.s.H));
+  if (dtype == SPECV_F32) hipLaunchKernelGGL((k_prompt_attn<SPECV_F32, D>), grid, dim3(kPBlock), 0, st, p);
+  else hipLaunchKernelGGL((k_prompt_attn<SPECV_BF16, D>), grid, dim3(kPBlock), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace sv

@@ -1,0 +1,143 @@
+// Operand fragments of the bf16 matrix instructions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "specverify.h"
+
+namespace sv {
+
+namespace frag {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.44269504088896f;
+
+// Number of bf16 pieces of an element: 32 bits are the sum of three.
+template <int DT>
+constexpr int kPieces = DT == SPECV_F32 ? 3 : 1;
+
+// x as a sum of NP bf16 pieces.  One piece: round to nearest.  Three: the
+// leading 8 bits, the next 8 and the last 8 of the 24, an exact sum (by
+// truncation, so that the largest floats stay finite); x that is not finite
+// is its own first piece.
+template <int NP>
+__device__ inline void split(float x, __bf16* piece) {
+  if constexpr (NP == 1) {
+    piece[0] = static_cast<__bf16>(x);
+  } else {
+    auto lead = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
+    auto bits = [](float f) { return __builtin_bit_cast(__bf16, static_cast<uint16_t>(__float_as_uint(f) >> 16)); };
+    piece[0] = bits(x);
+    const float r = isfinite(x) ? x - lead(x) : 0.f;
+    piece[1] = bits(r);
+    piece[2] = bits(r - lead(r));
+  }
+}
+
+// Eight consecutive elements, as they are loaded: 16 bytes of bf16, 32 of fp32.
+template <int DT>
+struct Raw8 {
+  uint4 w[DT == SPECV_F32 ? 2 : 1];
+  __device__ void load(const void* base, long i) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + i * (DT == SPECV_F32 ? 4 : 2));
+    w[0] = p[0];
+    if constexpr (DT == SPECV_F32) w[1] = p[1];
+  }
+  __device__ void clear() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (DT == SPECV_F32) w[1] = w[0];
+  }
+  __device__ void negate(bool yes) {
+    const uint32_t signs = yes ? (DT == SPECV_F32 ? 0x80000000u : 0x80008000u) : 0u;
+    uint32_t* u = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < (DT == SPECV_F32 ? 8 : 4); ++i) u[i] ^= signs;
+  }
+  // Makes the compiler take the elements as new here, so that what is computed
+  // from them is not kept across a loop.
+  __device__ void hide() {
+    uint32_t* u = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < (DT == SPECV_F32 ? 8 : 4); ++i) asm volatile("" : "+v"(u[i]));
+  }
+  __device__ float at(int j) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (DT == SPECV_F32) return __uint_as_float(u[j]);
+    else return __uint_as_float(j % 2 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+  }
+  // Whether an element is infinite or NaN.
+  __device__ bool wild() const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < (DT == SPECV_F32 ? 8 : 4); ++i) {
+      if constexpr (DT == SPECV_F32) any |= ((u[i] & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
+      else any |= ((u[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+    }
+    return any != 0;
+  }
+  // 0 in place of what is infinite or NaN.
+  __device__ void tame() {
+    uint32_t* u = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < (DT == SPECV_F32 ? 8 : 4); ++i) {
+      if constexpr (DT == SPECV_F32) {
+        if (!isfinite(__uint_as_float(u[i]))) u[i] = 0;
+      } else {
+        if ((u[i] & 0x7f80u) == 0x7f80u) u[i] &= 0xffff0000u;
+        if ((u[i] & 0x7f800000u) == 0x7f800000u) u[i] &= 0xffffu;
+      }
+    }
+  }
+  __device__ void pieces(bf16x8* f) const {
+    if constexpr (DT == SPECV_BF16) {
+      f[0] = __builtin_bit_cast(bf16x8, w[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        __bf16 s[3];
+        split<3>(at(j), s);
+        f[0][j] = s[0];
+        f[1][j] = s[1];
+        f[2][j] = s[2];
+      }
+    }
+  }
+};
+
+// D[32][32] += A[32][16] B[16][32].  A: lane l has row l % 32 and columns 8
+// (l / 32) .. + 7; B: column l % 32 and rows 8 (l / 32) .. + 7; D: column l %
+// 32, and register i row 8 (i / 4) + 4 (l / 32) + i % 4.
+__device__ inline f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Maximum and sum over the two lanes l and l + 32.
+__device__ inline float halves_max(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ inline float halves_sum(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// A barrier that orders LDS only: __syncthreads would also wait for every
+// global load in flight, the next tile's among them.
+__device__ inline void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+}  // namespace frag
+
+}  // namespace sv
