@@ -51,7 +51,7 @@ typedef enum { SPECV_F32 = 0, SPECV_BF16 = 1 } specv_dtype_t;
 #define SPECV_E_ALIGN      -6   /* a logits pointer is not aligned to its element size, or a cache array or stride to 16 bytes */
 #define SPECV_E_HIP        -7   /* a kernel launch failed */
 #define SPECV_E_SCRATCH    -8   /* spec_verify_noalloc: the shape needs more than SPECV_NOALLOC_SCRATCH bytes */
-#define SPECV_E_OVERLAP    -9   /* spec_kv_append: out_lengths overlaps an array that the call reads */
+#define SPECV_E_OVERLAP    -9   /* an output of a cache call overlaps an array that the call reads, or another output */
 
 #define SPECV_MAX_K        32   /* one 64-lane wave runs the acceptance scan */
 #define SPECV_MAX_TREE     64   /* token-tree nodes: one per lane of a wave */
@@ -534,6 +534,93 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
 int spec_prompt_attention(const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                           const int32_t* starts, float scale, int B, int T, int heads, int Hq, int dim, void* out,
                           float* out_lse, int dtype, void* stream);
+
+/*
+ * The cache under a budget.  A cache may keep, of every sequence and head, the
+ * tokens that matter: the latest ones, and those that gathered the most
+ * attention weight.  Weights are floats [B][heads][capacity] by cached
+ * position, capacity at least max_pages * page_size: the sum, over the queries
+ * so far and over the query heads that share the cached head, of e^(s - lse),
+ * the attention's own weights.  spec_prompt_weights gives a prompt's,
+ * spec_kv_weights adds those of the nodes that a round keeps (to be called in
+ * every layer with the same path as spec_kv_append, before or after it, and
+ * with the lengths from before it), and spec_kv_evict lets go of the rest.
+ *
+ * spec_prompt_weights - the weights that the tokens of packed prompts gather
+ * from the prompts themselves: with s and lse as in spec_prompt_attention,
+ *   out_weights[b][h][j] = sum over tokens i >= j of sequence b and query heads
+ *                          of head h of e^(s_ij - lse_i),
+ * 0 behind the sequence's tokens; those at and behind `capacity` are left out.
+ * A query whose lse is -infinity weighs nothing.
+ *   lse         [T][Hq] float: out_lse of spec_prompt_attention
+ *   out_weights [B][heads][capacity] float; overlaps no input
+ *   1 <= capacity < 2^31;  (ceil(T / 128) + B) * heads < 2^24
+ * q, k, their strides, starts, scale and the other limits as for
+ * spec_prompt_attention.  Sums are in 32 bits, in an order that does not
+ * change from call to call.  Needs no workspace; nothing synchronises.
+ */
+int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* lse,
+                        const int32_t* starts, float scale, int B, int T, int heads, int Hq, int dim,
+                        float* out_weights, int64_t capacity, int dtype, void* stream);
+
+/*
+ * spec_kv_weights - add the attention weights of kept nodes.  Sequence b keeps
+ * the nodes index[b][0], index[b][1], ... as spec_kv_append takes tokens
+ * (counts of them, none from the first index outside [0, N) on), a path on
+ * which each sees those before it.  With s and lse as in spec_kv_attention,
+ *   out_weights[b][h][j] = weights[b][h][j] + sum over kept nodes i and query
+ *                          heads of head h of e^(s_ij - lse_i)
+ * at the cached positions j < lengths[b] (those without a page gather
+ * nothing), and, when k_new is given, for the m-th kept node at position
+ * lengths[b] + m the sum over itself and the kept nodes after it alone.
+ * Positions behind are left as they were.
+ *   q, k_new    as for spec_kv_attention (k_new NULL: the cached tokens only)
+ *   lse         [B][N][Hq] float: out_lse of spec_kv_attention; -infinity: a
+ *               query that weighs nothing
+ *   weights, out_weights  [B][heads][capacity] float; the same array, or
+ *               arrays that do not overlap (SPECV_E_OVERLAP)
+ *   max_pages * page_size <= capacity < 2^31;  B * heads < 2^24
+ * The other limits are those of spec_kv_attention.  Sums are in 32 bits, in
+ * an order that does not change from call to call.  Needs no workspace;
+ * nothing synchronises.
+ */
+int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const float* lse, const void* k_new,
+                    int64_t k_stride, const int32_t* lengths, const int32_t* counts, const int32_t* index,
+                    float scale, int B, int N, int Hq, const float* weights, float* out_weights, int64_t capacity,
+                    int dtype, void* stream);
+
+/*
+ * spec_kv_evict - cut sequences of more than `limit` cached tokens down to
+ * `budget`.  Of such a sequence every head keeps its last `recent` positions
+ * and, of the others, the budget - recent of largest weight (of equal weights
+ * those at the lowest positions; NaN is below every number), in their order,
+ * which become positions 0 .. budget-1.  They are moved to the pages
+ * new_pages[b], so that pages shared with other sequences stay whole; a
+ * block's new scale is the one that spec_kv_append would give its values, and
+ * codes round to nearest even in it.  Slots of the last new page behind the
+ * last token are left as they were.  Positions without a page count as zeros;
+ * a new page outside [0, num_pages) is not written.  The other sequences keep
+ * their pages, lengths and weights.
+ *   weights     [B][heads][capacity] float
+ *   new_pages   [B][ceil(budget / page_size)] int32 (device): pages that no
+ *               table row holds and no other sequence is given; read for the
+ *               sequences that are cut only
+ *   1 <= budget <= max_pages * page_size;  0 <= recent <= budget <= limit;
+ *   max_pages * page_size <= capacity < 2^31;  B <= 65535;  B * heads *
+ *   ceil(budget / page_size) < 2^22
+ *   out_table   [B][max_pages] int32: the new pages, then -1, of a sequence
+ *               that was cut; else its row of the page table
+ *   out_lengths [B] int32: budget, or the length (clamped as the cache's calls do)
+ *   out_weights [B][heads][capacity] float: the weights by new position, 0 behind
+ *   out_kept    [B][heads][budget] int32: the old positions, or -1 where the
+ *               sequence was not cut
+ * The outputs overlap neither the inputs nor each other (SPECV_E_OVERLAP).
+ * Every layer can be cut by weights of its own: tables and lengths come out
+ * alike.  Needs no workspace; nothing synchronises.
+ */
+int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* weights, int64_t capacity,
+                  const int32_t* new_pages, int budget, int recent, int limit, int B, int32_t* out_table,
+                  int32_t* out_lengths, float* out_weights, int32_t* out_kept, void* stream);
 
 /* Device-side input validation, a debugging aid.  While it is on, every
  * spec_verify* call (spec_verify, _ex, _noalloc, _ragged, _ragged_ex) first

@@ -1,5 +1,5 @@
 """Binding of the 8-bit paged cache (argument marshalling only): KVCache,
-kv_append, kv_read, kv_attention.  Checks shapes and dtypes, allocates outputs
+kv_append, kv_read, kv_attention, kv_weights, kv_evict.  Checks shapes and dtypes, allocates outputs
 and workspaces with torch and passes device pointers plus torch's current
 stream of the tensors' device."""
 from __future__ import annotations
@@ -304,3 +304,89 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
           Hq, out.data_ptr(), _ptr(lse), code, workspace.data_ptr(), have)
     results = _forward_only((out, lse) if return_lse else (out,), (q, k_new, v_new))
     return results if return_lse else results[0]
+
+
+def _check_weights(cache: KVCache, page_table, name: str, t) -> None:
+    B, width = page_table.shape
+    if t.dtype is not torch.float32 or t.dim() != 3 or t.shape[:2] != (B, cache._heads) or t.device != cache._device or \
+            not t.is_contiguous() or t.shape[2] < width * cache._page:
+        raise ValueError(f"{name} must be a contiguous float32 [{B}, {cache._heads}, capacity] tensor on the cache's "
+                         f"device, capacity at least {width * cache._page}")
+
+
+def kv_weights(cache: KVCache, page_table, q, lse, lengths, weights, k_new=None, *, counts=None, index=None,
+               scale: Optional[float] = None, out=None):
+    """Add to weights the attention weight that cached tokens gather from the
+    nodes a round keeps (spec_kv_weights).
+
+    q [B, N, Hq, dim] and k_new [B, N, heads, dim] as for kv_attention, lse [B,
+    N, Hq] as it returns it, lengths [B] the tokens cached before the round,
+    counts [B] and index [B, N] the kept nodes as for kv_append; weights [B,
+    heads, capacity] float32 by cached position, capacity at least max_pages *
+    page_size.  Kept nodes get their own weights behind the cached positions
+    when k_new is given.  Works in weights itself, or into `out` (positions
+    behind are left as they were).  Returns the tensor written, without
+    gradients."""
+    _check_table(cache, page_table)
+    B, width = page_table.shape
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, dim]")
+    _, N, Hq, dim = q.shape
+    q_row = _check_rows(cache, "q", q, B, N, Hq)
+    k_row = 0
+    if k_new is not None:
+        k_row = _check_rows(cache, "k_new", k_new, B, N, cache._heads)
+        if k_new.dtype != q.dtype:
+            raise ValueError("k_new must have q's dtype")
+    if lse.dtype is not torch.float32 or lse.shape != (B, N, Hq) or lse.device != cache._device or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 {[B, N, Hq]} tensor on the cache's device")
+    _check_ints(cache, (B,), "lengths", lengths)
+    if counts is not None:
+        _check_ints(cache, (B,), "counts", counts)
+    if index is not None:
+        _check_ints(cache, (B, N), "index", index)
+    _check_weights(cache, page_table, "weights", weights)
+    if out is None:
+        out = weights
+    else:
+        _check_weights(cache, page_table, "out", out)
+        if out.shape != weights.shape:
+            raise ValueError("out must have weights' shape")
+    if out.requires_grad:
+        raise ValueError("weights that are written must not require gradients")
+    _call(cache._device, load().spec_kv_weights, _descriptor(cache, page_table.data_ptr(), width), q.data_ptr(), q_row,
+          lse.data_ptr(), _ptr(k_new), k_row, lengths.data_ptr(), _ptr(counts), _ptr(index),
+          dim ** -0.5 if scale is None else float(scale), B, N, Hq, weights.data_ptr(), out.data_ptr(), out.shape[2],
+          _dtype_code(q.dtype))
+    return out
+
+
+def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: int, recent: int, *,
+             limit: Optional[int] = None, return_kept: bool = False):
+    """Cut sequences of more than limit (default: budget) cached tokens down
+    to budget (spec_kv_evict): every head keeps its last `recent` positions and
+    the heaviest of the others, in order, in the pages new_pages[b].
+
+    weights [B, heads, capacity] float32 by cached position; new_pages [B,
+    ceil(budget / page_size)] int32, pages that no table holds.  Returns
+    (page_table, lengths, weights) as they are after the call, in new tensors,
+    and when asked the kept positions [B, heads, budget] int32 (-1 where a
+    sequence was not cut).  The old pages of the sequences that were cut can be
+    used again once the call's work is done."""
+    _check_table(cache, page_table)
+    B, width = page_table.shape
+    limit = budget if limit is None else limit
+    if budget < 1 or budget > width * cache._page or recent < 0 or recent > budget or limit < budget:
+        raise ValueError("0 <= recent <= budget <= limit, 1 <= budget <= max_pages * page_size: got "
+                         f"{recent}, {budget}, {limit}")
+    _check_ints(cache, (B,), "lengths", lengths)
+    _check_weights(cache, page_table, "weights", weights)
+    _check_ints(cache, (B, -(-budget // cache._page)), "new_pages", new_pages)
+    out_table, out_lengths = torch.empty_like(page_table), torch.empty_like(lengths)
+    out_weights = torch.empty(weights.shape, dtype=torch.float32, device=cache._device)
+    kept = torch.empty((B, cache._heads, budget), dtype=torch.int32, device=cache._device)
+    _call(cache._device, load().spec_kv_evict, _descriptor(cache, page_table.data_ptr(), width), lengths.data_ptr(),
+          weights.data_ptr(), weights.shape[2], new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B,
+          out_table.data_ptr(), out_lengths.data_ptr(), out_weights.data_ptr(), kept.data_ptr())
+    return (out_table, out_lengths, out_weights) + ((kept,) if return_kept else ())

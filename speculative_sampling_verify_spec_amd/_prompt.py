@@ -1,4 +1,5 @@
-"""Binding of whole prompts (argument marshalling only): prompt_attention.
+"""Binding of whole prompts (argument marshalling only): prompt_attention,
+prompt_weights.
 Checks shapes and dtypes, allocates outputs with torch and passes device
 pointers plus torch's current stream of the tensors' device."""
 from __future__ import annotations
@@ -60,3 +61,28 @@ def prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, return_l
               out.data_ptr(), _ptr(lse), code)
     results = _forward_only((out, lse) if return_lse else (out,), (q, k, v), "prompt_attention")
     return results if return_lse else results[0]
+
+
+def prompt_weights(q, k, lse, starts, capacity: int, *, scale: Optional[float] = None):
+    """The attention weight that the tokens of packed prompts gather from the
+    prompts themselves (spec_prompt_weights).
+
+    q, k, starts and scale as for prompt_attention, lse [T, Hq] float32 as it
+    returns it.  Returns weights [B, heads, capacity] float32: by token of the
+    sequence, the sum of e^(score - lse) over the queries that see it and the
+    query heads of its head; 0 behind the sequence (tokens at and behind
+    capacity are left out).  Without gradients."""
+    _bind_torch()
+    B, q_row, kv_row, code = _packed(q, k, starts)
+    T, Hq, dim = q.shape
+    if lse.dtype is not _kv.torch.float32 or lse.shape != (T, Hq) or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on q's device")
+    if capacity < 1:
+        raise ValueError("capacity must be at least 1")
+    weights = _kv.torch.empty((B, k.shape[1], capacity), dtype=_kv.torch.float32, device=q.device)
+    if not T:
+        return weights.zero_()
+    _call(q.device, load().spec_prompt_weights, q.data_ptr(), q_row, k.data_ptr(), kv_row, lse.data_ptr(),
+          starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, k.shape[1], Hq, dim,
+          weights.data_ptr(), capacity, code)
+    return weights

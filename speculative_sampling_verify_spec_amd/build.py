@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = ["api.cpp", "k_sweep.hip", "k_rounds.hip", "k_verify.hip", "k_exact.hip", "k_short.hip", "k_greedy.hip", "k_stats.hip",
            "k_tree.hip", "k_ngram.hip", "k_ngram_map.hip", "k_validate.hip", "api_kv.cpp", "k_kv_cache.hip",
            "k_kv_attn_64.hip", "k_kv_attn_96.hip", "k_kv_attn_128.hip", "k_kv_attn_256.hip", "k_kv_join.hip",
-           "api_prompt.cpp", "k_prompt_64.hip", "k_prompt_96.hip", "k_prompt_128.hip", "k_prompt_256.hip"]
+           "api_prompt.cpp", "k_prompt_64.hip", "k_prompt_96.hip", "k_prompt_128.hip", "k_prompt_256.hip",
+           "api_budget.cpp", "k_kv_weights.hip", "k_kv_evict.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

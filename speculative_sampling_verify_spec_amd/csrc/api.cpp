@@ -649,7 +649,7 @@ const char* spec_verify_strerror(int code) {
     case SPECV_E_ALIGN: return "logits pointer not aligned to its element size, or a cache array, token row or stride not to 16 bytes";
     case SPECV_E_HIP: return "a HIP launch failed";
     case SPECV_E_SCRATCH: return "the shape needs more than the 32 MiB static scratch of spec_verify_noalloc";
-    case SPECV_E_OVERLAP: return "out_lengths overlaps lengths, counts, index or the page table";
+    case SPECV_E_OVERLAP: return "an output overlaps an array that the call reads, or another output";
     default: return "unknown error";
   }
 }

@@ -1,0 +1,111 @@
+// Host side of the cache under a budget: argument checks and launches of
+// spec_kv_weights and spec_kv_evict.  Nothing here allocates, synchronises or
+// keeps state.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "specverify.h"
+#include "sv_budget.h"
+#include "sv_host.h"
+
+namespace sv {
+namespace {
+
+bool apart(const void* a, long na, const void* b, long nb) {
+  return !overlap(static_cast<const int32_t*>(a), na, static_cast<const int32_t*>(b), nb);
+}
+
+// Weights cover every position that the table can hold.
+bool covers(const KvView& c, int64_t capacity) {
+  return capacity >= (static_cast<int64_t>(c.width) << c.pshift) && capacity <= INT32_MAX;
+}
+
+// Workgroups to aim at, four waves each, of 64 tokens a turn.
+constexpr long kWeightGroups = 2048;
+
+}  // namespace
+}  // namespace sv
+
+extern "C" {
+
+int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const float* lse, const void* k_new,
+                    int64_t k_stride, const int32_t* lengths, const int32_t* counts, const int32_t* index,
+                    float scale, int B, int N, int Hq, const float* weights, float* out_weights, int64_t capacity,
+                    int dtype, void* stream) {
+  using namespace sv;
+  KvWeights p{};
+  if (dtype != SPECV_F32 && dtype != SPECV_BF16) return SPECV_E_DTYPE;
+  if (const int rc = check_cache(kv, &p.c)) return rc;
+  if (!q || !lse || !lengths || !weights || !out_weights) return SPECV_E_NULL;
+  if (B < 1 || B > kMaxSeqs || N < 1 || N > SPECV_MAX_TREE || Hq < 1 || Hq > kMaxHeads || Hq % p.c.H ||
+      Hq / p.c.H > SPECV_KV_MAX_GROUP || static_cast<long>(B) * p.c.H >= (1L << 24))
+    return SPECV_E_SHAPE;
+  if (!covers(p.c, capacity) || !std::isfinite(scale * 1.5f)) return SPECV_E_SHAPE;
+  if (const int rc = check_row(&q_stride, Hq, p.c.D, dtype)) return rc;
+  if (k_new)
+    if (const int rc = check_row(&k_stride, p.c.H, p.c.D, dtype)) return rc;
+  if (!aligned16(q) || !aligned16(k_new)) return SPECV_E_ALIGN;
+  const long all = static_cast<long>(B) * p.c.H * capacity;
+  if (weights != out_weights && !apart(weights, all, out_weights, all)) return SPECV_E_OVERLAP;
+  p.q = q;
+  p.kn = k_new;
+  p.q_row = q_stride;
+  p.k_row = k_stride;
+  p.lse = lse;
+  p.lengths = lengths;
+  p.counts = counts;
+  p.index = index;
+  p.scale = scale;
+  p.B = B;
+  p.N = N;
+  p.Hq = Hq;
+  p.G = Hq / p.c.H;
+  p.w = weights;
+  p.out = out_weights;
+  p.capacity = capacity;
+  const long turns = ((static_cast<long>(p.c.width) << p.c.pshift) + 255) / 256, pairs = static_cast<long>(B) * p.c.H;
+  p.splits = static_cast<unsigned>(std::min(turns, std::max(1L, kWeightGroups / pairs)));
+  return launch_kv_weights(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
+}
+
+int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* weights, int64_t capacity,
+                  const int32_t* new_pages, int budget, int recent, int limit, int B, int32_t* out_table,
+                  int32_t* out_lengths, float* out_weights, int32_t* kept, void* stream) {
+  using namespace sv;
+  KvEvict p{};
+  if (const int rc = check_cache(kv, &p.c)) return rc;
+  if (!lengths || !weights || !new_pages || !out_table || !out_lengths || !out_weights || !kept) return SPECV_E_NULL;
+  const long most = static_cast<long>(p.c.width) << p.c.pshift;
+  if (B < 1 || B > kMaxSeqs || p.c.H > kMaxHeads || budget < 1 || budget > most || recent < 0 || recent > budget ||
+      limit < budget || !covers(p.c, capacity))
+    return SPECV_E_SHAPE;
+  const long width = (budget + p.c.P - 1) / p.c.P, table = static_cast<long>(B) * p.c.width;
+  const long pages = B * width, heads = static_cast<long>(B) * p.c.H, all = heads * capacity, keep = heads * budget;
+  if (heads * width >= (1L << 22)) return SPECV_E_SHAPE;  // a grid's threads stay below 2^32
+  // workgroups write these while others still read those
+  const struct { const void* at; long n; } in[] = {{lengths, B}, {p.c.table, table}, {new_pages, pages}, {weights, all}},
+      out[] = {{out_table, table}, {out_lengths, B}, {out_weights, all}, {kept, keep}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& x : in)
+      if (!apart(x.at, x.n, out[i].at, out[i].n)) return SPECV_E_OVERLAP;
+    for (int j = 0; j < i; ++j)
+      if (!apart(out[j].at, out[j].n, out[i].at, out[i].n)) return SPECV_E_OVERLAP;
+  }
+  p.lengths = lengths;
+  p.w = weights;
+  p.capacity = capacity;
+  p.new_pages = new_pages;
+  p.new_width = static_cast<int>(width);
+  p.budget = budget;
+  p.recent = recent;
+  p.limit = limit;
+  p.B = B;
+  p.out_table = out_table;
+  p.out_lengths = out_lengths;
+  p.out_w = out_weights;
+  p.kept = kept;
+  return launch_kv_evict(p, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
+}
+
+}  // extern "C"

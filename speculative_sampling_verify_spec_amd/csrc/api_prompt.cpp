@@ -1,5 +1,5 @@
 // Host side of whole prompts: argument checks and launches of
-// spec_prompt_attention.  Nothing here allocates, synchronises or keeps state.
+// spec_prompt_attention and spec_prompt_weights.  Nothing here allocates, synchronises or keeps state.
 #include <cmath>
 #include <cstdint>
 
@@ -62,6 +62,34 @@ int spec_prompt_attention(const void* q, int64_t q_stride, const void* k, const 
                        : dim == 96  ? launch_prompt_96(p, dtype, st)
                        : dim == 128 ? launch_prompt_128(p, dtype, st)
                                     : launch_prompt_256(p, dtype, st);
+  return e == hipSuccess ? SPECV_OK : SPECV_E_HIP;
+}
+
+int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* lse,
+                        const int32_t* starts, float scale, int B, int T, int heads, int Hq, int dim,
+                        float* out_weights, int64_t capacity, int dtype, void* stream) {
+  using namespace sv;
+  PromptWeights p{};
+  if (const int rc = check_packed(q, q_stride, k, nullptr, k_stride, starts, scale, B, T, heads, Hq, dim, dtype, &p.s))
+    return rc;
+  if (!lse || !out_weights) return SPECV_E_NULL;
+  if (capacity < 1 || capacity > INT32_MAX) return SPECV_E_SHAPE;
+  if (prompt_slots(T, 1, B, kWeightKeys) * heads >= (1L << 24)) return SPECV_E_SHAPE;
+  p.lse = lse;
+  p.w = out_weights;
+  p.capacity = static_cast<int>(capacity);
+  p.slots = static_cast<unsigned>(prompt_slots(T, 1, B, kWeightKeys));
+  // r / G for r < 2^31 is mulhi(r, m) >> (l - 1) with 2^l >= G and m = floor(2^(31 + l) / G) + 1 < 2^32:
+  // r m / 2^(31 + l) exceeds r / G by r (m G - 2^(31 + l)) / (G 2^(31 + l)) < 2^31 G / (G 2^31 2^l) <= 1 / G
+  int l = 1;
+  while ((1 << l) < p.s.G) ++l;
+  p.magic = p.s.G > 1 ? static_cast<uint32_t>((uint64_t(1) << (31 + l)) / p.s.G + 1) : 0;
+  p.shift = l - 1;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const hipError_t e = dim == 64    ? launch_prompt_weights_64(p, dtype, st)
+                       : dim == 96  ? launch_prompt_weights_96(p, dtype, st)
+                       : dim == 128 ? launch_prompt_weights_128(p, dtype, st)
+                                    : launch_prompt_weights_256(p, dtype, st);
   return e == hipSuccess ? SPECV_OK : SPECV_E_HIP;
 }
 

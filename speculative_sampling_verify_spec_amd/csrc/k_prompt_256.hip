@@ -1,8 +1,13 @@
-// Attention of whole prompts, heads of 256 channels.
+// Attention of whole prompts and the weights they give, heads of 256 channels.
 #include "prompt_attn.h"
+#include "prompt_weights.h"
 
 namespace sv {
 
 hipError_t launch_prompt_256(const PromptAttn& p, int dtype, hipStream_t s) { return launch_prompt<256>(p, dtype, s); }
+
+hipError_t launch_prompt_weights_256(const PromptWeights& p, int dtype, hipStream_t s) {
+  return launch_weights<256>(p, dtype, s);
+}
 
 }  // namespace sv

@@ -1,8 +1,13 @@
-// Attention of whole prompts, heads of 96 channels.
+// Attention of whole prompts and the weights they give, heads of 96 channels.
 #include "prompt_attn.h"
+#include "prompt_weights.h"
 
 namespace sv {
 
 hipError_t launch_prompt_96(const PromptAttn& p, int dtype, hipStream_t s) { return launch_prompt<96>(p, dtype, s); }
+
+hipError_t launch_prompt_weights_96(const PromptWeights& p, int dtype, hipStream_t s) {
+  return launch_weights<96>(p, dtype, s);
+}
 
 }  // namespace sv

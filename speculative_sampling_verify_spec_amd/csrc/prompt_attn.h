@@ -48,23 +48,6 @@ template <int DT, int D> struct PromptShape {
   static constexpr int waves = DT == SPECV_F32 || D == 256 ? 1 : 2;
 };
 
-// Where the 16-byte piece c of a tile's row t stands in the row, for both
-// reads: eight rows' same piece (K), and four rows' same pair of pieces (V),
-// fall into different banks.
-template <int D>
-__device__ inline int swizzle(int t, int c) {
-  if constexpr (D == 96) return c ^ ((t >> 2) & 3);
-  else if constexpr (D == 64) return c ^ (2 * ((t >> 1) & 3));
-  else return c ^ (2 * (t & 7));
-}
-
-// 16 bytes a lane from memory straight to LDS: the wave's 1024 bytes from `to` on.
-__device__ inline void load_lds(const void* from, const void* to) {
-  typedef __attribute__((address_space(3))) const void* lds_ptr;
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)to)));
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
-}
-
 template <int DT, int D>
 __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt_attn(PromptAttn p) {
   using Shape = PromptShape<DT, D>;
@@ -188,15 +171,9 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
     }
     if (odd) wild = 1;
   };
-  auto landed = [] {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-
   if (tid == 0) wild = 0;
   request(0, 0);
-  if constexpr (DT == SPECV_BF16) landed();
+  if constexpr (DT == SPECV_BF16) landed_barrier();
 
   for (int tile = 0; tile < ntile; ++tile) {
     const int buf = Shape::buffers == 2 ? tile & 1 : 0;
@@ -333,7 +310,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
         }
       }
     }
-    landed();
+    landed_barrier();
   }
 
   l = halves_sum(l);

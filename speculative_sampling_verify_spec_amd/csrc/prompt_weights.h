@@ -1,0 +1,203 @@
+// The attention weight that a prompt's tokens gather from the prompt itself
+// (the kernel template; k_prompt_<dim>.hip instantiate it):
+//   w[j] = sum over the queries i >= j, and the query heads that share a key
+//          head, of e^(scale q_i . k_j - lse_i).
+//
+// A workgroup takes 128 tokens of one sequence and key head as keys, a wave 32
+// of them, whose fragments stay in registers, and goes through the rows (query
+// head r % G of token r / G) from its first key's token on:
+//   S = Q K^T         A = 32 rows x 16 channels,  B = 16 channels x 32 keys
+// A lane then has one key, so that the sum over rows stays in its registers and
+// no atomics join anything.  The rows pass through LDS, 64 at a time and for
+// all waves, from memory without registers between.
+//
+// Bound by the exponentials: a score costs one quarter-rate instruction and two
+// of full rate, 24 cycles of a SIMD for 64, against 16 of its products.
+#pragma once
+
+#include "sv_device.h"
+#include "sv_mfma.h"
+#include "sv_prompt.h"
+
+namespace sv {
+
+namespace {
+
+using namespace frag;
+
+constexpr int kWBlock = 256;
+
+// Rows of a tile and waves a SIMD.
+template <int DT, int D> struct WeightShape {
+  static constexpr int tile = DT == SPECV_F32 || D == 256 ? 32 : 64;
+  static constexpr int buffers = DT == SPECV_F32 ? 1 : 2;
+  static constexpr int waves = DT == SPECV_F32 ? (D == 256 ? 1 : 2) : D == 256 ? 2 : 3;
+};
+
+template <int DT, int D>
+__global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt_weights(PromptWeights p) {
+  using Shape = WeightShape<DT, D>;
+  constexpr int NP = kPieces<DT>, NF = D / 16, BM = Shape::tile, NB = BM / 32, NC = D / 8;
+  constexpr int kPlane = BM * D, kAll = BM * NC, kLoads = (kAll + kWBlock - 1) / kWBlock;
+  static_assert(DT == SPECV_F32 || kAll % kWBlock == 0, "whole loads");
+  static_assert(kWeightKeys == 32 * (kWBlock / kWave), "32 keys a wave");
+  const Packed& s = p.s;
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(s.H));
+  const unsigned place = blockIdx.x / static_cast<unsigned>(s.H);
+  const PromptBlock at = prompt_block<kWBlock>(s, place, 1, kWeightKeys);
+  const int tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int col = lane % 32, half = lane / 32;
+  if (at.block < 0) {
+    // sequences without tokens: a wave clears one at a time
+    const unsigned free = p.slots - at.used;
+    for (long b = (place - at.used) * (kWBlock / kWave) + w; b < s.B; b += static_cast<long>(free) * (kWBlock / kWave)) {
+      int first, last;
+      prompt_range(s, static_cast<int>(b), first, last);
+      if (first < last) continue;
+      for (int j = lane; j < p.capacity; j += kWave) p.w[(b * s.H + h) * p.capacity + j] = 0.f;
+    }
+    return;
+  }
+  const int len = at.last - at.first, rows = len * s.G;
+  // the first keys, which all rows see, first
+  const int nblock = (len + kWeightKeys - 1) / kWeightKeys, block = nblock - 1 - at.block;
+  const int key0 = block * kWeightKeys, wkey = key0 + 32 * w, key = wkey + col;
+  float* const wrow = p.w + (static_cast<long>(at.seq) * s.H + h) * p.capacity;
+  if (block == nblock - 1)  // behind the prompt
+    for (int j = len + tid; j < p.capacity; j += kWBlock) wrow[j] = 0.f;
+
+  __shared__ __align__(16) __bf16 lq[Shape::buffers][NP * kPlane];
+  __shared__ __align__(16) float ll[Shape::buffers][BM];  // lse in log2; +infinity where a row weighs nothing
+
+  const float kscale = s.scale * kLog2e;
+  bf16x8 k[NF][NP];
+  {
+    const long base = (static_cast<long>(at.first) + min(key, len - 1)) * s.kv_row + static_cast<long>(h) * D + 8 * half;
+    Raw8<DT> x[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) x[f].load(s.k, base + 16 * f);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) x[f].pieces(k[f]);
+  }
+
+  auto token_of = [&](int r) {
+    return s.G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.magic) >> p.shift);
+  };
+  const int row_first = key0 * s.G, ntile = (rows - row_first + BM - 1) / BM;
+  const long qbase = static_cast<long>(at.first) * s.q_row + static_cast<long>(h) * s.G * D;
+  auto offset = [&](int tile, int e) {
+    const int t = e / NC, r = min(row_first + tile * BM + t, rows - 1), tok = token_of(r);
+    return qbase + static_cast<long>(tok) * s.q_row + static_cast<long>(r - tok * s.G) * D + 8 * swizzle<D>(t, e % NC);
+  };
+  auto request = [&](int tile, int buf) {
+    if constexpr (DT == SPECV_BF16) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        load_lds(static_cast<const uint16_t*>(s.q) + offset(tile, tid + i * kWBlock), &lq[buf][8 * (i * kWBlock + w * kWave)]);
+    }
+  };
+  auto fill = [&](int tile) {
+    if constexpr (DT == SPECV_F32) {
+#pragma unroll D == 256 ? 1 : kLoads
+      for (int i = 0; i < kLoads; ++i) {
+        const int e = tid + i * kWBlock;
+        if (kAll % kWBlock && e >= kAll) break;
+        Raw8<DT> x;
+        x.load(s.q, offset(tile, e));
+        bf16x8 f[NP];
+        x.pieces(f);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&lq[0][j * kPlane + 8 * e]) = f[j];
+      }
+    }
+  };
+  // the statistics of a tile's rows, by its first threads
+  auto stat = [&](int tile) {
+    float x = INFINITY;
+    const int r = row_first + tile * BM + tid;
+    if (tid < BM && r < rows) {
+      const int tok = token_of(r);
+      x = p.lse[(static_cast<long>(at.first) + tok) * s.Hq + h * s.G + (r - tok * s.G)];
+      x = x == -INFINITY ? INFINITY : x * kLog2e;
+    }
+    return x;
+  };
+
+  request(0, 0);
+  float next = stat(0);
+  float sum = 0.f, lost = 0.f;  // the tiles' sums are added with what each addition rounds away
+  if constexpr (DT == SPECV_BF16) {
+    if (tid < BM) ll[0][tid] = next;
+    landed_barrier();
+  }
+  for (int tile = 0; tile < ntile; ++tile) {
+    const int buf = Shape::buffers == 2 ? tile & 1 : 0;
+    const bool more = tile + 1 < ntile;
+    if constexpr (DT == SPECV_F32) {
+      fill(tile);
+      if (tid < BM) ll[0][tid] = next;
+      if (more) next = stat(tile + 1);
+      __syncthreads();
+    } else if (more) {
+      request(tile + 1, buf ^ 1);
+      next = stat(tile + 1);
+    }
+    const int r0 = row_first + tile * BM;
+    if (wkey < len && r0 + BM > wkey * s.G) {  // a row sees a key of the wave
+      f32x16 sc[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[n][i] = 0.f;
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          bf16x8 a[NP];
+          const int t = 32 * n + col;
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
+#pragma unroll
+          for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i <= z; ++i) sc[n] = mfma32(a[z - i], k[f][i], sc[n]);
+        }
+      float part = 0.f;
+      const bool all = r0 >= (wkey + 31) * s.G;  // every row sees every key of the wave
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float e = ex2(fmaf(sc[n][4 * j + i], kscale, -l4[i]));
+            if (!all && r0 + 32 * n + 8 * j + 4 * half + i < key * s.G) e = 0.f;
+            part += e;
+          }
+        }
+      const float y = part - lost, z = sum + y;
+      lost = (z - sum) - y;
+      sum = z;
+    }
+    if constexpr (DT == SPECV_BF16) {
+      if (more && tid < BM) ll[buf ^ 1][tid] = next;
+    }
+    landed_barrier();
+  }
+  sum = halves_sum(sum);
+  if (half == 0 && key < len && key < p.capacity) wrow[key] = sum;
+}
+
+template <int D>
+hipError_t launch_weights(const PromptWeights& p, int dtype, hipStream_t st) {
+  const dim3 grid(p.slots * static_cast<unsigned>(p.s.H));
+  if (dtype == SPECV_F32) hipLaunchKernelGGL((k_prompt_weights<SPECV_F32, D>), grid, dim3(kWBlock), 0, st, p);
+  else hipLaunchKernelGGL((k_prompt_weights<SPECV_BF16, D>), grid, dim3(kWBlock), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace sv

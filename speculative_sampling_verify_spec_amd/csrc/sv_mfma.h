@@ -130,10 +130,34 @@ __device__ inline float halves_sum(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// Where the 16-byte piece c of row t stands in a row of D elements in LDS, so
+// that eight rows' same piece, and four rows' same pair of pieces (a transposing
+// read), fall into different banks.
+template <int D>
+__device__ inline int swizzle(int t, int c) {
+  if constexpr (D == 96) return c ^ ((t >> 2) & 3);
+  else if constexpr (D == 64) return c ^ (2 * ((t >> 1) & 3));
+  else return c ^ (2 * (t & 7));
+}
+
+// 16 bytes a lane from memory straight to LDS: the wave's 1024 bytes from `to` on.
+__device__ inline void load_lds(const void* from, const void* to) {
+  typedef __attribute__((address_space(3))) const void* lds_ptr;
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)to)));
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+}
+
 // A barrier that orders LDS only: __syncthreads would also wait for every
 // global load in flight, the next tile's among them.
 __device__ inline void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A barrier after which what load_lds requested before it is in LDS.
+__device__ inline void landed_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }

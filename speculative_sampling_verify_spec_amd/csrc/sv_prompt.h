@@ -27,6 +27,17 @@ struct PromptAttn {
   unsigned slots;         // places for blocks of kPromptRows rows of a head (prompt_slots)
 };
 
+struct PromptWeights {
+  Packed s;               // no v
+  const float* lse;       // [T][Hq]
+  float* w;               // [B][H][capacity]
+  int capacity;
+  unsigned slots;         // places for blocks of kWeightKeys tokens of a head
+  uint32_t magic;         // r / G is mulhi(r, magic) >> shift for r < 2^31 (G > 1)
+  int shift;
+};
+
+constexpr int kWeightKeys = 128;  // tokens of one workgroup, as keys
 constexpr int kPromptRows = 128;  // rows (a token's query head each) of one workgroup
 
 // Places for the blocks of all sequences of one head, whatever their lengths:
@@ -38,12 +49,17 @@ hipError_t launch_prompt_64(const PromptAttn& p, int dtype, hipStream_t s);
 hipError_t launch_prompt_96(const PromptAttn& p, int dtype, hipStream_t s);
 hipError_t launch_prompt_128(const PromptAttn& p, int dtype, hipStream_t s);
 hipError_t launch_prompt_256(const PromptAttn& p, int dtype, hipStream_t s);
+hipError_t launch_prompt_weights_64(const PromptWeights& p, int dtype, hipStream_t s);
+hipError_t launch_prompt_weights_96(const PromptWeights& p, int dtype, hipStream_t s);
+hipError_t launch_prompt_weights_128(const PromptWeights& p, int dtype, hipStream_t s);
+hipError_t launch_prompt_weights_256(const PromptWeights& p, int dtype, hipStream_t s);
 
 #ifdef __HIPCC__
 
 // A block of a sequence's rows: the sequence's token range and the block's number.
 struct PromptBlock {
   int first, last;  // the sequence's tokens first .. last-1
+  int seq;          // the sequence
   int block;        // -1: none
   int used;         // blocks of all sequences (valid when block < 0)
 };
@@ -60,7 +76,7 @@ __device__ inline void prompt_range(const Packed& s, int b, int& first, int& las
 template <int THREADS>
 __device__ inline PromptBlock prompt_block(const Packed& s, unsigned place, int per_token, int size) {
   __shared__ long wave_sum[THREADS / 64 + 1];
-  __shared__ int found[3];
+  __shared__ int found[4];
   PromptBlock r;
   r.block = -1;
   r.used = 0;
@@ -86,6 +102,7 @@ __device__ inline PromptBlock prompt_block(const Packed& s, unsigned place, int 
       found[0] = first;
       found[1] = last;
       found[2] = static_cast<int>(sum - 1 - place);
+      found[3] = b;
     }
     long total = 0;
     for (int i = 0; i < THREADS / 64; ++i) total += wave_sum[i];
@@ -95,6 +112,7 @@ __device__ inline PromptBlock prompt_block(const Packed& s, unsigned place, int 
       r.first = found[0];
       r.last = found[1];
       r.block = found[2];
+      r.seq = found[3];
       return r;
     }
     __syncthreads();

@@ -43,3 +43,23 @@ def test_binding_refusals():
     x = torch.zeros(5, 4, 64)
     with pytest.raises(ValueError, match="GPU"):
         sv.prompt_attention(x, x, x, torch.zeros(2, dtype=torch.int32))
+
+
+def weigh(lib, **kw):
+    a = dict(q=BASE, qs=0, k=2 * BASE, ks=0, lse=3 * BASE, starts=4 * BASE, scale=0.1, B=4, T=100, H=8, Hq=32, D=128,
+             out=5 * BASE, C=100, dtype=BF16)
+    a.update(kw)
+    return lib.spec_prompt_weights(a["q"], a["qs"], a["k"], a["ks"], a["lse"], a["starts"], a["scale"], a["B"], a["T"],
+                                   a["H"], a["Hq"], a["D"], a["out"], a["C"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,code", PACKED + [(dict(lse=None), -1), (dict(out=None), -1), (dict(C=0), -2),
+                                              (dict(C=1 << 31), -2)])
+def test_weights_refusals(lib, kw, code):
+    assert weigh(lib, **kw) == code
+
+
+def test_weights_binding_refuses_host_tensors():
+    x = torch.zeros(5, 4, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        sv.prompt_weights(x, x, torch.zeros(5, 4), torch.zeros(2, dtype=torch.int32), 5)
