@@ -39,78 +39,26 @@
 
 #include "sv_device.h"
 #include "sv_kv.h"
+#include "sv_mfma.h"
 #include "sv_tree.h"
 
 namespace sv {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+using namespace frag;
 
-constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLazyMax = 8.f;  // log2: how far a score may exceed the held maximum
 
 // V scales below this count as 0 with bf16 weights: the values are below
 // 2^-77, and weights down to 2^-40 stay in the sums beside scales above it.
 constexpr float kFlatScale = 0x1p-86f;
 
-// Eight codes to bf16, exact.
-template <int FMT>
-__device__ inline bf16x8 codes8(uint32_t a, uint32_t b) {
-  union { uint32_t w[4]; bf16x2 h[4]; bf16x8 v; } u;
-  if constexpr (FMT == SPECV_E4M3) {
-    u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
-    u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
-    u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
-    u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
-  } else {
-    // integers up to 127 have at most 7 significant bits: their floats' upper halves are their bf16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? a : b;
-      const int s = 16 * (i & 1);
-      const uint32_t lo = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> s)));
-      const uint32_t hi = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> (s + 8))));
-      u.w[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-    }
-  }
-  return u.v;
-}
-
 // The bytes of a word of codes that are NaN.
 template <int FMT>
 __device__ inline uint32_t nan_bytes(uint32_t w) {
   if constexpr (FMT == SPECV_E4M3) return ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu;
   else return 0;
-}
-
-__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// Number of bf16 pieces of an element.
-template <int DT>
-constexpr int kPieces = DT == SPECV_F32 ? 3 : 1;
-
-// x as a sum of NP bf16 pieces.  One piece: round to nearest.  Three: the
-// leading 8 bits, the next 8 and the last 8 of the 24, an exact sum (by
-// truncation, so that the largest floats stay finite); x that is not finite
-// is its own first piece.
-template <int NP>
-__device__ inline void split(float x, __bf16* piece) {
-  if constexpr (NP == 1) {
-    piece[0] = static_cast<__bf16>(x);
-  } else {
-    auto lead = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
-    auto bits = [](float f) { return __builtin_bit_cast(__bf16, static_cast<uint16_t>(__float_as_uint(f) >> 16)); };
-    piece[0] = bits(x);
-    const float r = isfinite(x) ? x - lead(x) : 0.f;
-    piece[1] = bits(r);
-    piece[2] = bits(r - lead(r));
-  }
 }
 
 // Eight consecutive elements as NP operand fragments.
@@ -137,40 +85,6 @@ template <int DT>
 __device__ inline float load1(const void* base, long i) {
   if constexpr (DT == SPECV_F32) return static_cast<const float*>(base)[i];
   else return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << 16);
-}
-
-// A barrier that orders LDS only: __syncthreads would also wait for every
-// global load and store in flight, the next tile's among them.
-__device__ inline void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// First channel of the 8 that lane group g holds of fragment f: fragments 2c
-// and 2c + 1 are the halves of the 16 bytes a lane loads of 64 channels; a
-// last odd fragment is an 8-byte load of 32.
-template <int D>
-__device__ inline int chan(int f, int g) {
-  return f < D / 64 * 2 ? f / 2 * 64 + 16 * g + f % 2 * 8 : D / 64 * 64 + 8 * g;
-}
-
-// Maximum and sum over the four lanes that hold the same query (lane % 16).
-__device__ inline float groups_max(float v) {
-  const unsigned u = __float_as_uint(v);
-  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const unsigned w = __float_as_uint(v);
-  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ inline float groups_sum(float v) {
-  const unsigned u = __float_as_uint(v);
-  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const unsigned w = __float_as_uint(v);
-  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 constexpr int kAWaves = 4, kABlock = kAWaves * kWave;  // waves and threads per workgroup

@@ -8,12 +8,14 @@
 // head r % G of token r / G) from its first key's token on:
 //   S = Q K^T         A = 32 rows x 16 channels,  B = 16 channels x 32 keys
 // A lane then has one key, so that the sum over rows stays in its registers and
-// no atomics join anything.  The rows pass through LDS, 64 at a time and for
+// no atomics join anything.  The rows pass through LDS, 128 at a time and for
 // all waves, from memory without registers between.
 //
 // Bound by the exponentials: a score costs one quarter-rate instruction and two
 // of full rate, 24 cycles of a SIMD for 64, against 16 of its products.
 #pragma once
+
+#include <type_traits>
 
 #include "sv_device.h"
 #include "sv_mfma.h"
@@ -29,9 +31,9 @@ constexpr int kWBlock = 256;
 
 // Rows of a tile and waves a SIMD.
 template <int DT, int D> struct WeightShape {
-  static constexpr int tile = DT == SPECV_F32 || D == 256 ? 32 : 64;
+  static constexpr int tile = DT == SPECV_F32 ? 32 : D == 256 ? 64 : 128;
   static constexpr int buffers = DT == SPECV_F32 ? 1 : 2;
-  static constexpr int waves = DT == SPECV_F32 ? (D == 256 ? 1 : 2) : D == 256 ? 2 : 3;
+  static constexpr int waves = DT == SPECV_F32 && D == 256 ? 1 : 2;
 };
 
 template <int DT, int D>
@@ -144,39 +146,40 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
     }
     const int r0 = row_first + tile * BM;
     if (wkey < len && r0 + BM > wkey * s.G) {  // a row sees a key of the wave
-      f32x16 sc[NB];
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sc[n][i] = 0.f;
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
+      float part = 0.f;
+      // mixed: some rows do not see some of the wave's keys
+      auto blocks = [&](auto mixed) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          bf16x8 a[NP];
-          const int t = 32 * n + col;
+          f32x16 sc;
 #pragma unroll
-          for (int j = 0; j < NP; ++j)
-            a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
+          for (int i = 0; i < 16; ++i) sc[i] = 0.f;
 #pragma unroll
-          for (int z = NP - 1; z >= 0; --z)
+          for (int f = 0; f < NF; ++f) {
+            bf16x8 a[NP];
+            const int t = 32 * n + col;
 #pragma unroll
-            for (int i = 0; i <= z; ++i) sc[n] = mfma32(a[z - i], k[f][i], sc[n]);
-        }
-      float part = 0.f;
-      const bool all = r0 >= (wkey + 31) * s.G;  // every row sees every key of the wave
+            for (int j = 0; j < NP; ++j)
+              a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+            for (int z = NP - 1; z >= 0; --z)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
+              for (int i = 0; i <= z; ++i) sc = mfma32(a[z - i], k[f][i], sc);
+          }
+          const int first = key * s.G - (r0 + 32 * n + 4 * half);  // rows from here on see the lane's key
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float e = ex2(fmaf(sc[n][4 * j + i], kscale, -l4[i]));
-            if (!all && r0 + 32 * n + 8 * j + 4 * half + i < key * s.G) e = 0.f;
-            part += e;
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e = ex2(fmaf(sc[4 * j + i], kscale, -l4[i]));
+              part += decltype(mixed)::value && 8 * j + i < first ? 0.f : e;  // whatever an unseen score is
+            }
           }
         }
+      };
+      if (r0 >= (wkey + 31) * s.G) blocks(std::false_type{});
+      else blocks(std::true_type{});
       const float y = part - lost, z = sum + y;
       lost = (z - sum) - y;
       sum = z;

@@ -111,11 +111,67 @@ struct Raw8 {
   }
 };
 
+// Eight codes to bf16, exact.
+template <int FMT>
+__device__ inline bf16x8 codes8(uint32_t a, uint32_t b) {
+  union { uint32_t w[4]; bf16x2 h[4]; bf16x8 v; } u;
+  if constexpr (FMT == SPECV_E4M3) {
+    u.h[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
+    u.h[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
+    u.h[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
+    u.h[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
+  } else {
+    // integers up to 127 have at most 7 significant bits: their floats' upper halves are their bf16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? a : b;
+      const int s = 16 * (i & 1);
+      const uint32_t lo = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> s)));
+      const uint32_t hi = __float_as_uint(static_cast<float>(static_cast<int8_t>(w >> (s + 8))));
+      u.w[i] = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+    }
+  }
+  return u.v;
+}
+
+// D[16][16] += A[16][32] B[32][16].  A: lane l has row l % 16 and columns 8
+// (l / 16) .. + 7; B: column l % 16 and rows 8 (l / 16) .. + 7; D: column l %
+// 16, and register i row 4 (l / 16) + i.
+__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 // D[32][32] += A[32][16] B[16][32].  A: lane l has row l % 32 and columns 8
 // (l / 32) .. + 7; B: column l % 32 and rows 8 (l / 32) .. + 7; D: column l %
 // 32, and register i row 8 (i / 4) + 4 (l / 32) + i % 4.
 __device__ inline f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// First channel of the 8 that lane group g holds of fragment f: fragments 2c
+// and 2c + 1 are the halves of the 16 bytes a lane loads of 64 channels; a
+// last odd fragment is an 8-byte load of 32.
+template <int D>
+__device__ inline int chan(int f, int g) {
+  return f < D / 64 * 2 ? f / 2 * 64 + 16 * g + f % 2 * 8 : D / 64 * 64 + 8 * g;
+}
+
+// Maximum and sum over the four lanes that hold the same query (lane % 16).
+__device__ inline float groups_max(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const unsigned w = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float groups_sum(float v) {
+  const unsigned u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const unsigned w = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Maximum and sum over the two lanes l and l + 32.
