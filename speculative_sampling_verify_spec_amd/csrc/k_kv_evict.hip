@@ -2,10 +2,13 @@
 // stays, and moving it to new pages.
 #include "sv_budget.h"
 #include "sv_device.h"
+#include "sv_mfma.h"
 
 namespace sv {
 
 namespace {
+
+using frag::lds_barrier;
 
 constexpr int kSBlock = 1024, kSWaves = kSBlock / kWave;
 constexpr int kBins = 2048;
@@ -232,14 +235,6 @@ __device__ inline float largest16(const uint4& v) {
   return fmaxf(fmaxf(largest4<FMT>(v.x), largest4<FMT>(v.y)), fmaxf(largest4<FMT>(v.z), largest4<FMT>(v.w)));
 }
 
-__device__ inline float block_max(float x, float* at) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) x = fmaxf(x, __shfl_xor(x, d, kWave));
-  if (threadIdx.x % kWave == 0) at[threadIdx.x / kWave] = x;
-  __syncthreads();
-  return fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]));
-}
-
 // What a token's codes are multiplied by; finite, so that a code of 0 stays 0.
 __device__ inline float code_ratio(float from, float to) { return fminf(from / to, 0x1.fffffep127f); }
 
@@ -247,9 +242,11 @@ __device__ inline float code_ratio(float from, float to) { return fminf(from / t
 // them, so that 64 channels' same token falls into 64 different banks.
 __host__ __device__ inline int v_row(int P) { return P + 4; }
 
-// One workgroup per sequence, head, new page and K or V: gathers the tokens
-// that stay, finds the block's new scale (as an append of them would) and
-// writes their codes in its units.
+// One workgroup per sequence, head and new page: gathers the tokens that stay,
+// finds the blocks' new scales (as an append of them would) and writes their
+// codes in their units.  A workgroup's time is that of the loads that wait for
+// each other, so there are three: the kept positions, their pages, and then
+// codes and scales together.
 //
 // K rows are copied 16 bytes a thread and stay in its registers between the
 // two.  V pages have a channel's tokens side by side: a lane takes a channel
@@ -259,72 +256,41 @@ __host__ __device__ inline int v_row(int P) { return P + 4; }
 template <int FMT, int kMost>  // kMost: pieces of 16 K codes of a block that a thread has at most
 __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
   const KvView& c = p.c;
-  const int col = blockIdx.x % static_cast<unsigned>(p.new_width), is_v = blockIdx.x / static_cast<unsigned>(p.new_width);
-  const int h = blockIdx.y, tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int col = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid % kWave;
+  const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const long b = blockIdx.z;
-  if (kv_len(c, p.lengths, b) <= p.limit) return;
-  const int to = p.new_pages[b * p.new_width + col];
-  if (to < 0 || to >= c.pages) return;
   const int D = c.D, P = c.P, n = min(p.budget - col * P, P);
-  __shared__ size_t block_at[128];  // start of a token's block in the pages
-  __shared__ int slot[128];         // its place there, -1: no page
-  __shared__ __align__(16) float unit[128];  // its scale
-  __shared__ float waves[kMWaves];
+  const int32_t* const kept = p.kept + (b * c.H + h) * static_cast<long>(p.budget) + col * P;
+  // a thread per token, and the tokens of a wave's share of V one a lane
+  const int per = (n + kMWaves - 1) / kMWaves, t0 = min(w * per, n), own = min(per, n - t0);
+  const int to = p.new_pages[b * p.new_width + col], first = kept[0];
+  const int at_k = tid < n ? kept[tid] : -1, at_v = lane < own ? kept[t0 + lane] : -1;
+  if (first < 0 || to < 0 || to >= c.pages) return;  // not cut, or no page to move to
+  const int page_k = at_k < 0 ? -1 : kv_page(c, b, at_k >> c.pshift), page_v = at_v < 0 ? -1 : kv_page(c, b, at_v >> c.pshift);
+  __shared__ size_t row_at[128];    // start of a token's row of K codes, ~0: no page
+  __shared__ __align__(16) float unit_k[128], unit_v[128];  // the scales
+  __shared__ float waves[2][kMWaves];
   extern __shared__ __align__(16) uint8_t codes[];  // V: [D][v_row(P)]
   const size_t bytes = static_cast<size_t>(P) * D, dst = (static_cast<size_t>(to) * c.H + h) * bytes;
-  if (tid < P) {
-    int page = -1, at = 0;
-    if (tid < n) {
-      at = p.kept[(b * c.H + h) * static_cast<long>(p.budget) + col * P + tid];
-      page = at < 0 ? -1 : kv_page(c, b, at >> c.pshift);
-    }
-    const size_t blk = static_cast<size_t>(max(page, 0)) * c.H + h;
-    block_at[tid] = blk * bytes;
-    slot[tid] = page < 0 ? -1 : at & (P - 1);
-    unit[tid] = page < 0 ? 0.f : (is_v ? c.vs : c.ks)[blk];
+  const size_t blk_k = static_cast<size_t>(max(page_k, 0)) * c.H + h;
+  if (tid < P) row_at[tid] = page_k < 0 ? ~size_t(0) : blk_k * bytes + static_cast<size_t>(at_k & (P - 1)) * D;
+  const float ks = tid < P && page_k >= 0 ? c.ks[blk_k] : 0.f, vs = tid < P && page_k >= 0 ? c.vs[blk_k] : 0.f;
+  lds_barrier();
+  // ---- K: into registers ----
+  const int pieces = D / 16, all = n * pieces;
+  const unsigned inv = 65536u / pieces + 1;  // e / pieces is e * inv >> 16 for e < 2048
+  uint4 x[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int e = tid + i * kMBlock, t = static_cast<int>(e * inv >> 16);
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (e < all && row_at[t] != ~size_t(0)) x[i] = *reinterpret_cast<const uint4*>(c.kp + row_at[t] + 16 * (e - t * pieces));
   }
-  __syncthreads();
-  float top = 0.f;
-  if (!is_v) {
-    const int per = D / 16, all = n * per;
-    const unsigned inv = 65536u / per + 1;  // e / per is e * inv >> 16 for e < 2048
-    uint4 x[kMost];
-    float u[kMost];
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int e = tid + i * kMBlock, t = static_cast<int>(e * inv >> 16), d = e - t * per;
-      x[i] = make_uint4(0, 0, 0, 0);
-      u[i] = 0.f;
-      if (e < all && slot[t] >= 0) {
-        x[i] = *reinterpret_cast<const uint4*>(c.kp + block_at[t] + static_cast<size_t>(slot[t]) * D + 16 * d);
-        u[i] = unit[t];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kMost; ++i)
-      if (i * kMBlock < all) top = fmaxf(top, largest16<FMT>(x[i]) * u[i]);
-    top = block_max(top, waves);
-    const float s = kv_scale<FMT>(fminf(top, 0x1.fffffep127f));
-    if (tid == 0) c.ks[static_cast<size_t>(to) * c.H + h] = s;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int e = tid + i * kMBlock;
-      if (e < all) {
-        const float r = code_ratio(u[i], s);
-        *reinterpret_cast<uint4*>(c.kp + dst + 16 * static_cast<size_t>(e)) =
-            make_uint4(kv_rescale4<FMT>(x[i].x, r), kv_rescale4<FMT>(x[i].y, r), kv_rescale4<FMT>(x[i].z, r),
-                       kv_rescale4<FMT>(x[i].w, r));
-      }
-    }
-    return;
-  }
-  // ---- V ----
+  // ---- V: into LDS; the wave's tokens in runs that lie in the same 16 tokens
+  // of a page, four of which are loaded before the first is needed ----
   const int row = v_row(P);
-  // a wave's share of the tokens, one a lane; in it, runs that lie in the same
-  // 16 tokens of a page, four of which are loaded before the first is needed
-  const int per = (n + kMWaves - 1) / kMWaves, t0 = min(w * per, n), own = min(per, n - t0);
-  const int mine = lane < own ? slot[t0 + lane] : -1;
-  const uint64_t mine_at = lane < own ? block_at[t0 + lane] + (mine < 0 ? 0 : mine & ~15) : 0;
+  const int mine = page_v < 0 ? -1 : at_v & (P - 1);
+  const uint64_t mine_at = mine < 0 ? 0 : (static_cast<size_t>(page_v) * c.H + h) * bytes + (mine & ~15);
   const uint32_t at_lo = static_cast<uint32_t>(mine_at), at_hi = static_cast<uint32_t>(mine_at >> 32);
   const int prev = __shfl_up(mine, 1, kWave);
   const uint32_t prev_lo = __shfl_up(at_lo, 1, kWave), prev_hi = __shfl_up(at_hi, 1, kWave);
@@ -349,9 +315,9 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
         for (int i = 0; i < 2; ++i)
           if (half + i < run) {
             const int d = min((half + i) * kWave + lane, D - 1);
-            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(c.vp + from + static_cast<size_t>(d) * P);
-            lo[k][i] = x.x;
-            hi[k][i] = x.y;
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(c.vp + from + static_cast<size_t>(d) * P);
+            lo[k][i] = y.x;
+            hi[k][i] = y.y;
           }
       }
       rest = left;
@@ -367,8 +333,8 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
           for (int i = 0; i < 2; ++i)
             if (half + i < run) {
               const int d = (half + i) * kWave + lane;
-              const uint64_t x = at & 8 ? hi[k][i] : lo[k][i];
-              if (d < D) codes[d * row + t0 + t] = static_cast<uint8_t>(x >> (8 * (at & 7)));
+              const uint64_t y = at & 8 ? hi[k][i] : lo[k][i];
+              if (d < D) codes[d * row + t0 + t] = static_cast<uint8_t>(y >> (8 * (at & 7)));
             }
         }
       }
@@ -376,7 +342,19 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
 #pragma unroll
     for (int k = 0; k < kRuns; ++k) left &= left - 1;
   }
+  if (tid < P) {
+    unit_k[tid] = ks;
+    unit_v[tid] = vs;
+  }
   __syncthreads();
+  // ---- the new scales ----
+  float top_k = 0.f, top_v = 0.f, u[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int e = tid + i * kMBlock;
+    u[i] = e < all ? unit_k[e * inv >> 16] : 0.f;
+    top_k = fmaxf(top_k, largest16<FMT>(x[i]) * u[i]);
+  }
   // words of four codes; of a row's, the last ones may be behind the last token
   const int wshift = c.pshift - 2, words = 1 << wshift;
   for (int e = tid; e < D << wshift; e += kMBlock) {
@@ -384,36 +362,61 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
     if (t >= n) continue;
     float f[4];
     kv_decode4<FMT>(*reinterpret_cast<const uint32_t*>(&codes[d * row + t]), f);
-    const float4 u = *reinterpret_cast<const float4*>(&unit[t]);  // 0 behind the last token
-    top = fmaxf(fmaxf(top, fmaxf(fabsf(f[0]) * u.x, fabsf(f[1]) * u.y)), fmaxf(fabsf(f[2]) * u.z, fabsf(f[3]) * u.w));
+    const float4 y = *reinterpret_cast<const float4*>(&unit_v[t]);  // 0 behind the last token
+    top_v = fmaxf(fmaxf(top_v, fmaxf(fabsf(f[0]) * y.x, fabsf(f[1]) * y.y)), fmaxf(fabsf(f[2]) * y.z, fabsf(f[3]) * y.w));
   }
-  top = block_max(top, waves);
-  const float s = kv_scale<FMT>(fminf(top, 0x1.fffffep127f));
-  if (tid == 0) c.vs[static_cast<size_t>(to) * c.H + h] = s;
-  if (tid < P) unit[tid] = code_ratio(unit[tid], s);
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) {
+    top_k = fmaxf(top_k, __shfl_xor(top_k, d, kWave));
+    top_v = fmaxf(top_v, __shfl_xor(top_v, d, kWave));
+  }
+  if (lane == 0) {
+    waves[0][w] = top_k;
+    waves[1][w] = top_v;
+  }
   __syncthreads();
+  auto scale_of = [&](const float* m) {
+    return kv_scale<FMT>(fminf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), 0x1.fffffep127f));
+  };
+  const float sk = scale_of(waves[0]), sv = scale_of(waves[1]);
+  if (tid == 0) {
+    c.ks[static_cast<size_t>(to) * c.H + h] = sk;
+    c.vs[static_cast<size_t>(to) * c.H + h] = sv;
+  }
+  if (tid < P) unit_v[tid] = code_ratio(unit_v[tid], sv);
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int e = tid + i * kMBlock;
+    if (e < all) {
+      const float r = code_ratio(u[i], sk);
+      *reinterpret_cast<uint4*>(c.kp + dst + 16 * static_cast<size_t>(e)) =
+          make_uint4(kv_rescale4<FMT>(x[i].x, r), kv_rescale4<FMT>(x[i].y, r), kv_rescale4<FMT>(x[i].z, r),
+                     kv_rescale4<FMT>(x[i].w, r));
+    }
+  }
+  lds_barrier();
   for (int e = tid; e < D << wshift; e += kMBlock) {
     const int d = e >> wshift, t = 4 * (e & (words - 1));
     if (t >= n) continue;
     float f[4];
     kv_decode4<FMT>(*reinterpret_cast<const uint32_t*>(&codes[d * row + t]), f);
-    const float4 u = *reinterpret_cast<const float4*>(&unit[t]);
-    f[0] *= u.x;
-    f[1] *= u.y;
-    f[2] *= u.z;
-    f[3] *= u.w;
-    const uint32_t x = kv_encode4<FMT>(f);
+    const float4 y = *reinterpret_cast<const float4*>(&unit_v[t]);
+    f[0] *= y.x;
+    f[1] *= y.y;
+    f[2] *= y.z;
+    f[3] *= y.w;
+    const uint32_t v = kv_encode4<FMT>(f);
     uint8_t* const out = c.vp + dst + static_cast<size_t>(d) * P + t;
-    if (t + 4 <= n) *reinterpret_cast<uint32_t*>(out) = x;
+    if (t + 4 <= n) *reinterpret_cast<uint32_t*>(out) = v;
     else
-      for (int i = 0; t + i < n; ++i) out[i] = static_cast<uint8_t>(x >> (8 * i));
+      for (int i = 0; t + i < n; ++i) out[i] = static_cast<uint8_t>(v >> (8 * i));
   }
 }
 
 template <int FMT, int M>
 hipError_t launch_move_of(const KvEvict& p, hipStream_t st) {
   const size_t lds = static_cast<size_t>(p.c.D) * v_row(p.c.P);
-  hipLaunchKernelGGL((k_kv_move<FMT, M>), dim3(2 * p.new_width, p.c.H, p.B), dim3(kMBlock), lds, st, p);
+  hipLaunchKernelGGL((k_kv_move<FMT, M>), dim3(p.new_width, p.c.H, p.B), dim3(kMBlock), lds, st, p);
   return hipGetLastError();
 }
 
