@@ -607,20 +607,25 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
  *               sequences that are cut only
  *   1 <= budget <= max_pages * page_size;  0 <= recent <= budget <= limit;
  *   max_pages * page_size <= capacity < 2^31;  B <= 65535;  B * heads *
- *   ceil(budget / page_size) < 2^22
+ *   ceil(budget / page_size) < 2^23;  B * heads * ceil(max_pages * page_size /
+ *   16384) < 2^22
  *   out_table   [B][max_pages] int32: the new pages, then -1, of a sequence
  *               that was cut; else its row of the page table
  *   out_lengths [B] int32: budget, or the length (clamped as the cache's calls do)
  *   out_weights [B][heads][capacity] float: the weights by new position, 0 behind
  *   out_kept    [B][heads][budget] int32: the old positions, or -1 where the
  *               sequence was not cut
+ *   workspace   spec_kv_evict_workspace_size() bytes, 256-byte aligned
  * The outputs overlap neither the inputs nor each other (SPECV_E_OVERLAP).
  * Every layer can be cut by weights of its own: tables and lengths come out
- * alike.  Needs no workspace; nothing synchronises.
+ * alike.  Nothing synchronises.
  */
+size_t spec_kv_evict_workspace_size(const specv_kv_t* kv, int B);
+
 int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* weights, int64_t capacity,
                   const int32_t* new_pages, int budget, int recent, int limit, int B, int32_t* out_table,
-                  int32_t* out_lengths, float* out_weights, int32_t* out_kept, void* stream);
+                  int32_t* out_lengths, float* out_weights, int32_t* out_kept, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 /* Device-side input validation, a debugging aid.  While it is on, every
  * spec_verify* call (spec_verify, _ex, _noalloc, _ragged, _ragged_ex) first

@@ -11,11 +11,11 @@ from ._lib import (DEBUG_COUNTERS, ERRORS, EXPORTS, FLAG_BAD_DRAFT, FLAG_FP64, F
                    tree_mask, verify,
                    verify_tree_greedy, version, workspace_size)
 from ._kv import (KV_DIMS, KV_PAGE_SIZES, SPECV_E4M3, SPECV_I8, KVCache, kv_append, kv_attention,
-                  kv_attention_workspace_size, kv_evict, kv_read, kv_weights)
+                  kv_attention_workspace_size, kv_evict, kv_evict_workspace_size, kv_read, kv_weights)
 from ._prompt import prompt_attention, prompt_weights
 
 __all__ = ["KV_DIMS", "KV_PAGE_SIZES", "KVCache", "SPECV_E4M3", "SPECV_I8", "kv_append", "kv_attention",
-           "kv_attention_workspace_size", "kv_evict", "kv_read", "kv_weights",
+           "kv_attention_workspace_size", "kv_evict", "kv_evict_workspace_size", "kv_read", "kv_weights",
            "prompt_attention", "prompt_weights",
            "DEBUG_COUNTERS", "ERRORS", "EXPORTS", "FLAG_BAD_DRAFT", "FLAG_FP64", "FLAG_ZW_ZERO", "LIB_PATH", "SPECV_BF16", "SPECV_F32",
            "SPECV_MAX_K", "SPECV_MAX_NGRAM", "SPECV_MAX_TREE", "NOALLOC_SCRATCH", "SpecVerifyError",

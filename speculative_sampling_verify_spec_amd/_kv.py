@@ -188,6 +188,23 @@ def _call(device, fn, *args) -> None:
         raise SpecVerifyError(rc, strerror(rc))
 
 
+def _workspace(cache: KVCache, need: int, workspace):
+    """A workspace of at least `need` bytes: the one given, if it is large enough, or a new one; and its bytes."""
+    if need == 0:
+        raise SpecVerifyError(-2, strerror(-2))
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        return torch.empty(need, dtype=torch.uint8, device=cache._device), need
+    if workspace.device != cache._device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    return workspace, have
+
+
+def kv_evict_workspace_size(cache: KVCache, B: int, max_pages: int) -> int:
+    """Workspace bytes of kv_evict for page tables of max_pages columns (0: invalid sizes)."""
+    return int(load().spec_kv_evict_workspace_size(_descriptor(cache, 16, max_pages), B))
+
+
 def kv_append(cache: KVCache, page_table, k, v, lengths, *, counts=None, index=None, out_lengths=None):
     """Quantise tokens into the cache behind each sequence's lengths[b] cached
     ones (spec_kv_append).
@@ -289,14 +306,7 @@ def kv_attention(cache: KVCache, page_table, q, lengths, k_new=None, v_new=None,
     code = _dtype_code(q.dtype)
     kv = _descriptor(cache, page_table.data_ptr(), width)
     lib = load()
-    need = lib.spec_kv_attention_workspace_size(kv, B, N, Hq)
-    if need == 0:
-        raise SpecVerifyError(-2, strerror(-2))
-    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if have < need:
-        workspace, have = torch.empty(need, dtype=torch.uint8, device=cache._device), need
-    elif workspace.device != cache._device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    workspace, have = _workspace(cache, lib.spec_kv_attention_workspace_size(kv, B, N, Hq), workspace)
     out = torch.empty((B, N, Hq, dim), dtype=q.dtype, device=cache._device)
     lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache._device) if return_lse else None
     _call(cache._device, lib.spec_kv_attention, kv, q.data_ptr(), q_row, _ptr(k_new), _ptr(v_new), kv_row,
@@ -363,7 +373,7 @@ def kv_weights(cache: KVCache, page_table, q, lse, lengths, weights, k_new=None,
 
 
 def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: int, recent: int, *,
-             limit: Optional[int] = None, return_kept: bool = False):
+             limit: Optional[int] = None, return_kept: bool = False, workspace=None):
     """Cut sequences of more than limit (default: budget) cached tokens down
     to budget (spec_kv_evict): every head keeps its last `recent` positions and
     the heaviest of the others, in order, in the pages new_pages[b].
@@ -383,10 +393,13 @@ def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: in
     _check_ints(cache, (B,), "lengths", lengths)
     _check_weights(cache, page_table, "weights", weights)
     _check_ints(cache, (B, -(-budget // cache._page)), "new_pages", new_pages)
+    kv = _descriptor(cache, page_table.data_ptr(), width)
+    lib = load()
+    workspace, have = _workspace(cache, lib.spec_kv_evict_workspace_size(kv, B), workspace)
     out_table, out_lengths = torch.empty_like(page_table), torch.empty_like(lengths)
     out_weights = torch.empty(weights.shape, dtype=torch.float32, device=cache._device)
     kept = torch.empty((B, cache._heads, budget), dtype=torch.int32, device=cache._device)
-    _call(cache._device, load().spec_kv_evict, _descriptor(cache, page_table.data_ptr(), width), lengths.data_ptr(),
-          weights.data_ptr(), weights.shape[2], new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B,
-          out_table.data_ptr(), out_lengths.data_ptr(), out_weights.data_ptr(), kept.data_ptr())
+    _call(cache._device, lib.spec_kv_evict, kv, lengths.data_ptr(), weights.data_ptr(), weights.shape[2], new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B,
+          out_table.data_ptr(), out_lengths.data_ptr(), out_weights.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+          have)
     return (out_table, out_lengths, out_weights) + ((kept,) if return_kept else ())

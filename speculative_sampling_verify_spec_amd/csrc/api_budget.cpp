@@ -69,9 +69,19 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
   return launch_kv_weights(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
 }
 
+size_t spec_kv_evict_workspace_size(const specv_kv_t* kv, int B) {
+  using namespace sv;
+  KvView c{};
+  if (check_cache(kv, &c) != SPECV_OK || B < 1 || B > kMaxSeqs) return 0;
+  const long rows = static_cast<long>(B) * c.H, tiles = kv_evict_tiles(c);
+  if (rows * tiles >= (1L << 22)) return 0;  // a grid's threads stay below 2^32
+  return std::max(kAlign, tiles > 1 ? align_up(static_cast<size_t>(rows) * tiles * kEvictWords * sizeof(uint32_t)) : 0);
+}
+
 int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* weights, int64_t capacity,
                   const int32_t* new_pages, int budget, int recent, int limit, int B, int32_t* out_table,
-                  int32_t* out_lengths, float* out_weights, int32_t* kept, void* stream) {
+                  int32_t* out_lengths, float* out_weights, int32_t* kept, void* workspace, size_t workspace_bytes,
+                  void* stream) {
   using namespace sv;
   KvEvict p{};
   if (const int rc = check_cache(kv, &p.c)) return rc;
@@ -82,7 +92,9 @@ int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* wei
     return SPECV_E_SHAPE;
   const long width = (budget + p.c.P - 1) / p.c.P, table = static_cast<long>(B) * p.c.width;
   const long pages = B * width, heads = static_cast<long>(B) * p.c.H, all = heads * capacity, keep = heads * budget;
-  if (heads * width >= (1L << 22)) return SPECV_E_SHAPE;  // a grid's threads stay below 2^32
+  const size_t need = spec_kv_evict_workspace_size(kv, B);
+  if (!need || heads * width >= (1L << 23)) return SPECV_E_SHAPE;  // a grid's threads stay below 2^32
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign || workspace_bytes < need) return SPECV_E_WORKSPACE;
   // workgroups write these while others still read those
   const struct { const void* at; long n; } in[] = {{lengths, B}, {p.c.table, table}, {new_pages, pages}, {weights, all}},
       out[] = {{out_table, table}, {out_lengths, B}, {out_weights, all}, {kept, keep}};
@@ -105,6 +117,8 @@ int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* wei
   p.out_lengths = out_lengths;
   p.out_w = out_weights;
   p.kept = kept;
+  p.tiles = static_cast<int>(kv_evict_tiles(p.c));
+  p.scratch = static_cast<uint32_t*>(workspace);
   return launch_kv_evict(p, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
 }
 

@@ -11,9 +11,9 @@ namespace {
 using frag::lds_barrier;
 
 constexpr int kSBlock = 1024, kSWaves = kSBlock / kWave;
-constexpr int kBins = 2048;
-constexpr int kGroups = 4, kTile = kGroups * 4 * kSBlock;  // groups of four weights a thread holds; weights of a tile
-constexpr int kList = 8192;                                // weights kept in LDS for the last digit
+constexpr int kGroups = 4, kTile = kEvictTile;  // groups of four weights a thread holds; weights of a workgroup
+static_assert(kTile == kGroups * 4 * kSBlock, "a workgroup's weights are in its registers");
+constexpr int kBins = kEvictBins, kList = kEvictList;
 
 // Weights as integers that order as they do (0 has one sign); NaN is below all.
 __device__ inline uint32_t weight_key(float w) {
@@ -22,202 +22,341 @@ __device__ inline uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup per sequence and head: which positions stay.  The weight of
-// the last one to stay is found by its digits (11, 11 and 10 bits, from the
-// highest): a pass counts the weights by their next digit among those that
-// agree with the digits found.  What is above that weight stays, and of those
-// equal to it the first ones.  A thread holds 16 weights; up to 16384 stay in
-// registers from the first pass to the last, longer rows are read again for
-// the second digit and at the end (for the third if more than 8192 weights
-// agree in the first).
-__global__ __launch_bounds__(kSBlock) void k_kv_select(KvEvict p) {
-  const KvView& c = p.c;
-  const int h = blockIdx.x, tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const long b = blockIdx.y;
-  const int len = kv_len(c, p.lengths, b);
-  const bool cut = len > p.limit;
-  const long base = (b * c.H + h) * p.capacity;
-  const float* const row = p.w + base;
-  float* const out_row = p.out_w + base;
-  int32_t* const kept = p.kept + (b * c.H + h) * static_cast<long>(p.budget);
-  const int after = cut ? p.budget : len;
+// Inclusive prefix sum over the lanes of a wave: in rows of 16 lanes, then + the rows' totals.
+__device__ inline uint32_t lanes_upto(uint32_t v) {
+  int s = static_cast<int>(v);
+  s += dpp_i32<0x111, 0xf>(static_cast<int>(v));
+  s += dpp_i32<0x112, 0xf>(static_cast<int>(v));
+  s += dpp_i32<0x113, 0xf>(static_cast<int>(v));
+  s += dpp_i32<0x114, 0xf, 0xe>(s);
+  s += dpp_i32<0x118, 0xf, 0xc>(s);
+  s += dpp_i32<0x142, 0xa>(s);
+  s += dpp_i32<0x143, 0xc>(s);
+  return static_cast<uint32_t>(s);
+}
 
-  // weights 4 (tid + 1024 j) .. of a tile; behind the row 0
+__device__ inline uint32_t lane_of(uint32_t v, int lane) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane)); }
+
+// How many of the lanes before this one, added to `sum`.
+__device__ inline uint32_t lanes_before(uint64_t m, uint32_t sum) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), sum));
+}
+
+// A sequence's head in the choice: its weights, and what is to be chosen.
+struct Choice {
+  const float* row;
+  float* out_row;
+  int32_t* kept;
+  int len, n;     // positions, and the first n of them to choose among
+  int need;       // how many
+  bool cut;
+  long pair;
+};
+__device__ inline Choice choice(const KvEvict& p, long b, int h) {
+  Choice x;
+  x.len = kv_len(p.c, p.lengths, b);
+  x.cut = x.len > p.limit;
+  x.n = x.len - p.recent;
+  x.need = p.budget - p.recent;
+  x.pair = b * p.c.H + h;
+  x.row = p.w + x.pair * p.capacity;
+  x.out_row = p.out_w + x.pair * p.capacity;
+  x.kept = p.kept + x.pair * static_cast<long>(p.budget);
+  return x;
+}
+
+// A workgroup's weights: a thread has 4 (tid + 1024 j) .. + 3 of a tile.  What
+// is behind the row, or behind its capacity, is any number.
+struct Held {
   struct __attribute__((packed, aligned(4))) Four { float x[4]; };
   Four v[kGroups];
-  auto load = [&](int tile) {
+  int at0;
+  __device__ void load(const float* row, int len, long capacity, int tile) {
+    at0 = tile * kTile;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
-      const int at = tile * kTile + 4 * (tid + j * kSBlock);
-      if (at + 4 <= len) v[j] = *reinterpret_cast<const Four*>(row + at);
-      else
+      if (at0 + 4 * j * kSBlock >= len) break;
+      const int at = place(j);
+      if (at0 + 4 * (j + 1L) * kSBlock <= capacity) {
+        v[j] = *reinterpret_cast<const Four*>(row + at);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[j].x[k] = at + k < len ? row[at + k] : 0.f;
+        for (int k = 0; k < 4; ++k) v[j].x[k] = row[min(static_cast<long>(at + k), capacity - 1)];
+      }
     }
-  };
-  // use(position, weight): of a tile's existing weights
-  auto each = [&](int tile, auto&& use) {
+  }
+  __device__ int place(int j) const { return at0 + 4 * (static_cast<int>(threadIdx.x) + j * kSBlock); }
+  // use(position, weight), by all lanes of a wave at once
+  template <class F>
+  __device__ void each(int len, F&& use) const {
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
-      if (tile * kTile + 4 * j * kSBlock >= len) break;
-      const int at = tile * kTile + 4 * (tid + j * kSBlock);
+      if (at0 + 4 * j * kSBlock >= len) break;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) use(at + k, v[j].x[k]);
+      for (int k = 0; k < 4; ++k) use(place(j) + k, v[j].x[k]);
     }
-  };
-  const int ntile = (len + kTile - 1) / kTile;
-  if (ntile) load(0);
+  }
+};
 
-  if (h == 0) {
+// What the workgroups of a long row tell each other (KvEvict.scratch): their
+// counts by the first digit; then how many of their weights are above that
+// digit, and those that have it (if they are not too many).
+struct Told {
+  uint32_t over, same, digit, need;
+};
+__device__ inline uint32_t* bins_of(const KvEvict& p, long pair, int tile) {
+  return p.scratch + (pair * p.tiles + tile) * kEvictWords;
+}
+__device__ inline uint32_t* list_of(const KvEvict& p, long pair, int tile) { return bins_of(p, pair, tile) + kBins; }
+__device__ inline Told* told_of(const KvEvict& p, long pair, int tile) {
+  return reinterpret_cast<Told*>(list_of(p, pair, tile) + kList);
+}
+
+// Long rows, first: a workgroup per 16384 weights counts them by their highest 11 bits.
+__global__ __launch_bounds__(kSBlock) void k_kv_count(KvEvict p) {
+  const Choice x = choice(p, blockIdx.z, blockIdx.y);
+  const int tile = blockIdx.x, tid = threadIdx.x;
+  if (!x.cut || tile * kTile >= x.len) return;
+  Held v;
+  v.load(x.row, x.len, p.capacity, tile);
+  __shared__ uint32_t hist[kBins][2];  // even and odd lanes: fewer of a wave at the same place
+  static_assert(kBins == 2 * kSBlock, "two bins a thread");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) (&hist[0][0])[tid + i * kSBlock] = 0;
+  __syncthreads();
+  v.each(x.len, [&](int at, float w) {
+    if (at < x.n) atomicAdd(&hist[weight_key(w) >> 21][tid & 1], 1u);
+  });
+  __syncthreads();
+  uint32_t* const bins = bins_of(p, x.pair, tile);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) bins[tid + i * kSBlock] = hist[tid + i * kSBlock][0] + hist[tid + i * kSBlock][1];
+}
+
+// Long rows, second: every workgroup of a row finds the digit that the last
+// weight to stay has, and lists its own weights that have it.
+__global__ __launch_bounds__(kSBlock) void k_kv_list(KvEvict p) {
+  const Choice x = choice(p, blockIdx.z, blockIdx.y);
+  const int tile = blockIdx.x, tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  if (!x.cut || tile * kTile >= x.len) return;
+  Held v;
+  v.load(x.row, x.len, p.capacity, tile);
+  const int ntile = (x.len + kTile - 1) / kTile, top = kBins - 1 - 2 * tid;
+  uint32_t x0 = 0, x1 = 0;  // a thread's two bins, counted from the top
+  for (int t = 0; t < ntile; ++t) {
+    const uint2 y = *reinterpret_cast<const uint2*>(bins_of(p, x.pair, t) + top - 1);
+    x0 += y.y;
+    x1 += y.x;
+  }
+  __shared__ uint32_t wave_at[kSWaves], digit, need, over, same;
+  uint32_t upto = lanes_upto(x0 + x1);
+  if (lane == kWave - 1) wave_at[w] = upto;
+  if (tid == 0) {
+    digit = kBins;  // nothing to choose: none has it
+    need = over = same = 0;
+  }
+  __syncthreads();
+  for (int i = 0; i < w; ++i) upto += wave_at[i];
+  const uint32_t above = upto - x0 - x1, want = static_cast<uint32_t>(x.need);
+  if (above < want && upto >= want) {
+    const bool first = above + x0 >= want;
+    digit = first ? top : top - 1;
+    need = want - (first ? above : above + x0);
+  }
+  __syncthreads();
+  uint32_t* const list = list_of(p, x.pair, tile);
+  const uint32_t found = digit;
+  uint32_t more = 0;
+  v.each(x.len, [&](int at, float y) {
+    const uint32_t key = weight_key(y);
+    const bool chosen = at < x.n, agrees = chosen && key >> 21 == found;
+    more += at < x.len && (!chosen || key >> 21 > found) ? 1u : 0u;
+    const uint64_t m = __ballot(agrees);
+    if (!m) return;
+    uint32_t first = 0;
+    if (lane == 0) first = atomicAdd(&same, static_cast<uint32_t>(__popcll(m)));  // in any order: they are only counted
+    const uint32_t i = lanes_before(m, __builtin_amdgcn_readfirstlane(first));
+    if (agrees && i < kList) list[i] = key;
+  });
+  more = lane_of(lanes_upto(more), kWave - 1);
+  if (lane == 0 && more) atomicAdd(&over, more);
+  __syncthreads();
+  if (tid == 0) *told_of(p, x.pair, tile) = Told{over, same, found, need};
+}
+
+// One workgroup per sequence, head and 16384 positions: which of them stay.
+// The weight of the last one to stay is found by its digits, from the highest:
+// a pass counts the weights by their next 8 bits among those that agree with
+// the digits found, in a table of its own, which every wave then looks through
+// for itself.  What is above that weight stays, and of those equal to it the
+// first ones.  Rows of up to 16384 weights are in the workgroup's registers
+// (MANY false).  Of longer ones the first 11 bits are known, and the weights
+// that have them are listed by the workgroups of the row (or read again, where
+// a workgroup has more of them than its list takes).
+template <bool MANY>
+__global__ __launch_bounds__(kSBlock) void k_kv_select(KvEvict p) {
+  const KvView& c = p.c;
+  const int tile = MANY ? blockIdx.x : 0, h = blockIdx.y, tid = threadIdx.x, lane = tid % kWave;
+  const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const long b = blockIdx.z;
+  const Choice x = choice(p, b, h);
+  const int after = x.cut ? p.budget : x.len, ntile = (x.len + kTile - 1) / kTile;
+  Held v;
+  v.load(x.row, x.len, p.capacity, tile);
+  __shared__ uint32_t hist[4][256][4];  // a pass's counts, four lanes' apart: fewer of a wave at the same place
+#pragma unroll
+  for (int i = 0; i < 4; ++i) (&hist[i][0][0])[tid] = 0;
+  if (h == 0 && tile == 0) {
     if (tid == 0) p.out_lengths[b] = after;
     for (int i = tid; i < c.width; i += kSBlock)
-      p.out_table[b * c.width + i] = !cut ? c.table[b * c.width + i] : i < p.new_width ? p.new_pages[b * p.new_width + i] : -1;
+      p.out_table[b * c.width + i] = !x.cut ? c.table[b * c.width + i] : i < p.new_width ? p.new_pages[b * p.new_width + i] : -1;
   }
-  for (long i = after + tid; i < p.capacity; i += kSBlock) out_row[i] = 0.f;
-  if (!cut) {
-    for (int t = 0; t < ntile; ++t) {
-      if (t) load(t);
-      each(t, [&](int at, float x) {
-        if (at < len) out_row[at] = x;
-      });
-    }
-    for (int i = tid; i < p.budget; i += kSBlock) kept[i] = -1;
+  const long end = MANY && tile + 1 < p.tiles ? (tile + 1L) * kTile : p.capacity;
+  for (long i = max(static_cast<long>(after), static_cast<long>(tile) * kTile) + tid; i < end; i += kSBlock) x.out_row[i] = 0.f;
+  if (!x.cut) {
+    v.each(x.len, [&](int at, float y) {
+      if (at < x.len) x.out_row[at] = y;
+    });
+    if (tile == 0)
+      for (int i = tid; i < p.budget; i += kSBlock) x.kept[i] = -1;
     return;
   }
+  if (tile >= ntile) return;
 
-  const int n = len - p.recent;  // the positions to choose among
-  int need = p.budget - p.recent;
-  const bool some = need > 0;
-  __shared__ uint32_t hist[kBins], list[kList];
-  __shared__ uint32_t wave_at[kSWaves], digit_found, rest_found, listed;
-  uint32_t found = 0;  // the digits found
+  uint32_t found = 0, need = static_cast<uint32_t>(x.need);
+  const bool some = x.need > 0;
+  uint32_t out = 0, ties = 0;  // what stays above, and the equal weights, before the tile
+  if constexpr (MANY) {
+    const Told mine = *told_of(p, x.pair, tile);
+    found = mine.digit << 21;
+    need = mine.need;
+  }
+  // a tile's weights that may be the last to stay: use(key)
+  auto candidates = [&](int t, uint32_t mask, auto&& use) {
+    if constexpr (MANY) {
+      const uint32_t same = told_of(p, x.pair, t)->same;
+      const uint32_t* const list = list_of(p, x.pair, t);
+      if (same <= kList) {
+        for (uint32_t i = tid; i < same; i += kSBlock)
+          if ((list[i] & mask) == (found & mask)) use(list[i]);
+        return;
+      }
+      if (t != tile) {
+        Held other;
+        other.load(x.row, x.len, p.capacity, t);
+        other.each(x.len, [&](int at, float y) {
+          const uint32_t key = weight_key(y);
+          if (at < x.n && (key & mask) == (found & mask)) use(key);
+        });
+        return;
+      }
+    }
+    v.each(x.len, [&](int at, float y) {
+      const uint32_t key = weight_key(y);
+      if (at < x.n && (key & mask) == (found & mask)) use(key);
+    });
+  };
+  __syncthreads();
   if (some) {
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? ~0u << 21 : ~0u << 10, digit = pass == 2 ? 1023u : 2047u;
-      hist[tid] = hist[tid + kSBlock] = 0;
-      if (tid == 0 && pass < 2) listed = 0;
-      __syncthreads();
-      auto count = [&](uint32_t key) { atomicAdd(&hist[(key >> shift) & digit], 1u); };
-      if (pass == 2 && ntile > 1 && listed <= kList) {
-        for (uint32_t i = tid; i < listed; i += kSBlock)
-          if ((list[i] & mask) == found) count(list[i]);
-      } else {
-#pragma unroll 1
-        for (int t = 0; t < ntile; ++t) {
-          if (ntile > 1) load(t);
-          each(t, [&](int at, float x) {
-            const uint32_t key = weight_key(x);
-            const bool agrees = at < n && (key & mask) == found;
-            if (agrees) count(key);
-            if (pass == 1 && ntile > 1) {
-              const uint64_t m = __ballot(agrees);
-              if (!m) return;
-              uint32_t first = 0;
-              if (lane == 0) first = atomicAdd(&listed, static_cast<uint32_t>(__popcll(m)));
-              const uint32_t i = __builtin_amdgcn_readfirstlane(first) +
-                                 __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), 0u));
-              if (agrees && i < kList) list[i] = key;
-            }
-          });
-        }
-      }
-      __syncthreads();
-      // the highest digit with `need` weights at and above it: a thread has two bins, counted from the top
-      const int top = kBins - 1 - 2 * tid;
-      const uint32_t x0 = hist[top], x1 = hist[top - 1];
-      uint32_t sum = x0 + x1;
+    constexpr int kPasses = MANY ? 3 : 4;
 #pragma unroll
-      for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t y = __shfl_up(sum, d, kWave);
-        if (lane >= d) sum += y;
-      }
-      if (lane == kWave - 1) wave_at[w] = sum;
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int upper = MANY ? 21 - 8 * pass : 32 - 8 * pass, shift = upper > 8 ? upper - 8 : 0;  // bits below those found
+      const uint32_t mask = upper == 32 ? 0u : ~0u << upper;
+      for (int t = 0; t < (MANY ? ntile : 1); ++t)
+        candidates(t, mask, [&](uint32_t key) { atomicAdd(&hist[pass][(key >> shift) & 255u & ~(mask >> shift)][lane & 3], 1u); });
       __syncthreads();
-      for (int i = 0; i < w; ++i) sum += wave_at[i];
-      const uint32_t above = sum - x0 - x1;  // weights with a higher digit than this thread's
-      if (above < static_cast<uint32_t>(need) && sum >= static_cast<uint32_t>(need)) {
-        const bool first = above + x0 >= static_cast<uint32_t>(need);
-        digit_found = first ? top : top - 1;
-        rest_found = first ? above : above + x0;
+      // the highest digit with `need` weights at and above it: a lane has four, counted from the top
+      uint32_t n[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(&hist[pass][255 - 4 * lane - i][0]);
+        n[i] = y.x + y.y + y.z + y.w;
+        sum += n[i];
       }
-      __syncthreads();
-      found |= digit_found << shift;
-      need -= static_cast<int>(rest_found);
+      const uint32_t upto = lanes_upto(sum);
+      const int at = __builtin_ctzll(__ballot(upto >= need));  // need is at most the count of all
+      uint32_t above = lane_of(upto - sum, at);
+      int digit = 255 - 4 * at;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t y = lane_of(n[i], at);
+        const bool next = above + y < need && digit == 255 - 4 * at - i;
+        above += next ? y : 0u;
+        digit -= next ? 1 : 0;
+      }
+      need -= above;
+      found |= static_cast<uint32_t>(digit) << shift;
     }
   }
-
-  // `need` of the weights equal to `found` stay, the first ones, and all above.
-  // Positions of a tile go up with the group, the wave, the lane and the place
-  // in the four: a count for each group and wave, scanned by every wave.
-  const uint32_t last = static_cast<uint32_t>(need);
-  uint32_t out = 0, ties = 0;  // what stays above, and the equal weights, before the tile
-  __shared__ uint32_t counts[2][kGroups * kSWaves];
-  static_assert(kGroups * kSWaves == kWave, "a lane per group and wave");
-#pragma unroll 1
-  for (int t = 0; t < ntile; ++t) {
-    if (ntile > 1) load(t);
-    uint32_t over = 0, tie = 0;  // bit 4 j + k
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      const int at = t * kTile + 4 * (tid + j * kSBlock);
-      uint32_t mine = 0;  // counts of the group's four: above, and equal in the upper half
-      if (t * kTile + 4 * j * kSBlock < len) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t key = weight_key(v[j].x[k]);
-          const bool chosen = at + k < n;
-          const bool o = at + k < len && (!chosen || (some && key > found)), e = chosen && some && key == found;
-          over |= o ? 1u << (4 * j + k) : 0u;
-          tie |= e ? 1u << (4 * j + k) : 0u;
-          mine += static_cast<uint32_t>(__popcll(__ballot(o))) + (static_cast<uint32_t>(__popcll(__ballot(e))) << 16);
-        }
-      }
-      if (lane == 0) counts[t & 1][j * kSWaves + w] = mine;
+  // `need` of the weights equal to `found` stay, the first ones, and all above
+  if constexpr (MANY) {
+    __shared__ uint32_t before[2];
+    if (tid < 2) before[tid] = 0;
+    __syncthreads();
+    uint32_t more = 0, equal = 0;
+    for (int t = 0; t < tile; ++t) {
+      if (tid == 0) more += told_of(p, x.pair, t)->over;
+      if (some)
+        candidates(t, ~0u << 21, [&](uint32_t key) {
+          more += key > found ? 1u : 0u;
+          equal += key == found ? 1u : 0u;
+        });
+    }
+    more = lane_of(lanes_upto(more), kWave - 1);
+    equal = lane_of(lanes_upto(equal), kWave - 1);
+    if (lane == 0) {
+      atomicAdd(&before[0], more);
+      atomicAdd(&before[1], equal);
     }
     __syncthreads();
-    const uint32_t own = counts[t & 1][lane];  // at most 16384 in all: the halves do not meet
-    uint32_t upto = own;
+    out = before[0];
+    ties = before[1];
+  }
+  // Positions go up with the group, the wave, the lane and the place in the
+  // four: a count for each group and wave, scanned by every wave.
+  __shared__ uint32_t counts[kGroups * kSWaves];
+  static_assert(kGroups * kSWaves == kWave, "a lane per group and wave");
+  uint32_t over = 0, tie = 0;  // bit 4 j + k
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-      const uint32_t y = __shfl_up(upto, d, kWave);
-      if (lane >= d) upto += y;
-    }
-    const uint32_t before = upto - own;
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j) {
-      if (t * kTile + 4 * j * kSBlock >= len) break;
-      const int at = t * kTile + 4 * (tid + j * kSBlock);
-      const uint32_t x = __builtin_amdgcn_readlane(before, j * kSWaves + w);
-      uint32_t equal = ties + (x >> 16);  // equal weights before this lane's
-      uint32_t rank = out + (x & 0xffffu);
-      const uint32_t o = over >> (4 * j) & 15u, e = tie >> (4 * j) & 15u;
-      auto lanes_before = [&](uint32_t bits) {
-        uint32_t sum = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t m = __ballot(bits >> k & 1u);
-          sum = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(m), sum));
-        }
-        return sum;
-      };
-      equal += lanes_before(e);
-      rank += lanes_before(o) + min(equal, last);  // of the equal ones, the first `last` stay
+  for (int j = 0; j < kGroups; ++j) {
+    uint32_t mine = 0;  // counts of the group's four: above, and equal in the upper half
+    if (v.at0 + 4 * j * kSBlock < x.len) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const bool eq = e >> k & 1u, stays = (o >> k & 1u) || (eq && equal < last);
-        equal += eq ? 1u : 0u;
-        if (stays) {
-          kept[rank] = at + k;
-          out_row[rank] = v[j].x[k];
-          ++rank;
-        }
+        const int at = v.place(j) + k;
+        const uint32_t key = weight_key(v.v[j].x[k]);
+        const bool chosen = at < x.n, o = at < x.len && (!chosen || (some && key > found)), e = chosen && some && key == found;
+        over |= o ? 1u << (4 * j + k) : 0u;
+        tie |= e ? 1u << (4 * j + k) : 0u;
+        mine += static_cast<uint32_t>(__popcll(__ballot(o))) + (static_cast<uint32_t>(__popcll(__ballot(e))) << 16);
       }
     }
-    const uint32_t all = __builtin_amdgcn_readlane(upto, kWave - 1);
-    out += all & 0xffffu;
-    ties += all >> 16;
+    if (lane == 0) counts[j * kSWaves + w] = mine;
+  }
+  __syncthreads();
+  const uint32_t own = counts[lane], before = lanes_upto(own) - own;  // at most 16384 in all: the halves do not meet
+#pragma unroll
+  for (int j = 0; j < kGroups; ++j) {
+    if (v.at0 + 4 * j * kSBlock >= x.len) break;
+    const uint32_t y = lane_of(before, j * kSWaves + w), o = over >> (4 * j) & 15u, e = tie >> (4 * j) & 15u;
+    uint32_t equal = ties + (y >> 16), rank = out + (y & 0xffffu);  // before this lane's
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      equal = lanes_before(__ballot(e >> k & 1u), equal);
+      rank = lanes_before(__ballot(o >> k & 1u), rank);
+    }
+    rank += min(equal, need);  // of the equal ones, the first `need` stay
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool eq = e >> k & 1u, stays = (o >> k & 1u) || (eq && equal < need);
+      equal += eq ? 1u : 0u;
+      if (stays) {
+        x.kept[rank] = v.place(j) + k;
+        x.out_row[rank] = v.v[j].x[k];
+        ++rank;
+      }
+    }
   }
 }
 
@@ -235,8 +374,12 @@ __device__ inline float largest16(const uint4& v) {
   return fmaxf(fmaxf(largest4<FMT>(v.x), largest4<FMT>(v.y)), fmaxf(largest4<FMT>(v.z), largest4<FMT>(v.w)));
 }
 
-// What a token's codes are multiplied by; finite, so that a code of 0 stays 0.
-__device__ inline float code_ratio(float from, float to) { return fminf(from / to, 0x1.fffffep127f); }
+// What a token's codes are multiplied by, from its scale and the new one's
+// reciprocal (a power of two too); finite, so that a code of 0 stays 0.
+__device__ inline float code_ratio(float from, float per_to) { return fminf(from * per_to, kLargest<SPECV_F32>); }
+
+// 1 / s of a power of two 2^-126 .. 2^126, exactly.
+__device__ inline float reciprocal(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
 // Bytes of a channel's row of V codes in LDS: whole words, an odd number of
 // them, so that 64 channels' same token falls into 64 different banks.
@@ -271,7 +414,8 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
   __shared__ __align__(16) float unit_k[128], unit_v[128];  // the scales
   __shared__ float waves[2][kMWaves];
   extern __shared__ __align__(16) uint8_t codes[];  // V: [D][v_row(P)]
-  const size_t bytes = static_cast<size_t>(P) * D, dst = (static_cast<size_t>(to) * c.H + h) * bytes;
+  const size_t bytes = static_cast<size_t>(P) * D;
+  const size_t dst = (static_cast<size_t>(to) * c.H + h) * bytes;
   const size_t blk_k = static_cast<size_t>(max(page_k, 0)) * c.H + h;
   if (tid < P) row_at[tid] = page_k < 0 ? ~size_t(0) : blk_k * bytes + static_cast<size_t>(at_k & (P - 1)) * D;
   const float ks = tid < P && page_k >= 0 ? c.ks[blk_k] : 0.f, vs = tid < P && page_k >= 0 ? c.vs[blk_k] : 0.f;
@@ -346,70 +490,87 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
     unit_k[tid] = ks;
     unit_v[tid] = vs;
   }
-  __syncthreads();
+  lds_barrier();
   // ---- the new scales ----
-  float top_k = 0.f, top_v = 0.f, u[kMost];
+  // A thread's words of four V codes, kMost * 4 at most, are a workgroup's
+  // threads apart: of different channels, but always of the same four tokens.
+  const int wshift = c.pshift - 2, vt = 4 * (tid & ((1 << wshift) - 1)), vall = D << wshift;
+  auto word = [&](int e) {
+    return e < vall && vt < n ? *reinterpret_cast<const uint32_t*>(&codes[(e >> wshift) * row + vt]) : 0u;
+  };
+  float most[4] = {0.f, 0.f, 0.f, 0.f};
+  float top_k = 0.f, u[kMost];
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int e = tid + i * kMBlock;
     u[i] = e < all ? unit_k[e * inv >> 16] : 0.f;
     top_k = fmaxf(top_k, largest16<FMT>(x[i]) * u[i]);
   }
-  // words of four codes; of a row's, the last ones may be behind the last token
-  const int wshift = c.pshift - 2, words = 1 << wshift;
-  for (int e = tid; e < D << wshift; e += kMBlock) {
-    const int d = e >> wshift, t = 4 * (e & (words - 1));
-    if (t >= n) continue;
-    float f[4];
-    kv_decode4<FMT>(*reinterpret_cast<const uint32_t*>(&codes[d * row + t]), f);
-    const float4 y = *reinterpret_cast<const float4*>(&unit_v[t]);  // 0 behind the last token
-    top_v = fmaxf(fmaxf(top_v, fmaxf(fabsf(f[0]) * y.x, fabsf(f[1]) * y.y)), fmaxf(fabsf(f[2]) * y.z, fabsf(f[3]) * y.w));
-  }
 #pragma unroll
-  for (int d = 32; d > 0; d /= 2) {
-    top_k = fmaxf(top_k, __shfl_xor(top_k, d, kWave));
-    top_v = fmaxf(top_v, __shfl_xor(top_v, d, kWave));
+  for (int i = 0; i < 4 * kMost; ++i) {
+    float f[4];
+    kv_decode4<FMT>(word(tid + i * kMBlock), f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) most[k] = fmaxf(most[k], fabsf(f[k]));  // NaN does not count
   }
+  const float4 uv = *reinterpret_cast<const float4*>(&unit_v[vt]);  // 0 behind the last token
+  float top_v = fmaxf(fmaxf(most[0] * uv.x, most[1] * uv.y), fmaxf(most[2] * uv.z, most[3] * uv.w));
+  top_k = wave_max(top_k);
+  top_v = wave_max(top_v);
   if (lane == 0) {
     waves[0][w] = top_k;
     waves[1][w] = top_v;
   }
-  __syncthreads();
-  auto scale_of = [&](const float* m) {
-    return kv_scale<FMT>(fminf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), 0x1.fffffep127f));
-  };
-  const float sk = scale_of(waves[0]), sv = scale_of(waves[1]);
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < kMWaves; ++i) {
+    top_k = fmaxf(top_k, waves[0][i]);
+    top_v = fmaxf(top_v, waves[1][i]);
+  }
+  const float sk = kv_scale<FMT>(fminf(top_k, kLargest<SPECV_F32>)), sv = kv_scale<FMT>(fminf(top_v, kLargest<SPECV_F32>));
   if (tid == 0) {
     c.ks[static_cast<size_t>(to) * c.H + h] = sk;
     c.vs[static_cast<size_t>(to) * c.H + h] = sv;
   }
-  if (tid < P) unit_v[tid] = code_ratio(unit_v[tid], sv);
+  // ---- the codes in their units: all in the format's range, unless a value passed that of 32 bits ----
+  const float per_sk = reciprocal(sk), per_sv = reciprocal(sv);
+  const float rv[4] = {code_ratio(uv.x, per_sv), code_ratio(uv.y, per_sv), code_ratio(uv.z, per_sv), code_ratio(uv.w, per_sv)};
+  auto write = [&](auto encode) {
 #pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    const int e = tid + i * kMBlock;
-    if (e < all) {
-      const float r = code_ratio(u[i], sk);
-      *reinterpret_cast<uint4*>(c.kp + dst + 16 * static_cast<size_t>(e)) =
-          make_uint4(kv_rescale4<FMT>(x[i].x, r), kv_rescale4<FMT>(x[i].y, r), kv_rescale4<FMT>(x[i].z, r),
-                     kv_rescale4<FMT>(x[i].w, r));
+    for (int i = 0; i < kMost; ++i) {
+      const int e = tid + i * kMBlock;
+      const float r = code_ratio(u[i], per_sk), rk[4] = {r, r, r, r};
+      if (e < all)
+        *reinterpret_cast<uint4*>(c.kp + dst + 16 * static_cast<size_t>(e)) =
+            make_uint4(encode(x[i].x, rk), encode(x[i].y, rk), encode(x[i].z, rk), encode(x[i].w, rk));
     }
-  }
-  lds_barrier();
-  for (int e = tid; e < D << wshift; e += kMBlock) {
-    const int d = e >> wshift, t = 4 * (e & (words - 1));
-    if (t >= n) continue;
-    float f[4];
-    kv_decode4<FMT>(*reinterpret_cast<const uint32_t*>(&codes[d * row + t]), f);
-    const float4 y = *reinterpret_cast<const float4*>(&unit_v[t]);
-    f[0] *= y.x;
-    f[1] *= y.y;
-    f[2] *= y.z;
-    f[3] *= y.w;
-    const uint32_t v = kv_encode4<FMT>(f);
-    uint8_t* const out = c.vp + dst + static_cast<size_t>(d) * P + t;
-    if (t + 4 <= n) *reinterpret_cast<uint32_t*>(out) = v;
-    else
-      for (int i = 0; t + i < n; ++i) out[i] = static_cast<uint8_t>(v >> (8 * i));
+#pragma unroll
+    for (int i = 0; i < 4 * kMost; ++i) {
+      const int e = tid + i * kMBlock;
+      const uint32_t v = encode(word(e), rv);
+      uint8_t* const out = c.vp + dst + static_cast<size_t>(e >> wshift) * P + vt;
+      if (e < vall && vt + 4 <= n) *reinterpret_cast<uint32_t*>(out) = v;
+      else if (e < vall)
+        for (int k = 0; vt + k < n; ++k) out[k] = static_cast<uint8_t>(v >> (8 * k));
+    }
+  };
+  auto product = [](uint32_t code, const float* r, float* f) {
+    kv_decode4<FMT>(code, f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] *= r[k];
+  };
+  if (fmaxf(top_k, top_v) <= kLargest<SPECV_F32>) {
+    write([&](uint32_t code, const float* r) {
+      float f[4];
+      product(code, r, f);
+      return kv_encode4_finite<FMT>(f);  // NaN stays NaN in e4m3, and int8 has none
+    });
+  } else {
+    write([&](uint32_t code, const float* r) {
+      float f[4];
+      product(code, r, f);
+      return kv_encode4<FMT>(f);
+    });
   }
 }
 
@@ -432,7 +593,14 @@ hipError_t launch_move(const KvEvict& p, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_kv_evict(const KvEvict& p, int fmt, hipStream_t st) {
-  hipLaunchKernelGGL(k_kv_select, dim3(p.c.H, p.B), dim3(kSBlock), 0, st, p);
+  const dim3 grid(p.tiles, p.c.H, p.B);
+  if (p.tiles > 1) {
+    hipLaunchKernelGGL(k_kv_count, grid, dim3(kSBlock), 0, st, p);
+    hipLaunchKernelGGL(k_kv_list, grid, dim3(kSBlock), 0, st, p);
+    hipLaunchKernelGGL((k_kv_select<true>), grid, dim3(kSBlock), 0, st, p);
+  } else {
+    hipLaunchKernelGGL((k_kv_select<false>), grid, dim3(kSBlock), 0, st, p);
+  }
   if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   return fmt == SPECV_E4M3 ? launch_move<SPECV_E4M3>(p, st) : launch_move<SPECV_I8>(p, st);
 }

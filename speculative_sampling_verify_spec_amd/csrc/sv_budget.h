@@ -34,7 +34,16 @@ struct KvEvict {
   int32_t* out_lengths;     // [B]
   float* out_w;             // [B][H][capacity]
   int32_t* kept;            // [B][H][budget]
+  int tiles;                // workgroups that share a head's choice (kv_evict_tiles)
+  uint32_t* scratch;        // [B][H][tiles][kEvictWords] if there are several
 };
+
+// The weights that a workgroup of the choice holds; the counts by the first 11
+// bits and the list of those weights that workgroups of the same row tell each
+// other, and with two more counts and two findings what that takes.
+constexpr int kEvictTile = 16384, kEvictBins = 2048, kEvictList = 2044;
+constexpr int kEvictWords = kEvictBins + kEvictList + 4;
+inline long kv_evict_tiles(const KvView& c) { return ((static_cast<long>(c.width) << c.pshift) + kEvictTile - 1) / kEvictTile; }
 
 hipError_t launch_kv_weights(const KvWeights& p, int dtype, int fmt, hipStream_t s);
 hipError_t launch_kv_evict(const KvEvict& p, int fmt, hipStream_t s);

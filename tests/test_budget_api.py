@@ -28,11 +28,12 @@ def weigh(lib, c=None, **kw):
 
 def evict(lib, c=None, **kw):
     a = dict(lengths=9 * BASE, w=FAR, C=640, new=10 * BASE, budget=100, recent=10, limit=200, B=4, table=11 * BASE,
-             out_len=12 * BASE, out=2 * FAR, kept=3 * FAR)
+             out_len=12 * BASE, out=2 * FAR, kept=3 * FAR, ws=16 * BASE, wsb=1 << 40)
     a.update(kw)
     c = kv() if c is None else c
     return lib.spec_kv_evict(ctypes.byref(c), a["lengths"], a["w"], a["C"], a["new"], a["budget"], a["recent"],
-                             a["limit"], a["B"], a["table"], a["out_len"], a["out"], a["kept"], None)
+                             a["limit"], a["B"], a["table"], a["out_len"], a["out"], a["kept"], a["ws"],
+                             a["wsb"], None)
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHE)
@@ -60,7 +61,7 @@ def test_weights_of_too_many_heads(lib):
     (dict(lengths=None), -1), (dict(w=None), -1), (dict(new=None), -1), (dict(table=None), -1), (dict(out_len=None), -1),
     (dict(out=None), -1), (dict(kept=None), -1), (dict(B=0), -2), (dict(B=65536), -2), (dict(budget=0), -2),
     (dict(budget=641, limit=700), -2), (dict(recent=-1), -2), (dict(recent=101), -2), (dict(limit=99), -2),
-    (dict(C=639), -2), (dict(C=1 << 31), -2)])
+    (dict(C=639), -2), (dict(C=1 << 31), -2), (dict(ws=None), -5), (dict(ws=BASE + 16), -5), (dict(wsb=255), -5)])
 def test_evict_refusals(lib, kw, code):
     assert evict(lib, **kw) == code
 
@@ -81,9 +82,22 @@ def test_evict_overlap(lib):
 
 
 def test_evict_of_too_many_pages(lib):
-    c = kv(heads=512, page_size=16, max_pages=1 << 14)
+    c = kv(heads=512, page_size=16, max_pages=1 << 15)
     far = {n: (i + 1) << 44 for i, n in enumerate(("lengths", "w", "new", "table", "out_len", "out", "kept"))}
-    assert evict(lib, c, C=1 << 18, budget=1 << 17, limit=1 << 17, B=1, **far) == -2
+    assert evict(lib, c, C=1 << 19, budget=1 << 19, limit=1 << 19, B=1, **far) == -2
+
+
+def test_evict_workspace_sizes(lib):
+    """256 bytes up to 16384 positions, then counts and lists of every 16384 of a head; 0 for what is refused."""
+    def size(B, **kw):
+        return lib.spec_kv_evict_workspace_size(ctypes.byref(kv(**kw)), B)
+    assert size(4) == size(4, max_pages=256) == 256
+    assert size(4, max_pages=257) == 4 * 8 * 2 * 16384 and size(1, heads=1, max_pages=1 << 24) == (1 << 16) * 16384
+    assert size(0) == size(65536) == size(65535, heads=65) == size(4, max_pages=1 << 25) == 0
+    assert lib.spec_kv_evict_workspace_size(None, 1) == 0
+    far = {n: (i + 1) << 48 for i, n in enumerate(("lengths", "w", "new", "table", "out_len", "out", "kept"))}
+    assert evict(lib, kv(max_pages=257), C=1 << 15, wsb=4 * 8 * 2 * 16384 - 1, **far) == -5
+    assert evict(lib, kv(heads=65), B=65535, **far) == -2
 
 
 def test_binding_refuses_host_tensors():

@@ -293,6 +293,41 @@ def test_evict_long_and_shared_pages(gpu_lib):
     np.testing.assert_array_equal(c["k_pages"][table[0, :50]], before)
 
 
+@pytest.mark.parametrize("kind", ["any", "equal", "mostly zero", "two", "nan"])
+@pytest.mark.parametrize("budget,recent", [(1500, 100), (33, 33), (16400, 0)])
+def test_evict_rows_of_several_workgroups(gpu_lib, kind, budget, recent):
+    """Rows of more than 16384 positions, which several workgroups share, and
+    short ones beside them; with more equal leading digits than are listed."""
+    rng = np.random.default_rng(len(kind) + budget)
+    lens = [40001, 16384, 16385, 100, 32768]
+    c, table, new, weights = _evict_state(rng, "e4m3", 128, 1, 64, lens, budget)
+    pick = rng.random(weights.shape)
+    if kind == "equal":
+        weights[:] = 0.3
+    elif kind == "mostly zero":
+        weights = np.where(pick < 0.01, weights, 0.0).astype(np.float32)
+    elif kind == "two":
+        weights = np.where(pick < 0.7, 1.0, 1.0 + 2.0 ** -23).astype(np.float32)
+    elif kind == "nan":
+        weights[pick < 0.999] = np.nan
+    _evict_check(gpu_lib, c, table, lens, weights, new, budget, recent, budget)
+
+
+def test_evict_workspace_is_taken(gpu_lib):
+    """A given workspace of any contents serves as a new one does; one that is too small is replaced."""
+    import torch
+    rng = np.random.default_rng(11)
+    lens, budget = [20000, 300], 100
+    c, table, new, weights = _evict_state(rng, "int8", 64, 2, 64, lens, budget)
+    args = (_i32(table), _i32(lens), _f32(weights), _i32(new), budget, 5)
+    size = gpu_lib.kv_evict_workspace_size(kh.to_device(gpu_lib, c), 2, table.shape[1])
+    assert size > 256
+    first = gpu_lib.kv_evict(kh.to_device(gpu_lib, c), *args, return_kept=True)
+    for ws in (torch.full((size,), 0xff, dtype=torch.uint8, device="cuda"), torch.zeros(16, dtype=torch.uint8, device="cuda")):
+        again = gpu_lib.kv_evict(kh.to_device(gpu_lib, c), *args, return_kept=True, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 # ----------------------------------------------------------- together --
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "f32")])
 def test_prompt_rounds_and_eviction_together(gpu_lib, fmt, dtype):
