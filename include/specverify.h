@@ -513,8 +513,9 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
  * memory holds.
  *   q           [T] token rows of Hq*dim elements (dtype)
  *   k, v        [T] token rows of heads*dim elements
- *   q_stride, kv_stride  elements between token rows, multiples of 16 bytes;
- *               0: contiguous (rows of a fused projection: their full length)
+ *   q_stride, kv_stride  elements between token rows, multiples of 16 bytes,
+ *               below 2^24; 0: contiguous (rows of a fused projection: their
+ *               full length)
  *   starts      [B + 1] int32 (device); sequences may be empty
  *   scale       any sign; finite, also when multiplied by 1.5
  *   out         [T][Hq][dim] (dtype);  out_lse [T][Hq] float or NULL

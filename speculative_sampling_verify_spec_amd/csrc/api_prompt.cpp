@@ -24,6 +24,7 @@ int check_packed(const void* q, int64_t q_stride, const void* k, const void* v, 
   if (!std::isfinite(scale * 1.5f)) return SPECV_E_SHAPE;  // times log2(e), as the kernels use it
   if (const int rc = check_row(&q_stride, Hq, dim, dtype)) return rc;
   if (const int rc = check_row(&kv_stride, heads, dim, dtype)) return rc;
+  if (q_stride >= (1 << 24) || kv_stride >= (1 << 24)) return SPECV_E_SHAPE;  // a tile's rows are reached in 32 bits
   if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return SPECV_E_ALIGN;
   s->q = q;
   s->k = k;

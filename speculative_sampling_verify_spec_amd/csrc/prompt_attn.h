@@ -27,6 +27,7 @@
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "sv_device.h"
 #include "sv_kv.h"
@@ -118,15 +119,27 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
     const int t = e / NC;
     return kbase + static_cast<long>(min(tile * BN + t, len - 1)) * s.kv_row + 8 * swizzle<D>(t, e % NC);
   };
-  // bf16: memory to LDS, whose rows hold the pieces in the swizzled order
+  // bf16: memory to LDS, whose rows hold the pieces in the swizzled order.  A
+  // lane's places in a tile are below 2^32 bytes: rows are below 2^24 elements.
+  uint32_t place_at[kLoads];
+  const uint32_t row_bytes = 2 * static_cast<uint32_t>(s.kv_row);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int e = tid + i * kPBlock, t = e / NC;
+    place_at[i] = t * row_bytes + 16 * swizzle<D>(t, e % NC);
+  }
   auto request = [&](int tile, int buf) {
     if constexpr (DT == SPECV_BF16) {
+      const long first = kbase + static_cast<long>(tile) * BN * s.kv_row;
+      const uint16_t *k = static_cast<const uint16_t*>(s.k) + first, *v = static_cast<const uint16_t*>(s.v) + first;
+      const int rest = len - tile * BN;  // tokens from the tile's first on; its further rows are the last one's again
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const long a = offset(tile, tid + i * kPBlock);
+        uint32_t at = place_at[i];
+        if (rest < BN) at -= static_cast<uint32_t>(max((tid + i * kPBlock) / NC - (rest - 1), 0)) * row_bytes;
         const int to = 8 * (i * kPBlock + w * kWave);
-        load_lds(static_cast<const uint16_t*>(s.k) + a, &lk[buf][to]);
-        load_lds(static_cast<const uint16_t*>(s.v) + a, &lv[buf][to]);
+        load_lds(k, at, &lk[buf][to]);
+        load_lds(v, at, &lv[buf][to]);
       }
     }
   };
@@ -175,23 +188,22 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   request(0, 0);
   if constexpr (DT == SPECV_BF16) landed_barrier();
 
-  for (int tile = 0; tile < ntile; ++tile) {
+  // a tile's part in the rows; mixed: some rows of the workgroup do not see all of it
+  auto step = [&](int tile, auto mixed) {
     const int buf = Shape::buffers == 2 ? tile & 1 : 0;
-    const bool more = tile + 1 < ntile;
     if constexpr (DT == SPECV_F32) {
       fill(tile);
       __syncthreads();
-    } else if (more) {
+    } else if (tile + 1 < ntile) {
       request(tile + 1, buf ^ 1);
     }
-    if (tile * BN + BN - 1 > first_tok) {  // some rows do not see all of it
+    if constexpr (decltype(mixed)::value) {
       tame(buf);
       lds_barrier();
     }
-    // waves whose rows see nothing of the tile wait for the others
     const int t0 = tile * BN;
-    const bool any = t0 * s.G < wrow + 32 && wrow < rows;
-    if (any) {
+    // waves whose rows see nothing of the tile wait for the others
+    if (!decltype(mixed)::value || (t0 * s.G < wrow + 32 && wrow < rows)) {
       // the lane's places in LDS are computed in every tile where registers are short
       int own = lane;
       if constexpr (kWhole) asm volatile("" : "+v"(own));
@@ -222,12 +234,13 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
             for (int i = 0; i <= z; ++i) sc[n] = mfma32(a[z - i], q[f * kStep][i], sc[n]);
         }
       }
-      if (t0 + BN - 1 > wrow / s.G) {  // some of the wave's rows do not see all of the tile
+      if constexpr (decltype(mixed)::value) {
+        const int sees = tok - t0 - 4 * half;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (t0 + 32 * n + 8 * (i / 4) + 4 * half + i % 4 > tok) sc[n][i] = -INFINITY;
+            if (32 * n + 8 * (i / 4) + i % 4 > sees) sc[n][i] = -INFINITY;
       }
       float x = sc[0][0];
 #pragma unroll
@@ -251,13 +264,11 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float e = ex2(fmaf(sc[n][i], kscale, -m));
-          sum += e;
-          __bf16 piece[3];
-          split<NP>(e, piece);
-#pragma unroll
-          for (int j = 0; j < NP; ++j) pf[2 * n + i / 8][j][i % 8] = piece[j];
+        for (int i = 0; i < 16; i += 2) {
+          const f32x2 e = {ex2(fmaf(sc[n][i], kscale, -m)), ex2(fmaf(sc[n][i + 1], kscale, -m))};
+          sum += e[0];
+          sum += e[1];
+          split2<NP>(e, &pf[2 * n + i / 8][0], i % 8);
         }
       l += sum;
       // ---- values: slots 0..3 of half h hold tokens 16 c + 4 h .., 4..7 those 8 further ----
@@ -266,52 +277,50 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
           bf16x8 a[NP];
-          const int t = 16 * c + 4 * (own / 32) + (own % 16) / 4, piece = 4 * d + 2 * ((own / 16) % 2) + (own % 4) / 2;
+          const int t = 4 * (own / 32) + (own % 16) / 4, piece = 4 * d + 2 * ((own / 16) % 2) + (own % 4) / 2;
 #pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const __bf16* lo = &lv[buf][j * kPlane + t * D + 8 * swizzle<D>(t, piece) + 4 * (own % 2)];
-            const __bf16* hi = &lv[buf][j * kPlane + (t + 8) * D + 8 * swizzle<D>(t + 8, piece) + 4 * (own % 2)];
-            const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lo));
-            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(hi));
-            a[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
-          }
+          for (int j = 0; j < NP; ++j)
+            a[j] = read_transposed(&lv[buf][j * kPlane + (16 * c + t) * D + 8 * swizzle<D>(16 * c + t, piece) + 4 * (own % 2)],
+                                   &lv[buf][j * kPlane + (16 * c + t + 8) * D + 8 * swizzle<D>(16 * c + t + 8, piece) + 4 * (own % 2)]);
 #pragma unroll
           for (int z = NP - 1; z >= 0; --z)
 #pragma unroll
             for (int i = 0; i <= z; ++i) o[d] = mfma32(a[z - i], pf[c][i], o[d]);
         }
-      if (wild) {
-        // values that are not finite must not meet a weight of 0: they were
-        // left out, and are added where they are seen
+      if constexpr (decltype(mixed)::value)
+        if (wild) {
+          // values that are not finite must not meet a weight of 0: they were
+          // left out, and are added where they are seen
 #pragma unroll 1
-        for (int j = 0; j < BN && t0 + j < len; ++j) {
-          float e = 0.f;
+          for (int j = 0; j < BN && t0 + j < len; ++j) {
+            float e = 0.f;
 #pragma unroll
-          for (int c = 0; c < 2 * NB; ++c)
+            for (int c = 0; c < 2 * NB; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (16 * c + 8 * (i / 4) + 4 * half + i % 4 == j) e = static_cast<float>(pf[c][0][i]);
-          e = halves_sum(e);
-          const long a = kbase + static_cast<long>(t0 + j) * s.kv_row + 4 * half;
+              for (int i = 0; i < 8; ++i)
+                if (16 * c + 8 * (i / 4) + 4 * half + i % 4 == j) e = static_cast<float>(pf[c][0][i]);
+            e = halves_sum(e);
+            const long a = kbase + static_cast<long>(t0 + j) * s.kv_row + 4 * half;
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              // few loads at a time: this rare part's registers count for the whole kernel
-              if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-              const long k = a + 32 * d + 8 * (i / 4) + i % 4;
-              float y;
-              if constexpr (DT == SPECV_F32) y = static_cast<const float*>(s.v)[k];
-              else y = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(s.v)[k]) << 16);
-              if (!isfinite(y) && t0 + j <= tok) o[d][i] += e * y;
-            }
+              for (int i = 0; i < 16; ++i) {
+                // few loads at a time: this rare part's registers count for the whole kernel
+                if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+                const long k = a + 32 * d + 8 * (i / 4) + i % 4;
+                float y;
+                if constexpr (DT == SPECV_F32) y = static_cast<const float*>(s.v)[k];
+                else y = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(s.v)[k]) << 16);
+                if (!isfinite(y) && t0 + j <= tok) o[d][i] += e * y;
+              }
+          }
         }
-      }
     }
     landed_barrier();
-  }
+  };
+  const int whole = min((first_tok + 1) / BN, ntile);  // tiles that every row sees all of
+  for (int tile = 0; tile < whole; ++tile) step(tile, std::false_type{});
+  for (int tile = whole; tile < ntile; ++tile) step(tile, std::true_type{});
 
   l = halves_sum(l);
   const bool there = wrow + col < rows, some = !(l == 0.f);

@@ -93,9 +93,16 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   };
   auto request = [&](int tile, int buf) {
     if constexpr (DT == SPECV_BF16) {
+      // from the tile's first token on, a lane's places are below 2^32 bytes: rows are below 2^24 elements
+      const int r0 = min(row_first + tile * BM, rows - 1), tok0 = __builtin_amdgcn_readfirstlane(token_of(r0));
+      const uint16_t* const from = static_cast<const uint16_t*>(s.q) + qbase + static_cast<long>(tok0) * s.q_row;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        load_lds(static_cast<const uint16_t*>(s.q) + offset(tile, tid + i * kWBlock), &lq[buf][8 * (i * kWBlock + w * kWave)]);
+      for (int i = 0; i < kLoads; ++i) {
+        const int e = tid + i * kWBlock, t = e / NC, r = min(row_first + tile * BM + t, rows - 1), tok = token_of(r);
+        const uint32_t at = 2 * (static_cast<uint32_t>(tok - tok0) * static_cast<uint32_t>(s.q_row) +
+                                 static_cast<uint32_t>(r - tok * s.G) * D + 8 * swizzle<D>(t, e % NC));
+        load_lds(from, at, &lq[buf][8 * (i * kWBlock + w * kWave)]);
+      }
     }
   };
   auto fill = [&](int tile) {

@@ -13,6 +13,7 @@ namespace frag {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -37,6 +38,24 @@ __device__ inline void split(float x, __bf16* piece) {
     const float r = isfinite(x) ? x - lead(x) : 0.f;
     piece[1] = bits(r);
     piece[2] = bits(r - lead(r));
+  }
+}
+
+// Two values' pieces into elements at, at + 1 of NP fragments.
+template <int NP>
+__device__ inline void split2(f32x2 x, bf16x8* f, int at) {
+  if constexpr (NP == 1) {
+    const bf16x2 y = __builtin_convertvector(x, bf16x2);
+    f[0][at] = y[0];
+    f[0][at + 1] = y[1];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      __bf16 s[3];
+      split<3>(x[k], s);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) f[j][at + k] = s[j];
+    }
   }
 }
 
@@ -191,16 +210,28 @@ __device__ inline float halves_sum(float v) {
 // read), fall into different banks.
 template <int D>
 __device__ inline int swizzle(int t, int c) {
-  if constexpr (D == 96) return c ^ ((t >> 2) & 3);
-  else if constexpr (D == 64) return c ^ (2 * ((t >> 1) & 3));
-  else return c ^ (2 * (t & 7));
+  if constexpr (D == 96) return c ^ ((t >> 2) & 3);                                      // rows are 12 pieces: 4 banks' groups
+  else if constexpr (D == 64) return c ^ (4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1));      // two rows a round of banks
+  else return c ^ (4 * (t & 3) + 2 * ((t >> 2) & 1));
 }
 
-// 16 bytes a lane from memory straight to LDS: the wave's 1024 bytes from `to` on.
-__device__ inline void load_lds(const void* from, const void* to) {
+// Eight k of one column for an A operand, from rows of LDS: the 16 lanes of a
+// group give the addresses of 4 rows x 16 columns (lane j row j / 4, columns 4
+// (j % 4) .. + 3) twice, and lane j gets column j of both.
+__device__ inline bf16x8 read_transposed(const __bf16* lo, const __bf16* hi) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+  const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lo));
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(hi));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 16 bytes a lane from memory (the wave's `base`, `offset` bytes further)
+// straight to LDS: the wave's 1024 bytes from `to` on.
+__device__ inline void load_lds(const void* base, uint32_t offset, const void* to) {
   typedef __attribute__((address_space(3))) const void* lds_ptr;
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)to)));
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory");
 }
 
 // A barrier that orders LDS only: __syncthreads would also wait for every

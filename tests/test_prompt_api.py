@@ -28,7 +28,7 @@ PACKED = [
     (dict(D=0), -2), (dict(H=0), -2), (dict(H=1 << 15, Hq=1 << 15), -2), (dict(Hq=0), -2), (dict(Hq=12), -2),
     (dict(Hq=1 << 15), -2), (dict(Hq=8 * 1025), -2), (dict(scale=float("nan")), -2), (dict(scale=float("inf")), -2),
     (dict(scale=-3.2e38), -2), (dict(qs=100), -2), (dict(qs=-1), -2), (dict(qs=32 * 128 + 4), -6),
-    (dict(ks=8 * 128 - 8), -2), (dict(ks=8 * 128 + 1), -6), (dict(q=BASE + 2), -6), (dict(k=BASE + 8), -6),
+    (dict(ks=8 * 128 - 8), -2), (dict(qs=1 << 24), -2), (dict(ks=1 << 24), -2),  (dict(ks=8 * 128 + 1), -6), (dict(q=BASE + 2), -6), (dict(k=BASE + 8), -6),
     # rows of a sequence and workgroups of a grid are counted in 32 bits
     (dict(T=1 << 24, H=1, Hq=64), -2), (dict(T=1 << 24, H=128, Hq=128), -2), (dict(B=65535, T=1, H=256, Hq=256), -2)]
 
