@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   const Packed& s = p.s;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(s.H));
   const unsigned place = blockIdx.x / static_cast<unsigned>(s.H);
-  const PromptBlock at = prompt_block<kPBlock>(s, place, s.G, kPromptRows);
+  const PromptBlock at = prompt_block<kPBlock, false>(s, place, s.G, kPromptRows);
   const int tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane % 32, half = lane / 32;
   if (at.block < 0) {
@@ -143,26 +143,41 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
       }
     }
   };
-  // fp32: through registers, where an element becomes its pieces
+  // fp32: through registers, where an element becomes its pieces; a tile is
+  // loaded a tile ahead where there are registers for it
+  constexpr bool kAhead = DT == SPECV_F32 && D <= 128;
+  Raw8<DT> xk[kAhead ? kLoads : 1], xv[kAhead ? kLoads : 1];
+  auto load = [&](int tile) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const long a = offset(tile, min(tid + i * kPBlock, kAll - 1));
+        xk[i].load(s.k, a);
+        xv[i].load(s.v, a);
+      }
+    }
+  };
+  auto put = [&](__bf16* to, int e, const Raw8<DT>& x) {
+    bf16x8 f[NP];
+    x.pieces(f);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&to[j * kPlane + 8 * e]) = f[j];
+  };
   auto fill = [&](int tile) {
     if constexpr (DT == SPECV_F32) {
       int thread = tid;
       if constexpr (kWhole) asm volatile("" : "+v"(thread));
-#pragma unroll D == 256 ? 1 : kLoads
+#pragma unroll kAhead ? kLoads : 1
       for (int i = 0; i < kLoads; ++i) {
         const int e = thread + i * kPBlock;
         if (kAll % kPBlock && e >= kAll) break;
-        const long a = offset(tile, e);
-        Raw8<DT> x, y;
-        x.load(s.k, a);
-        y.load(s.v, a);
-        bf16x8 f[NP];
-        x.pieces(f);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&lk[0][j * kPlane + 8 * e]) = f[j];
-        y.pieces(f);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) *reinterpret_cast<bf16x8*>(&lv[0][j * kPlane + 8 * e]) = f[j];
+        if constexpr (!kAhead) {
+          const long a = offset(tile, e);
+          xk[0].load(s.k, a);
+          xv[0].load(s.v, a);
+        }
+        put(lk[0], e, xk[kAhead ? i : 0]);
+        put(lv[0], e, xv[kAhead ? i : 0]);
       }
     }
   };
@@ -186,6 +201,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   };
   if (tid == 0) wild = 0;
   request(0, 0);
+  load(0);
   if constexpr (DT == SPECV_BF16) landed_barrier();
 
   // a tile's part in the rows; mixed: some rows of the workgroup do not see all of it
@@ -193,7 +209,8 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
     const int buf = Shape::buffers == 2 ? tile & 1 : 0;
     if constexpr (DT == SPECV_F32) {
       fill(tile);
-      __syncthreads();
+      if (tile + 1 < ntile) load(tile + 1);
+      lds_barrier();
     } else if (tile + 1 < ntile) {
       request(tile + 1, buf ^ 1);
     }
@@ -316,7 +333,8 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
           }
         }
     }
-    landed_barrier();
+    if constexpr (DT == SPECV_F32) lds_barrier();
+    else landed_barrier();
   };
   const int whole = min((first_tok + 1) / BN, ntile);  // tiles that every row sees all of
   for (int tile = 0; tile < whole; ++tile) step(tile, std::false_type{});

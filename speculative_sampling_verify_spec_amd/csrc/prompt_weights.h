@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   const Packed& s = p.s;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(s.H));
   const unsigned place = blockIdx.x / static_cast<unsigned>(s.H);
-  const PromptBlock at = prompt_block<kWBlock>(s, place, 1, kWeightKeys);
+  const PromptBlock at = prompt_block<kWBlock, true>(s, place, 1, kWeightKeys);
   const int tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane % 32, half = lane / 32;
   if (at.block < 0) {
@@ -61,8 +61,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
     return;
   }
   const int len = at.last - at.first, rows = len * s.G;
-  // the first keys, which all rows see, first
-  const int nblock = (len + kWeightKeys - 1) / kWeightKeys, block = nblock - 1 - at.block;
+  const int nblock = (len + kWeightKeys - 1) / kWeightKeys, block = at.block;
   const int key0 = block * kWeightKeys, wkey = key0 + 32 * w, key = wkey + col;
   float* const wrow = p.w + (static_cast<long>(at.seq) * s.H + h) * p.capacity;
   if (block == nblock - 1)  // behind the prompt
@@ -85,23 +84,37 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   auto token_of = [&](int r) {
     return s.G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.magic) >> p.shift);
   };
-  const int row_first = key0 * s.G, ntile = (rows - row_first + BM - 1) / BM;
+  // A tile has `step` rows, a multiple of G where G is small, so that a lane's
+  // rows are the same heads in every tile and their places the same from the
+  // tile's first token on; further rows of the tile weigh nothing.
+  const bool even = s.G <= 32;
+  const int step = even ? BM / s.G * s.G : BM;
+  const int row_first = key0 * s.G, ntile = (rows - row_first + step - 1) / step;
   const long qbase = static_cast<long>(at.first) * s.q_row + static_cast<long>(h) * s.G * D;
   auto offset = [&](int tile, int e) {
-    const int t = e / NC, r = min(row_first + tile * BM + t, rows - 1), tok = token_of(r);
+    const int t = e / NC, r = min(row_first + tile * step + t, rows - 1), tok = token_of(r);
     return qbase + static_cast<long>(tok) * s.q_row + static_cast<long>(r - tok * s.G) * D + 8 * swizzle<D>(t, e % NC);
   };
+  // bf16: a lane's places from the tile's first token on, in bytes: below 2^32, as rows are below 2^24 elements
+  auto place_in = [&](int e, int r0, int most) {
+    const int t = e / NC, tok0 = token_of(r0), r = min(r0 + t, most), tok = token_of(r);
+    return 2 * (static_cast<uint32_t>(tok - tok0) * static_cast<uint32_t>(s.q_row) + static_cast<uint32_t>(r - tok * s.G) * D +
+                8 * swizzle<D>(t, e % NC));
+  };
+  uint32_t place_at[DT == SPECV_BF16 ? kLoads : 1];
+  if constexpr (DT == SPECV_BF16) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) place_at[i] = place_in(tid + i * kWBlock, row_first, row_first + step - 1);
+  }
   auto request = [&](int tile, int buf) {
     if constexpr (DT == SPECV_BF16) {
-      // from the tile's first token on, a lane's places are below 2^32 bytes: rows are below 2^24 elements
-      const int r0 = min(row_first + tile * BM, rows - 1), tok0 = __builtin_amdgcn_readfirstlane(token_of(r0));
-      const uint16_t* const from = static_cast<const uint16_t*>(s.q) + qbase + static_cast<long>(tok0) * s.q_row;
+      const int r0 = row_first + tile * step;
+      const uint16_t* const from = static_cast<const uint16_t*>(s.q) + qbase + static_cast<long>(__builtin_amdgcn_readfirstlane(token_of(r0))) * s.q_row;
+      const bool whole = even && r0 + step <= rows;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int e = tid + i * kWBlock, t = e / NC, r = min(row_first + tile * BM + t, rows - 1), tok = token_of(r);
-        const uint32_t at = 2 * (static_cast<uint32_t>(tok - tok0) * static_cast<uint32_t>(s.q_row) +
-                                 static_cast<uint32_t>(r - tok * s.G) * D + 8 * swizzle<D>(t, e % NC));
-        load_lds(from, at, &lq[buf][8 * (i * kWBlock + w * kWave)]);
+        const uint32_t a = whole ? place_at[i] : place_in(tid + i * kWBlock, r0, rows - 1);
+        load_lds(from, a, &lq[buf][8 * (i * kWBlock + w * kWave)]);
       }
     }
   };
@@ -120,67 +133,81 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
       }
     }
   };
-  // the statistics of a tile's rows, by its first threads
+  // the statistics of a tile's rows, by its first threads: loaded, and later put into LDS
   auto stat = [&](int tile) {
     float x = INFINITY;
-    const int r = row_first + tile * BM + tid;
-    if (tid < BM && r < rows) {
+    const int r = row_first + tile * step + tid;
+    if (tid < step && r < rows) {
       const int tok = token_of(r);
       x = p.lse[(static_cast<long>(at.first) + tok) * s.Hq + h * s.G + (r - tok * s.G)];
-      x = x == -INFINITY ? INFINITY : x * kLog2e;
     }
     return x;
   };
+  auto put_stat = [&](int buf, float x) {
+    asm volatile("" : "+v"(x));  // not looked at before: the wait for it would be one for the tile requested after it
+    if (tid < BM) ll[buf][tid] = x == -INFINITY ? INFINITY : x * kLog2e;
+  };
 
-  request(0, 0);
-  float next = stat(0);
+  // From the last tile on: all workgroups of a head begin with the same rows
+  // and go on together, so that they find them in the cache (2 x 8191: XXX us,
+  // from each one's own first rows on 716 us).
+  request(ntile - 1, 0);
+  float next = stat(ntile - 1);
   float sum = 0.f, lost = 0.f;  // the tiles' sums are added with what each addition rounds away
   if constexpr (DT == SPECV_BF16) {
-    if (tid < BM) ll[0][tid] = next;
+    put_stat(0, next);
     landed_barrier();
   }
-  for (int tile = 0; tile < ntile; ++tile) {
-    const int buf = Shape::buffers == 2 ? tile & 1 : 0;
-    const bool more = tile + 1 < ntile;
+  for (int tile = ntile - 1; tile >= 0; --tile) {
+    const int buf = Shape::buffers == 2 ? (ntile - 1 - tile) & 1 : 0;
+    const bool more = tile > 0;
     if constexpr (DT == SPECV_F32) {
       fill(tile);
-      if (tid < BM) ll[0][tid] = next;
-      if (more) next = stat(tile + 1);
+      put_stat(0, next);
+      if (more) next = stat(tile - 1);
       __syncthreads();
     } else if (more) {
-      request(tile + 1, buf ^ 1);
-      next = stat(tile + 1);
+      next = stat(tile - 1);
+      request(tile - 1, buf ^ 1);
     }
-    const int r0 = row_first + tile * BM;
+    const int r0 = row_first + tile * step;
     if (wkey < len && r0 + BM > wkey * s.G) {  // a row sees a key of the wave
       float part = 0.f;
+      // The products of a block of 32 rows are under way while the exponentials
+      // of the block before are taken: the matrix unit and the vector unit work
+      // at the same time, and a product's result is not waited for.
+      auto scores = [&](int n, f32x16& sc) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          bf16x8 a[NP];
+          const int t = 32 * n + col;
+#pragma unroll
+          for (int j = 0; j < NP; ++j)
+            a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
+#pragma unroll
+          for (int z = NP - 1; z >= 0; --z)
+#pragma unroll
+            for (int i = 0; i <= z; ++i) sc = mfma32(a[z - i], k[f][i], sc);
+        }
+      };
       // mixed: some rows do not see some of the wave's keys
       auto blocks = [&](auto mixed) {
+        f32x16 sc[2];
+        scores(0, sc[0]);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          f32x16 sc;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sc[i] = 0.f;
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            bf16x8 a[NP];
-            const int t = 32 * n + col;
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-              a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
-#pragma unroll
-            for (int z = NP - 1; z >= 0; --z)
-#pragma unroll
-              for (int i = 0; i <= z; ++i) sc = mfma32(a[z - i], k[f][i], sc);
-          }
-          const int first = key * s.G - (r0 + 32 * n + 4 * half);  // rows from here on see the lane's key
+          if (n + 1 < NB) scores(n + 1, sc[(n + 1) & 1]);
+          // rows from `first` on see the lane's key; from `past` on they are others' copies
+          const int first = key * s.G - (r0 + 32 * n + 4 * half), past = step - (32 * n + 4 * half);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float e = ex2(fmaf(sc[4 * j + i], kscale, -l4[i]));
-              part += decltype(mixed)::value && 8 * j + i < first ? 0.f : e;  // whatever an unseen score is
+              const float e = ex2(fmaf(sc[n & 1][4 * j + i], kscale, -l4[i]));
+              part += decltype(mixed)::value && (8 * j + i < first || 8 * j + i >= past) ? 0.f : e;  // whatever an unseen score is
             }
           }
         }
@@ -192,7 +219,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
       sum = z;
     }
     if constexpr (DT == SPECV_BF16) {
-      if (more && tid < BM) ll[buf ^ 1][tid] = next;
+      if (more) put_stat(buf ^ 1, next);
     }
     landed_barrier();
   }

@@ -206,13 +206,13 @@ __device__ inline float halves_sum(float v) {
 }
 
 // Where the 16-byte piece c of row t stands in a row of D elements in LDS, so
-// that eight rows' same piece, and four rows' same pair of pieces (a transposing
+// that sixteen rows' same piece, and four rows' same four pieces (a transposing
 // read), fall into different banks.
 template <int D>
 __device__ inline int swizzle(int t, int c) {
-  if constexpr (D == 96) return c ^ ((t >> 2) & 3);                                      // rows are 12 pieces: 4 banks' groups
-  else if constexpr (D == 64) return c ^ (4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1));      // two rows a round of banks
-  else return c ^ (4 * (t & 3) + 2 * ((t >> 2) & 1));
+  if constexpr (D == 96) return c ^ ((t >> 2) & 3);  // rows begin in four different places of the banks
+  else if constexpr (D == 64) return c ^ (4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1));  // two rows a round of banks
+  else return c ^ (4 * (t & 3) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1));
 }
 
 // Eight k of one column for an A operand, from rows of LDS: the 16 lanes of a
@@ -242,9 +242,13 @@ __device__ inline void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// A barrier after which what load_lds requested before it is in LDS.
+// A barrier after which what load_lds requested before it is in LDS.  The wait
+// is one that the compiler knows of (vmcnt 0, lgkmcnt 0): it would else wait
+// for its own loads from before again, and so for the next tile's requests,
+// wherever their results are used.
 __device__ inline void landed_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }

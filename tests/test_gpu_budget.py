@@ -72,6 +72,23 @@ def test_prompt_weights(gpu_lib, dtype, D, H, G, lens, capacity):
         np.testing.assert_allclose(got.sum(2).cpu().numpy(), np.outer(lens, [G] * H), rtol=2e-3)  # times at most 20 here
 
 
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 3), ("bf16", 64, 7), ("f32", 64, 5), ("bf16", 96, 33), ("bf16", 256, 12)])
+def test_prompt_weights_of_groups_of_any_size(gpu_lib, dtype, D, G):
+    """Groups that do not divide a tile's rows; queries before a key hold NaN,
+    and the weights of the keys behind them are as they were."""
+    rng = np.random.default_rng(G)
+    n, H = 190, 1
+    (q, k, v), host = ph.inputs(rng, n, H * G, H, D, dtype)
+    _, lse = gpu_lib.prompt_attention(q, k, v, _i32([0, n]), return_lse=True)
+    want = ob.prompt_weights(*host[:2], lse.double().cpu().numpy(), [0, n], D ** -0.5, n)
+    _weights_close(gpu_lib.prompt_weights(q, k, lse, _i32([0, n]), n), want, D)
+    for bad in (0, 41, 127, 150):
+        x = q.clone()
+        x[bad] = float("nan")
+        rows = np.broadcast_to(np.arange(n) > bad, want.shape[1:])
+        _weights_close(gpu_lib.prompt_weights(x, k, lse, _i32([0, n]), n), want, D, rows)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
 def test_prompt_weights_of_statistics_that_are_not_finite(gpu_lib, dtype, D):
     """lse of -infinity and +infinity weighs nothing; what other sequences and

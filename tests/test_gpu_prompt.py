@@ -141,6 +141,26 @@ def test_many_sequences(gpu_lib):
     _check(got, op.attention(*host, starts, 0.125), 64, "bf16")
 
 
+def test_blocks_of_few_sequences_in_any_order(gpu_lib):
+    """Up to 64 sequences, whose blocks are handed out longest first: each block
+    once, whatever the lengths."""
+    rng = np.random.default_rng(15)
+    for lens in ([0] * 63 + [90], [33] * 64, [0, 300, 0, 31, 32, 299, 1], list(rng.integers(0, 200, 64))):
+        starts = 1 + np.concatenate([[0], np.cumsum(lens)])
+        T = int(starts[-1]) + 40
+        (q, k, v), _ = ph.inputs(rng, T, 4, 1, 64, "bf16")
+        out, lse = gpu_lib.prompt_attention(q, k, v, _i32(starts), return_lse=True)
+        more = _i32(np.concatenate([starts, [starts[-1]] * 70]))  # more than 64: the other way
+        same = gpu_lib.prompt_attention(q, k, v, more, return_lse=True)
+        import torch
+        assert torch.equal(out, same[0]) and torch.equal(lse, same[1])
+        assert (out[:1] == 0).all() and (out[starts[-1]:] == 0).all() and torch.isfinite(lse[1:starts[-1]]).all()
+        for b in (0, len(lens) // 2, len(lens) - 1):
+            first, last = int(starts[b]), int(starts[b + 1])
+            if first < last:
+                _check((out[first:last], lse[first:last]), _exact(q[first:last], k[first:last], v[first:last], 0.125), 64, "bf16")
+
+
 def _exact(q, k, v, scale):
     """One sequence in 64 bits on the device: what op.attention gives."""
     import torch
