@@ -38,6 +38,12 @@ int check_packed(const void* q, int64_t q_stride, const void* k, const void* v, 
   s->H = heads;
   s->Hq = Hq;
   s->G = Hq / heads;
+  // r / G for r < 2^31 is mulhi(r, m) >> (l - 1) with 2^l >= G and m = floor(2^(31 + l) / G) + 1 < 2^32:
+  // r m / 2^(31 + l) exceeds r / G by r (m G - 2^(31 + l)) / (G 2^(31 + l)) < 2^31 G / (G 2^31 2^l) <= 1 / G
+  int l = 1;
+  while ((1 << l) < s->G) ++l;
+  s->magic = s->G > 1 ? static_cast<uint32_t>((uint64_t(1) << (31 + l)) / s->G + 1) : 0;
+  s->shift = l - 1;
   return SPECV_OK;
 }
 
@@ -80,12 +86,6 @@ int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t 
   p.w = out_weights;
   p.capacity = static_cast<int>(capacity);
   p.slots = static_cast<unsigned>(prompt_slots(T, 1, B, kWeightKeys));
-  // r / G for r < 2^31 is mulhi(r, m) >> (l - 1) with 2^l >= G and m = floor(2^(31 + l) / G) + 1 < 2^32:
-  // r m / 2^(31 + l) exceeds r / G by r (m G - 2^(31 + l)) / (G 2^(31 + l)) < 2^31 G / (G 2^31 2^l) <= 1 / G
-  int l = 1;
-  while ((1 << l) < p.s.G) ++l;
-  p.magic = p.s.G > 1 ? static_cast<uint32_t>((uint64_t(1) << (31 + l)) / p.s.G + 1) : 0;
-  p.shift = l - 1;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const hipError_t e = dim == 64    ? launch_prompt_weights_64(p, dtype, st)
                        : dim == 96  ? launch_prompt_weights_96(p, dtype, st)

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   const int len = at.last - at.first, rows = len * s.G;
   const int row0 = at.block * kPromptRows, wrow = row0 + 32 * w;
   const int r = min(wrow + col, rows - 1);  // a row that exists
-  const int tok = r / s.G, hq = h * s.G + (r - tok * s.G);
+  const int tok = s.token_of(r), hq = h * s.G + (r - tok * s.G);
 
   __shared__ __align__(16) __bf16 lk[Shape::buffers][NP * kPlane], lv[Shape::buffers][NP * kPlane];
   __shared__ int wild;  // a value that is not finite was cleared
@@ -92,17 +92,6 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   constexpr bool kWhole = DT == SPECV_F32 && D == 256;
   bf16x8 q[kWhole ? 1 : NF][NP];
   Raw8<DT> xq[NF];
-  {
-    const long base = (static_cast<long>(at.first) + tok) * s.q_row + static_cast<long>(hq) * D + 8 * half;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) xq[f].load(s.q, base + 16 * f);
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      xq[f].negate(s.scale < 0.f);
-      if constexpr (!kWhole) xq[f].pieces(q[f]);
-    }
-  }
-
   f32x16 o[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d)
@@ -111,7 +100,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   float m = -FLT_MAX, l = 0.f;
 
   // tokens seen by the workgroup's last and first row
-  const int last_tok = min(row0 + kPromptRows - 1, rows - 1) / s.G, first_tok = row0 / s.G;
+  const int last_tok = s.token_of(min(row0 + kPromptRows - 1, rows - 1)), first_tok = s.token_of(row0);
   const int ntile = last_tok / BN + 1;
   const long kbase = static_cast<long>(at.first) * s.kv_row + static_cast<long>(h) * D;
 
@@ -121,6 +110,7 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   };
   // bf16: memory to LDS, whose rows hold the pieces in the swizzled order.  A
   // lane's places in a tile are below 2^32 bytes: rows are below 2^24 elements.
+  const uint32_t lk_at = lds_address(&lk[0][0]), lv_at = lds_address(&lv[0][0]);
   uint32_t place_at[kLoads];
   const uint32_t row_bytes = 2 * static_cast<uint32_t>(s.kv_row);
 #pragma unroll
@@ -137,9 +127,9 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
       for (int i = 0; i < kLoads; ++i) {
         uint32_t at = place_at[i];
         if (rest < BN) at -= static_cast<uint32_t>(max((tid + i * kPBlock) / NC - (rest - 1), 0)) * row_bytes;
-        const int to = 8 * (i * kPBlock + w * kWave);
-        load_lds(k, at, &lk[buf][to]);
-        load_lds(v, at, &lv[buf][to]);
+        const uint32_t to = 2 * (buf * NP * kPlane) + 16 * (i * kPBlock + w * kWave);
+        load_lds(k, at, lk_at + to);
+        load_lds(v, at, lv_at + to);
       }
     }
   };
@@ -199,10 +189,22 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
     }
     if (odd) wild = 1;
   };
+  // the first tile is requested before the queries, and these are waited for with it
   if (tid == 0) wild = 0;
   request(0, 0);
   load(0);
-  if constexpr (DT == SPECV_BF16) landed_barrier();
+  {
+    const long base = (static_cast<long>(at.first) + tok) * s.q_row + static_cast<long>(hq) * D + 8 * half;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) xq[f].load(s.q, base + 16 * f);
+    if constexpr (DT == SPECV_BF16) landed_barrier();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      xq[f].hide();
+      xq[f].negate(s.scale < 0.f);
+      if constexpr (!kWhole) xq[f].pieces(q[f]);
+    }
+  }
 
   // a tile's part in the rows; mixed: some rows of the workgroup do not see all of it
   auto step = [&](int tile, auto mixed) {

@@ -8,7 +8,7 @@
 // head r % G of token r / G) from its first key's token on:
 //   S = Q K^T         A = 32 rows x 16 channels,  B = 16 channels x 32 keys
 // A lane then has one key, so that the sum over rows stays in its registers and
-// no atomics join anything.  The rows pass through LDS, 128 at a time and for
+// no atomics join anything.  The rows pass through LDS, 64 at a time and for
 // all waves, from memory without registers between.
 //
 // Bound by the exponentials: a score costs one quarter-rate instruction and two
@@ -31,7 +31,7 @@ constexpr int kWBlock = 256;
 
 // Rows of a tile and waves a SIMD.
 template <int DT, int D> struct WeightShape {
-  static constexpr int tile = DT == SPECV_F32 ? 32 : D == 256 ? 64 : 128;
+  static constexpr int tile = DT == SPECV_F32 ? 32 : 64;
   static constexpr int buffers = DT == SPECV_F32 ? 1 : 2;
   static constexpr int waves = DT == SPECV_F32 && D == 256 ? 1 : 2;
 };
@@ -81,9 +81,6 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
     for (int f = 0; f < NF; ++f) x[f].pieces(k[f]);
   }
 
-  auto token_of = [&](int r) {
-    return s.G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.magic) >> p.shift);
-  };
   // A tile has `step` rows, a multiple of G where G is small, so that a lane's
   // rows are the same heads in every tile and their places the same from the
   // tile's first token on; further rows of the tile weigh nothing.
@@ -92,15 +89,16 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   const int row_first = key0 * s.G, ntile = (rows - row_first + step - 1) / step;
   const long qbase = static_cast<long>(at.first) * s.q_row + static_cast<long>(h) * s.G * D;
   auto offset = [&](int tile, int e) {
-    const int t = e / NC, r = min(row_first + tile * step + t, rows - 1), tok = token_of(r);
+    const int t = e / NC, r = min(row_first + tile * step + t, rows - 1), tok = s.token_of(r);
     return qbase + static_cast<long>(tok) * s.q_row + static_cast<long>(r - tok * s.G) * D + 8 * swizzle<D>(t, e % NC);
   };
   // bf16: a lane's places from the tile's first token on, in bytes: below 2^32, as rows are below 2^24 elements
   auto place_in = [&](int e, int r0, int most) {
-    const int t = e / NC, tok0 = token_of(r0), r = min(r0 + t, most), tok = token_of(r);
+    const int t = e / NC, tok0 = s.token_of(r0), r = min(r0 + t, most), tok = s.token_of(r);
     return 2 * (static_cast<uint32_t>(tok - tok0) * static_cast<uint32_t>(s.q_row) + static_cast<uint32_t>(r - tok * s.G) * D +
                 8 * swizzle<D>(t, e % NC));
   };
+  const uint32_t lq_at = lds_address(&lq[0][0]);
   uint32_t place_at[DT == SPECV_BF16 ? kLoads : 1];
   if constexpr (DT == SPECV_BF16) {
 #pragma unroll
@@ -109,12 +107,12 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   auto request = [&](int tile, int buf) {
     if constexpr (DT == SPECV_BF16) {
       const int r0 = row_first + tile * step;
-      const uint16_t* const from = static_cast<const uint16_t*>(s.q) + qbase + static_cast<long>(__builtin_amdgcn_readfirstlane(token_of(r0))) * s.q_row;
+      const uint16_t* const from = static_cast<const uint16_t*>(s.q) + qbase + static_cast<long>(__builtin_amdgcn_readfirstlane(s.token_of(r0))) * s.q_row;
       const bool whole = even && r0 + step <= rows;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t a = whole ? place_at[i] : place_in(tid + i * kWBlock, r0, rows - 1);
-        load_lds(from, a, &lq[buf][8 * (i * kWBlock + w * kWave)]);
+        load_lds(from, a, lq_at + 2 * (buf * NP * kPlane) + 16 * (i * kWBlock + w * kWave));
       }
     }
   };
@@ -138,7 +136,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
     float x = INFINITY;
     const int r = row_first + tile * step + tid;
     if (tid < step && r < rows) {
-      const int tok = token_of(r);
+      const int tok = s.token_of(r);
       x = p.lse[(static_cast<long>(at.first) + tok) * s.Hq + h * s.G + (r - tok * s.G)];
     }
     return x;

@@ -226,12 +226,18 @@ __device__ inline bf16x8 read_transposed(const __bf16* lo, const __bf16* hi) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Where an array of shared memory begins in LDS.
+template <class T>
+__device__ inline uint32_t lds_address(T* shared) {
+  typedef __attribute__((address_space(3))) T* lds_ptr;
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)shared));
+}
+
 // 16 bytes a lane from memory (the wave's `base`, `offset` bytes further)
-// straight to LDS: the wave's 1024 bytes from `to` on.
-__device__ inline void load_lds(const void* base, uint32_t offset, const void* to) {
-  typedef __attribute__((address_space(3))) const void* lds_ptr;
-  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr)to)));
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory");
+// straight to LDS: the wave's 1024 bytes from address `to` on.
+__device__ inline void load_lds(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(base)
+               : "memory");
 }
 
 // A barrier that orders LDS only: __syncthreads would also wait for every

@@ -18,6 +18,13 @@ struct Packed {
   const int32_t* starts;  // [B + 1]
   float scale;
   int B, T, H, Hq, G;     // G = Hq / H query heads share a key head
+  uint32_t magic;         // r / G is mulhi(r, magic) >> shift for r < 2^31 (G > 1)
+  int shift;
+#ifdef __HIPCC__
+  __device__ int token_of(int r) const {
+    return G == 1 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), magic) >> shift);
+  }
+#endif
 };
 
 struct PromptAttn {
@@ -33,8 +40,6 @@ struct PromptWeights {
   float* w;               // [B][H][capacity]
   int capacity;
   unsigned slots;         // places for blocks of kWeightKeys tokens of a head
-  uint32_t magic;         // r / G is mulhi(r, magic) >> shift for r < 2^31 (G > 1)
-  int shift;
 };
 
 constexpr int kWeightKeys = 128;  // tokens of one workgroup, as keys
