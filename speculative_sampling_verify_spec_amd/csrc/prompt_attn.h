@@ -189,21 +189,43 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
     }
     if (odd) wild = 1;
   };
-  // the first tile is requested before the queries, and these are waited for with it
+  // The queries' rows come the way a tile does, in whole lines, into the buffers
+  // that the second tile will take, where these hold them; else from memory into
+  // registers (48 prompts of 1 to 1500 tokens 403 us, with rows read and written
+  // by lanes 421).
+  constexpr bool kQueriesInLds = DT == SPECV_BF16 && 2 * BN >= kPromptRows;
   if (tid == 0) wild = 0;
   request(0, 0);
   load(0);
-  {
+  if constexpr (kQueriesInLds) {
+    const int tok0 = s.token_of(row0);
+    const uint16_t* const from = static_cast<const uint16_t*>(s.q) + (static_cast<long>(at.first) + tok0) * s.q_row + static_cast<long>(h) * s.G * D;
+#pragma unroll
+    for (int i = 0; i < 2 * kLoads; ++i) {
+      const int e = tid + i * kPBlock, t = e / NC, x = min(row0 + t, rows - 1), y = s.token_of(x);  // the last row again behind it
+      const uint32_t a = 2 * (static_cast<uint32_t>(y - tok0) * static_cast<uint32_t>(s.q_row) + static_cast<uint32_t>(x - y * s.G) * D +
+                              8 * swizzle<D>(t % BN, e % NC));
+      load_lds(from, a, (i < kLoads ? lk_at : lv_at) + 2 * kPlane + 16 * (i % kLoads * kPBlock + w * kWave));
+    }
+    landed_barrier();
+    const __bf16* const rows_at = w < 2 ? lk[1] : lv[1];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int t = 32 * (w % 2) + col;
+      xq[f].w[0] = *reinterpret_cast<const uint4*>(&rows_at[t * D + 8 * swizzle<D>(t, 2 * f + half)]);
+    }
+    lds_barrier();  // before the second tile is requested
+  } else {
     const long base = (static_cast<long>(at.first) + tok) * s.q_row + static_cast<long>(hq) * D + 8 * half;
 #pragma unroll
     for (int f = 0; f < NF; ++f) xq[f].load(s.q, base + 16 * f);
     if constexpr (DT == SPECV_BF16) landed_barrier();
+  }
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      xq[f].hide();
-      xq[f].negate(s.scale < 0.f);
-      if constexpr (!kWhole) xq[f].pieces(q[f]);
-    }
+  for (int f = 0; f < NF; ++f) {
+    xq[f].hide();
+    xq[f].negate(s.scale < 0.f);
+    if constexpr (!kWhole) xq[f].pieces(q[f]);
   }
 
   // a tile's part in the rows; mixed: some rows of the workgroup do not see all of it
@@ -345,18 +367,45 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   l = halves_sum(l);
   const bool there = wrow + col < rows, some = !(l == 0.f);
   const float inv = some ? 1.f / l : 0.f;
-  if (!there) return;
   const long orow = (static_cast<long>(at.first) + tok) * s.Hq + hq;
-  if (p.lse && half == 0) p.lse[orow] = kv_lse(m, l, some);
+  if (p.lse && half == 0 && there) p.lse[orow] = kv_lse(m, l, some);
+  auto value = [&](int d, int i) { return some ? o[d][i] * inv : 0.f; };
+  if constexpr (DT == SPECV_F32) {
+    if (!there) return;
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      float y[4];
+      for (int i = 0; i < 16; i += 4) {
+        const float y[4] = {value(d, i), value(d, i + 1), value(d, i + 2), value(d, i + 3)};
+        kv_store4<DT>(p.out, orow * D + 32 * d + 2 * i + 4 * half, y);
+      }
+  } else {
+    // Through LDS, where a wave has 32 rows for itself by now, to whole lines:
+    // a lane has 4 channels of each 8 and its partner the others; they exchange
+    // what makes 16 bytes for each.
+    __bf16* const out = (w < 2 ? lk[0] : lv[0]) + w % 2 * 32 * D;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = some ? o[d][i + e] * inv : 0.f;
-      kv_store4<DT>(p.out, orow * D + 32 * d + 2 * i + 4 * half, y);
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 8) {
+        uint32_t a[2], b[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          a[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{value(d, i + 2 * k), value(d, i + 2 * k + 1)}), bf16x2));
+          b[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{value(d, i + 4 + 2 * k), value(d, i + 4 + 2 * k + 1)}), bf16x2));
+        }
+        const auto x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false), y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+        *reinterpret_cast<uint4*>(&out[col * D + 8 * swizzle<D>(col, 4 * d + i / 4 + half)]) = make_uint4(x[0], y[0], x[1], y[1]);
+      }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 32 * NC / kWave; ++i) {
+      const int e = i * kWave + lane, t = e / NC, x = wrow + t, y = s.token_of(min(x, rows - 1));
+      if (x < rows)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((static_cast<long>(at.first) + y) * s.Hq + h * s.G + (x - y * s.G)) * D + 8 * (e % NC)) =
+            *reinterpret_cast<const uint4*>(&out[t * D + 8 * swizzle<D>(t, e % NC)]);
     }
+  }
 }
 
 template <int D>
