@@ -396,8 +396,7 @@ def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: in
     kv = _descriptor(cache, page_table.data_ptr(), width)
     lib = load()
     workspace, have = _workspace(cache, lib.spec_kv_evict_workspace_size(kv, B), workspace)
-    out_table, out_lengths = torch.empty_like(page_table), torch.empty_like(lengths)
-    out_weights = torch.empty(weights.shape, dtype=torch.float32, device=cache._device)
+    out_table, out_lengths, out_weights = torch.empty_like(page_table), torch.empty_like(lengths), torch.empty_like(weights)
     kept = torch.empty((B, cache._heads, budget), dtype=torch.int32, device=cache._device)
     _call(cache._device, lib.spec_kv_evict, kv, lengths.data_ptr(), weights.data_ptr(), weights.shape[2], new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B,
           out_table.data_ptr(), out_lengths.data_ptr(), out_weights.data_ptr(), kept.data_ptr(), workspace.data_ptr(),

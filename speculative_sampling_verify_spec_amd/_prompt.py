@@ -7,20 +7,27 @@ from __future__ import annotations
 from typing import Optional
 
 from . import _kv
-from ._kv import KV_DIMS, _bind_torch, _call, _dtype_code, _forward_only, _token_stride
-from ._lib import _ptr, load
+from ._kv import KV_DIMS, _bind_torch, _call, _dtype_code, _forward_only
+from ._lib import load
 
 
-def _rows(name: str, t, T: int, dim: int, like) -> int:
-    """Elements between the token rows of t [T, heads, dim]."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != dim or t.device != like.device or t.dtype != like.dtype:
-        raise ValueError(f"{name} must be [{T}, heads, {dim}], with q's dtype and on q's device")
-    return _token_stride(name, t.unsqueeze(0), t.shape[1], dim)
+def _row(name: str, t, heads: int, dim: int) -> int:
+    """Elements between the token rows of t [T, heads, dim]: heads and channels
+    contiguous (a slice of a fused projection's rows will do)."""
+    row, head, channel = t.stride()
+    if t.shape[0] <= 1 or t.is_contiguous():
+        row = heads * dim
+    if (channel != 1 or (heads > 1 and head != dim)) and t.numel():
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    if row < heads * dim:
+        raise ValueError(f"{name}: tokens must be evenly spaced and must not overlap")
+    return row
 
 
 def _packed(q, k, starts):
-    """Checks of packed prompts: (sequences, q's stride, k's stride, dtype's code)."""
-    if q.device.type != "cuda":
+    """Checks of packed prompts: (T, Hq, dim, heads, sequences, q's stride, k's stride, dtype's code)."""
+    device = q.device
+    if device.type != "cuda":
         raise ValueError("q must be on a GPU")
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, dim]")
@@ -28,14 +35,15 @@ def _packed(q, k, starts):
     if dim not in KV_DIMS:
         raise ValueError(f"dim must be one of {KV_DIMS}, got {dim}")
     code = _dtype_code(q.dtype)
-    q_row, kv_row = _rows("q", q, T, dim, q), _rows("k", k, T, dim, q)
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != dim or k.device != device or k.dtype is not q.dtype:
+        raise ValueError(f"k must be [{T}, heads, {dim}], with q's dtype and on q's device")
     heads = k.shape[1]
     if Hq < 1 or heads < 1 or Hq % heads:
         raise ValueError(f"q's {Hq} heads must be a multiple of k's {heads}")
-    if starts.dtype is not _kv.torch.int32 or starts.dim() != 1 or starts.shape[0] < 2 or starts.device != q.device or \
+    if starts.dtype is not _kv.torch.int32 or starts.dim() != 1 or starts.shape[0] < 2 or starts.device != device or \
             not starts.is_contiguous():
         raise ValueError("starts must be a contiguous int32 [B + 1] tensor on q's device")
-    return starts.shape[0] - 1, q_row, kv_row, code
+    return T, Hq, dim, heads, starts.shape[0] - 1, _row("q", q, Hq, dim), _row("k", k, heads, dim), code
 
 
 def prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, return_lse: bool = False):
@@ -49,16 +57,16 @@ def prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, return_l
     -infinity.  Forward only: a backward pass through the results raises
     NotImplementedError."""
     _bind_torch()
-    B, q_row, kv_row, code = _packed(q, k, starts)
-    T, Hq, dim = q.shape
-    if v.shape != k.shape or _rows("v", v, T, dim, q) != kv_row:
-        raise ValueError("k and v must have the same shape and strides")
-    out = _kv.torch.empty((T, Hq, dim), dtype=q.dtype, device=q.device)
-    lse = _kv.torch.empty((T, Hq), dtype=_kv.torch.float32, device=q.device) if return_lse else None
+    T, Hq, dim, heads, B, q_row, kv_row, code = _packed(q, k, starts)
+    if v.shape != k.shape or v.device != q.device or v.dtype is not q.dtype or _row("v", v, heads, dim) != kv_row:
+        raise ValueError("v must have k's shape, dtype, strides and device")
+    torch = _kv.torch
+    out = torch.empty((T, Hq, dim), dtype=q.dtype, device=q.device)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
     if T:
         _call(q.device, load().spec_prompt_attention, q.data_ptr(), q_row, k.data_ptr(), v.data_ptr(), kv_row,
-              starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, k.shape[1], Hq, dim,
-              out.data_ptr(), _ptr(lse), code)
+              starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, heads, Hq, dim,
+              out.data_ptr(), lse.data_ptr() if return_lse else None, code)
     results = _forward_only((out, lse) if return_lse else (out,), (q, k, v), "prompt_attention")
     return results if return_lse else results[0]
 
@@ -73,16 +81,15 @@ def prompt_weights(q, k, lse, starts, capacity: int, *, scale: Optional[float] =
     query heads of its head; 0 behind the sequence (tokens at and behind
     capacity are left out).  Without gradients."""
     _bind_torch()
-    B, q_row, kv_row, code = _packed(q, k, starts)
-    T, Hq, dim = q.shape
+    T, Hq, dim, heads, B, q_row, kv_row, code = _packed(q, k, starts)
     if lse.dtype is not _kv.torch.float32 or lse.shape != (T, Hq) or lse.device != q.device or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous float32 [{T}, {Hq}] tensor on q's device")
     if capacity < 1:
         raise ValueError("capacity must be at least 1")
-    weights = _kv.torch.empty((B, k.shape[1], capacity), dtype=_kv.torch.float32, device=q.device)
+    weights = _kv.torch.empty((B, heads, capacity), dtype=_kv.torch.float32, device=q.device)
     if not T:
         return weights.zero_()
     _call(q.device, load().spec_prompt_weights, q.data_ptr(), q_row, k.data_ptr(), kv_row, lse.data_ptr(),
-          starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, k.shape[1], Hq, dim,
+          starts.data_ptr(), dim ** -0.5 if scale is None else float(scale), B, T, heads, Hq, dim,
           weights.data_ptr(), capacity, code)
     return weights

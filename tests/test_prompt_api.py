@@ -63,3 +63,13 @@ def test_weights_binding_refuses_host_tensors():
     x = torch.zeros(5, 4, 64)
     with pytest.raises(ValueError, match="GPU"):
         sv.prompt_weights(x, x, torch.zeros(5, 4), torch.zeros(2, dtype=torch.int32), 5)
+
+
+def test_row_strides():
+    from speculative_sampling_verify_spec_amd._prompt import _row
+    x = torch.zeros(5, 10, 64)
+    assert _row("x", x[:, :4], 4, 64) == 640 and _row("x", x, 10, 64) == 640 and _row("x", x[:, 9:], 1, 64) == 640
+    assert _row("x", x[:1, :4], 4, 64) == 256 and _row("x", x[:0, :4], 4, 64) == 256 and _row("x", x[::2], 10, 64) == 1280
+    for bad in (x[:, ::2], x[..., ::2], x.transpose(1, 2), x[:1].expand(5, 10, 64), x[:, :1].expand(5, 10, 64)):
+        with pytest.raises(ValueError):
+            _row("x", bad, bad.shape[1], bad.shape[2])
