@@ -218,7 +218,8 @@ __device__ inline int swizzle(int t, int c) {
 // Eight k of one column for an A operand, from rows of LDS: the 16 lanes of a
 // group give the addresses of 4 rows x 16 columns (lane j row j / 4, columns 4
 // (j % 4) .. + 3) twice, and lane j gets column j of both.
-__device__ inline bf16x8 read_transposed(const __bf16* lo, const __bf16* hi) {
+template <class P>
+__device__ inline bf16x8 read_transposed(P lo, P hi) {
   typedef short s16x4 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) s16x4* lds_ptr;
   const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lo));
@@ -248,13 +249,15 @@ __device__ inline void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// A barrier after which what load_lds requested before it is in LDS.  The wait
-// is one that the compiler knows of (vmcnt 0, lgkmcnt 0): it would else wait
-// for its own loads from before again, and so for the next tile's requests,
-// wherever their results are used.
+// A barrier after which what load_lds requested before it is in LDS, but for the
+// kLeft youngest requests.  The wait is one that the compiler knows of (vmcnt,
+// and lgkmcnt 0): it would else wait for its own loads from before again, and so
+// for the next tile's requests, wherever their results are used.
+template <int kLeft = 0>
 __device__ inline void landed_barrier() {
+  static_assert(kLeft < 64, "6 bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (kLeft & 15) | (kLeft >> 4) << 14);
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
