@@ -18,7 +18,7 @@
 // between, the next tile while this one is worked on.
 //
 // Softmax: the running maximum is held per row and only moved when a tile
-// exceeds it by more than 2^24 (the weights then stay below 2^24, and the sums
+// exceeds it by more than 2^8 (the weights then stay below 2^8, and the sums
 // are in 32 bits), so most tiles rescale nothing.  The weights are rounded to
 // bf16 for the product with the values, as the output is.
 //
@@ -49,7 +49,7 @@ __device__ __forceinline__ void in_order(F f, std::integer_sequence<int, I...>) 
   (f(std::integral_constant<int, I>{}), ...);
 }
 
-constexpr float kHeld = 24.f;  // how far, in powers of two, scores may exceed the held maximum
+constexpr float kHeld = 8.f;  // how far, in powers of two, scores may exceed the held maximum
 
 // Tokens of a tile, LDS buffers of tiles and waves a SIMD.
 template <int DT, int D> struct PromptShape {

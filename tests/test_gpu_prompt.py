@@ -117,6 +117,23 @@ def test_extreme_scores(gpu_lib):
     _check(got, op.attention(*host, [0, T], D ** -0.5), D, "f32")
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 256), ("f32", 96)])
+def test_the_largest_values_do_not_overflow(gpu_lib, dtype, D):
+    """Values up to 2^100 under scores that grow by little along the row, so
+    that weights stand above the held maximum."""
+    import torch
+    rng = np.random.default_rng(D)
+    T = 700
+    (q, k, v), _ = ph.inputs(rng, T, 2, 1, D, dtype)
+    q.fill_(0.5)
+    k.copy_(torch.linspace(0.0, 60.0 / D, T, device="cuda")[:, None, None])  # scores up to 30 * scale = 4 and below
+    v.clamp_(-1.0, 1.0).mul_(2.0 ** 100 * (1 - 2.0 ** -7))
+    host = [t.double().cpu().numpy() for t in (q, k, v)]
+    for scale in (0.13, 1.1):
+        got = gpu_lib.prompt_attention(q, k, v, _i32([0, T]), scale=scale, return_lse=True)
+        _check(got, op.attention(*host, [0, T], scale), D, dtype)
+
+
 def test_ranges_that_do_not_ascend_stay_inside(gpu_lib):
     """Whatever starts holds, rows are read and written inside [0, T) only, and
     a sequence that no other overlaps is right."""
