@@ -95,10 +95,11 @@ __device__ inline int lanes_sum_upto(int v) {
 // rows see).  Where the chip has work for several turns (places from kInOrder
 // on), sequences come one after the other, so that blocks that read the same
 // keys do so together; else the highest blocks of all sequences come first,
-// so that no long one begins late: 48 prompts of 1 to 1500 tokens (9648 places)
-// take 444 us in order and 480 us highest first, 6 of up to 2047 with heads of
-// 256 (632 places) 88 and 83 us.
-constexpr unsigned kInOrder = 2048;
+// so that no long one begins late.  In order and highest first: 48 prompts of 25
+// to 1405 tokens 411 and 448 us (9648 places), their weights 234 and 211 (2704
+// places), those of 2 prompts of 8000 and 8191 755 and 640 (1032), 6 prompts
+// with heads of 256 71 and 66 us (618).
+constexpr unsigned kInOrder = 4096;
 
 template <bool FROM_START>
 __device__ inline PromptBlock prompt_block_of_few(const Packed& s, int place, int per_token, int size) {
