@@ -21,8 +21,12 @@ bool covers(const KvView& c, int64_t capacity) {
   return capacity >= (static_cast<int64_t>(c.width) << c.pshift) && capacity <= INT32_MAX;
 }
 
-// Workgroups to aim at, four waves each, of 64 tokens a turn.
-constexpr long kWeightGroups = 2048;
+// Workgroups that share a head's tokens, for `pairs` sequences' heads: two a CU
+// where that fills them; more of one for so many pairs that the longest sequence
+// would end alone.  512 and 2048 workgroups aimed at: 1 sequence of 131072 tokens
+// 24 and 28 us, 16 of up to 4096 13 and 16, 64 of up to 2111 22.8 and 24.4, but
+// 100 of up to 4096 (800 pairs) 53 and 45.
+long weight_splits(long pairs) { return pairs <= 512 ? 512 / pairs : std::max(1L, 2048 / pairs); }
 
 }  // namespace
 }  // namespace sv
@@ -65,7 +69,7 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
   p.out = out_weights;
   p.capacity = capacity;
   const long turns = ((static_cast<long>(p.c.width) << p.c.pshift) + 255) / 256, pairs = static_cast<long>(B) * p.c.H;
-  p.splits = static_cast<unsigned>(std::min(turns, std::max(1L, kWeightGroups / pairs)));
+  p.splits = static_cast<unsigned>(std::min(turns, weight_splits(pairs)));
   return launch_kv_weights(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
 }
 
