@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
       int first, last;
       prompt_range(s, static_cast<int>(b), first, last);
       if (first < last) continue;
-      for (int j = lane; j < p.capacity; j += kWave) p.w[(b * s.H + h) * p.capacity + j] = 0.f;
+      for (long j = lane; j < p.capacity; j += kWave) p.w[(b * s.H + h) * p.capacity + j] = 0.f;
     }
     return;
   }
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   const int key0 = block * kWeightKeys, wkey = key0 + 32 * w, key = wkey + col;
   float* const wrow = p.w + (static_cast<long>(at.seq) * s.H + h) * p.capacity;
   if (block == nblock - 1)  // behind the prompt
-    for (int j = len + tid; j < p.capacity; j += kWBlock) wrow[j] = 0.f;
+    for (long j = static_cast<long>(len) + tid; j < p.capacity; j += kWBlock) wrow[j] = 0.f;
 
   __shared__ __align__(16) __bf16 lq[Shape::buffers][NP * kPlane];
   __shared__ __align__(16) float ll[Shape::buffers][BM];  // lse in log2; +infinity where a row weighs nothing

@@ -171,6 +171,20 @@ def test_rows_past_32_bits(gpu_lib):
         assert not far_w[b, 0, 200:].any()
 
 
+def test_the_largest_capacity(gpu_lib):
+    """Rows of 2^31 - 1 weights, of a sequence and of one without tokens, are cleared to their ends."""
+    import torch
+    rng = np.random.default_rng(11)
+    (q, k, v), _ = ph.inputs(rng, 70, 2, 1, 64, "bf16")
+    starts, capacity = _i32([0, 70, 70]), 2 ** 31 - 1
+    _, lse = gpu_lib.prompt_attention(q, k, v, starts, return_lse=True)
+    got = gpu_lib.prompt_weights(q, k, lse, starts, capacity)
+    assert torch.equal(got[:, :, :90], gpu_lib.prompt_weights(q, k, lse, starts, 90))
+    for b in range(2):
+        for part in got[b, 0, 70:].split(1 << 29):
+            assert not part.any()
+
+
 def test_pools_and_weights_past_32_bits(gpu_lib):
     """Pages whose codes stand behind 2^32 bytes, and a row of weights behind
     2^31 floats: gathered, cut and read as a small cache with the same tokens."""
