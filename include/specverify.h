@@ -580,7 +580,8 @@ int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t 
  *               query that weighs nothing
  *   weights, out_weights  [B][heads][capacity] float; the same array, or
  *               arrays that do not overlap (SPECV_E_OVERLAP)
- *   max_pages * page_size <= capacity < 2^31;  B * heads < 2^24
+ *   max_pages * page_size <= capacity < 2^31 and at most 2^31 - 2^15;
+ *   B * heads < 2^24
  * The other limits are those of spec_kv_attention.  Sums are in 32 bits, in
  * an order that does not change from call to call.  Needs no workspace;
  * nothing synchronises.
@@ -607,7 +608,8 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
  *               table row holds and no other sequence is given; read for the
  *               sequences that are cut only
  *   1 <= budget <= max_pages * page_size;  0 <= recent <= budget <= limit;
- *   max_pages * page_size <= capacity < 2^31;  B <= 65535;  B * heads *
+ *   max_pages * page_size <= capacity < 2^31 and at most 2^31 - 2^15;
+ *   B <= 65535;  B * heads *
  *   ceil(budget / page_size) < 2^23;  B * heads * ceil(max_pages * page_size /
  *   16384) < 2^22
  *   out_table   [B][max_pages] int32: the new pages, then -1, of a sequence

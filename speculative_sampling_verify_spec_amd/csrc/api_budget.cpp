@@ -16,9 +16,13 @@ bool apart(const void* a, long na, const void* b, long nb) {
   return !overlap(static_cast<const int32_t*>(a), na, static_cast<const int32_t*>(b), nb);
 }
 
+// Positions are rounded up to a workgroup's in 32 bits.
+constexpr int64_t kMostPositions = (int64_t(1) << 31) - 2 * kEvictTile;
+int64_t positions(const KvView& c) { return static_cast<int64_t>(c.width) << c.pshift; }
+
 // Weights cover every position that the table can hold.
 bool covers(const KvView& c, int64_t capacity) {
-  return capacity >= (static_cast<int64_t>(c.width) << c.pshift) && capacity <= INT32_MAX;
+  return capacity >= positions(c) && positions(c) <= kMostPositions && capacity <= INT32_MAX;
 }
 
 // Workgroups that share a head's tokens, for `pairs` sequences' heads: two a CU
@@ -76,7 +80,7 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
 size_t spec_kv_evict_workspace_size(const specv_kv_t* kv, int B) {
   using namespace sv;
   KvView c{};
-  if (check_cache(kv, &c) != SPECV_OK || B < 1 || B > kMaxSeqs) return 0;
+  if (check_cache(kv, &c) != SPECV_OK || B < 1 || B > kMaxSeqs || positions(c) > kMostPositions) return 0;
   const long rows = static_cast<long>(B) * c.H, tiles = kv_evict_tiles(c);
   if (rows * tiles >= (1L << 22)) return 0;  // a grid's threads stay below 2^32
   return std::max(kAlign, tiles > 1 ? align_up(static_cast<size_t>(rows) * tiles * kEvictWords * sizeof(uint32_t)) : 0);

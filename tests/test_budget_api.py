@@ -87,6 +87,18 @@ def test_evict_of_too_many_pages(lib):
     assert evict(lib, c, C=1 << 19, budget=1 << 19, limit=1 << 19, B=1, **far) == -2
 
 
+def test_tables_of_next_to_2_31_positions(lib):
+    """Positions are rounded up to whole workgroups in 32 bits, so the last 2^15 below 2^31 are refused."""
+    most = ((1 << 31) - (1 << 15)) // 128
+    for pages, ok in ((most, True), (most + 1, False), ((1 << 24) - 1, False)):
+        c, C = kv(heads=1, page_size=128, max_pages=pages), (1 << 31) - 1
+        assert (lib.spec_kv_evict_workspace_size(ctypes.byref(c), 1) > 0) == ok
+        if not ok:
+            far = {n: (i + 1) << 44 for i, n in enumerate(("lengths", "w", "new", "table", "out_len", "out", "kept"))}
+            assert evict(lib, c, C=C, B=1, **far) == -2
+            assert weigh(lib, c, C=C, B=1, Hq=4, w=FAR, out=FAR) == -2
+
+
 def test_evict_workspace_sizes(lib):
     """256 bytes up to 16384 positions, then counts and lists of every 16384 of a head; 0 for what is refused."""
     def size(B, **kw):
