@@ -1,5 +1,7 @@
 // Eviction of the cached tokens that gathered the least weight: choosing what
 // stays, and moving it to new pages.
+#include <type_traits>
+
 #include "sv_budget.h"
 #include "sv_device.h"
 #include "sv_mfma.h"
@@ -393,14 +395,20 @@ __host__ __device__ inline int v_row(int P) { return P + 4; }
 // codes and scales together.
 //
 // K rows are copied 16 bytes a thread and stay in its registers between the
-// two.  V pages have a channel's tokens side by side: a lane takes a channel
-// and loads 16 tokens of it, of which it puts those that stay into LDS one
-// after the other; which ones they are is the same for all lanes, so that this
-// costs one LDS write for a token and 64 channels.
+// two.  V pages have a channel's tokens side by side.  Where many of them stay, a
+// lane takes a channel and loads 16 tokens of it, of which it puts those that stay
+// into LDS one after the other; which ones they are is the same for all lanes, so
+// that this costs one LDS write for a token and 64 channels.  Where few stay, the
+// loads are what counts: four lanes take a channel's 64 tokens, so that a request
+// is of whole 64 bytes, and each puts its own into LDS.  Sequences cut the first
+// and the second way (us a call; heads of 128): in pages of 128 tokens to a
+// quarter 161 and 140, to an eighth 145 and 113, to a sixteenth (2 of up to
+// 131072) 134 and 118; in pages of 64 lengths of 900 to 4096 to 1024 107 and 114,
+// to a quarter 132 and 131, to an eighth 108 and 103, to a sixteenth 88 and 88.
 //
 // Bound by the lines of V that the kept tokens lie in, nearly all of them even
 // if one token in 16 stays: 64 sequences of up to 4096 tokens to 1024 (8 heads
-// of 128) 88 us, 4.1 TB/s; 2 of up to 131072 to 8192 89 us, 3.4 TB/s.
+// of 128) 88 us, 4.1 TB/s; 2 of up to 131072 to 8192 74 us, 4.1 TB/s.
 template <int FMT, int kMost>  // kMost: pieces of 16 K codes of a block that a thread has at most
 __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
   const KvView& c = p.c;
@@ -411,7 +419,7 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
   const int32_t* const kept = p.kept + (b * c.H + h) * static_cast<long>(p.budget) + col * P;
   // a thread per token, and the tokens of a wave's share of V one a lane
   const int per = (n + kMWaves - 1) / kMWaves, t0 = min(w * per, n), own = min(per, n - t0);
-  const int to = p.new_pages[b * p.new_width + col], first = kept[0];
+  const int to = p.new_pages[b * p.new_width + col], first = kept[0], last = kept[n - 1];
   const int at_k = tid < n ? kept[tid] : -1, at_v = lane < own ? kept[t0 + lane] : -1;
   if (first < 0 || to < 0 || to >= c.pages) return;  // not cut, or no page to move to
   const int page_k = at_k < 0 ? -1 : kv_page(c, b, at_k >> c.pshift), page_v = at_v < 0 ? -1 : kv_page(c, b, at_v >> c.pshift);
@@ -435,61 +443,137 @@ __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
     x[i] = make_uint4(0, 0, 0, 0);
     if (e < all && row_at[t] != ~size_t(0)) x[i] = *reinterpret_cast<const uint4*>(c.kp + row_at[t] + 16 * (e - t * pieces));
   }
-  // ---- V: into LDS; the wave's tokens in runs that lie in the same 16 tokens
-  // of a page, four of which are loaded before the first is needed ----
-  const int row = v_row(P);
+  // ---- V: into LDS; the wave's tokens in runs that lie in the same 16 tokens of a
+  // page, or in the same 64 (or all of a smaller page) where few stay; some runs
+  // are loaded before the first is needed ----
+  constexpr int kFew = kMost > 2 ? 3 : 5;  // larger blocks gain from a third on, smaller ones from a fifth
+  const bool few = P > 16 && last - first >= kFew * n;
+  const int row = v_row(P), sshift = few ? min(c.pshift, 6) - 4 : 0, seg = 16 << sshift;
   const int mine = page_v < 0 ? -1 : at_v & (P - 1);
-  const uint64_t mine_at = mine < 0 ? 0 : (static_cast<size_t>(page_v) * c.H + h) * bytes + (mine & ~15);
+  const uint64_t mine_at = mine < 0 ? 0 : (static_cast<size_t>(page_v) * c.H + h) * bytes + (mine & ~(seg - 1));
   const uint32_t at_lo = static_cast<uint32_t>(mine_at), at_hi = static_cast<uint32_t>(mine_at >> 32);
   const int prev = __shfl_up(mine, 1, kWave);
   const uint32_t prev_lo = __shfl_up(at_lo, 1, kWave), prev_hi = __shfl_up(at_hi, 1, kWave);
-  uint64_t left = __ballot(lane < own && (lane == 0 || mine < 0 || prev < 0 || prev_lo != at_lo || prev_hi != at_hi));
-  const int run = (D + kWave - 1) / kWave;  // blocks of 64 channels, at most 4
-  constexpr int kRuns = 4;
-  while (left) {
-    uint64_t lo[kRuns][2], hi[kRuns][2];
-    for (int half = 0; half < run; half += 2) {  // two blocks of channels at a time
+  // places do not go up where a table holds a page more than once
+  uint64_t left = __ballot(lane < own && (lane == 0 || mine < 0 || prev < 0 || mine <= prev || prev_lo != at_lo || prev_hi != at_hi));
+  if (!few) {
+    // a lane has a channel; the tokens that stay are the same for all lanes
+    const int run = (D + kWave - 1) / kWave;  // blocks of 64 channels, at most 4
+    constexpr int kRuns = 4;
+    while (left) {
+      uint64_t lo[kRuns][2], hi[kRuns][2];
+      for (int half = 0; half < run; half += 2) {  // two blocks of channels at a time
+        uint64_t rest = left;
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) lo[k][i] = hi[k][i] = 0;
+          if (!rest) continue;
+          const int s = __builtin_ctzll(rest);
+          rest &= rest - 1;
+          if (__builtin_amdgcn_readlane(mine, s) < 0) continue;
+          const uint64_t from = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(at_hi, s))) << 32 |
+                                static_cast<uint32_t>(__builtin_amdgcn_readlane(at_lo, s));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (half + i < run) {
+              const int d = min((half + i) * kWave + lane, D - 1);
+              const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(c.vp + from + static_cast<size_t>(d) * P);
+              lo[k][i] = y.x;
+              hi[k][i] = y.y;
+            }
+        }
+        rest = left;
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+          if (!rest) continue;
+          int t = __builtin_ctzll(rest);
+          rest &= rest - 1;
+          const int end = rest ? __builtin_ctzll(rest) : own;
+          for (; t < end; ++t) {
+            const int at = __builtin_amdgcn_readlane(mine, t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (half + i < run) {
+                const int d = (half + i) * kWave + lane;
+                const uint64_t y = at & 8 ? hi[k][i] : lo[k][i];
+                if (d < D) codes[d * row + t0 + t] = static_cast<uint8_t>(y >> (8 * (at & 7)));
+              }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k) left &= left - 1;
+    }
+  } else {
+    // lanes side by side have 16 tokens each of a channel, of which every lane puts its own into LDS
+    const int part = lane & ((1 << sshift) - 1), chan = lane >> sshift;
+    const int per_chunk = kWave >> sshift, chunks = (D + per_chunk - 1) / per_chunk;  // channels of a load, and loads
+    constexpr int kRuns = 2, kChunks = kMost > 2 ? 4 : 2;
+    while (left) {
+      uint64_t from[kRuns], stay[kRuns];  // a run's place, and its tokens among those of the place
+      int begin[kRuns];
       uint64_t rest = left;
 #pragma unroll
       for (int k = 0; k < kRuns; ++k) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) lo[k][i] = hi[k][i] = 0;
-        if (!rest) continue;
-        const int s = __builtin_ctzll(rest);
-        rest &= rest - 1;
-        if (__builtin_amdgcn_readlane(mine, s) < 0) continue;
-        const uint64_t from = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(at_hi, s))) << 32 |
-                              static_cast<uint32_t>(__builtin_amdgcn_readlane(at_lo, s));
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (half + i < run) {
-            const int d = min((half + i) * kWave + lane, D - 1);
-            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(c.vp + from + static_cast<size_t>(d) * P);
-            lo[k][i] = y.x;
-            hi[k][i] = y.y;
-          }
-      }
-      rest = left;
-#pragma unroll
-      for (int k = 0; k < kRuns; ++k) {
+        from[k] = stay[k] = 0;
+        begin[k] = 0;
         if (!rest) continue;
         int t = __builtin_ctzll(rest);
         rest &= rest - 1;
         const int end = rest ? __builtin_ctzll(rest) : own;
-        for (; t < end; ++t) {
-          const int at = __builtin_amdgcn_readlane(mine, t);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (half + i < run) {
-              const int d = (half + i) * kWave + lane;
-              const uint64_t y = at & 8 ? hi[k][i] : lo[k][i];
-              if (d < D) codes[d * row + t0 + t] = static_cast<uint8_t>(y >> (8 * (at & 7)));
-            }
+        begin[k] = t0 + t;
+        if (__builtin_amdgcn_readlane(mine, t) < 0) {  // no page: a zero
+          for (int d = lane; d < D; d += kWave) codes[d * row + t0 + t] = 0;
+          continue;
         }
+        from[k] = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(at_hi, t))) << 32 |
+                  static_cast<uint32_t>(__builtin_amdgcn_readlane(at_lo, t));
+        for (; t < end; ++t) stay[k] |= uint64_t(1) << (__builtin_amdgcn_readlane(mine, t) & (seg - 1));
       }
-    }
+      for (int first = 0; first < chunks; first += kChunks) {
+        uint64_t lo[kRuns][kChunks], hi[kRuns][kChunks];
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) left &= left - 1;
+        for (int k = 0; k < kRuns; ++k) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            lo[k][i] = hi[k][i] = 0;
+            if (stay[k] && first + i < chunks) {
+              const int d = min((first + i) * per_chunk + chan, D - 1);
+              const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(c.vp + from[k] + static_cast<size_t>(d) * P + 16 * part);
+              lo[k][i] = y.x;
+              hi[k][i] = y.y;
+            }
+          }
+        }
+        auto keep = [&](auto run) {
+          constexpr int k = decltype(run)::value;
+          if (!stay[k]) return;
+          uint32_t own16 = static_cast<uint32_t>(stay[k] >> (16 * part)) & 0xffffu;
+          uint8_t* to = &codes[begin[k] + __popcll(stay[k] & ((uint64_t(1) << (16 * part)) - 1))];
+          int most = 0;  // of a lane's
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = max(most, __popc(static_cast<uint32_t>(stay[k] >> (16 * i)) & 0xffffu));
+          for (int n16 = 0; n16 < most; ++n16, ++to) {
+            if (own16) {
+              const int at = __builtin_ctz(own16);
+#pragma unroll
+              for (int i = 0; i < kChunks; ++i) {
+                const int d = (first + i) * per_chunk + chan;
+                const uint64_t y = at & 8 ? hi[k][i] : lo[k][i];
+                const uint32_t z = static_cast<uint32_t>(at & 4 ? y >> 32 : y);
+                if (first + i < chunks && d < D) to[d * row] = static_cast<uint8_t>(z >> (8 * (at & 3)));
+              }
+            }
+            own16 &= own16 - 1;
+          }
+        };
+        keep(std::integral_constant<int, 0>{});
+        keep(std::integral_constant<int, 1>{});
+      }
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k) left &= left - 1;
+    }
   }
   if (tid < P) {
     unit_k[tid] = ks;

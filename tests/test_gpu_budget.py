@@ -214,6 +214,9 @@ EVICT = [  # fmt, P, H, D, lens, budget, recent, limit
     ("int8", 16, 1, 64, [2000, 1023, 1025], 1, 0, 1),
     ("e4m3", 32, 1, 64, [1500, 5000], 1024, 1000, 1024),
     ("int8", 64, 2, 96, [1100], 1000, 0, 1000),
+    ("e4m3", 64, 2, 128, [1000, 4000], 100, 7, 100),
+    ("int8", 32, 2, 256, [900, 400], 70, 3, 70),
+    ("e4m3", 128, 1, 128, [3000, 513], 140, 0, 140),
 ]
 
 
@@ -308,6 +311,20 @@ def test_evict_long_and_shared_pages(gpu_lib):
     before = c["k_pages"][table[0, :50]].copy()
     _evict_check(gpu_lib, c, table, lens, weights, new, budget, 300, budget)
     np.testing.assert_array_equal(c["k_pages"][table[0, :50]], before)
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128])
+def test_evict_a_page_that_a_table_holds_twice(gpu_lib, P):
+    """Positions of the same page one after the other, in and out of order."""
+    rng = np.random.default_rng(P)
+    lens, budget = [12 * P, 7 * P - 3], 2 * P + 5
+    c, table, new, weights = _evict_state(rng, "e4m3", P, 2, 96, lens, budget)
+    table[0, 1:6] = table[0, 0]
+    table[1, 3], table[0, 9] = table[1, 5], -1
+    weights[:, :, ::3] = 0
+    _evict_check(gpu_lib, c, table, lens, weights, new, budget, 2, budget)
+    weights[0, :, :4 * P:P // 2] = 1e9  # two a page, far apart
+    _evict_check(gpu_lib, c, table, lens, weights, new, budget, 2, budget)
 
 
 @pytest.mark.parametrize("kind", ["any", "equal", "mostly zero", "two", "nan"])
