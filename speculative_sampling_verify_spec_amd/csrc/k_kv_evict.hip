@@ -145,6 +145,7 @@ __global__ __launch_bounds__(kSBlock) void k_kv_list(KvEvict p) {
   v.load(x.row, x.len, p.capacity, tile);
   const int ntile = (x.len + kTile - 1) / kTile, top = kBins - 1 - 2 * tid;
   uint32_t x0 = 0, x1 = 0;  // a thread's two bins, counted from the top
+#pragma unroll 8
   for (int t = 0; t < ntile; ++t) {
     const uint2 y = *reinterpret_cast<const uint2*>(bins_of(p, x.pair, t) + top - 1);
     x0 += y.y;
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(kSBlock) void k_kv_list(KvEvict p) {
 // the digits found, in a table of its own, which every wave then looks through
 // for itself.  What is above that weight stays, and of those equal to it the
 // first ones.  Rows of up to 16384 weights are in the workgroup's registers
-// (MANY false); 512 rows of up to 4096 take 19 us, the passes' chain, as 32 rows
+// (MANY false); 512 rows of up to 4096 take 15 us, the passes' chain, as 32 rows
 // of 700 take 9.  Of longer ones the first 11 bits are known, and the weights
 // that have them are listed by the workgroups of the row (or read again, where
 // a workgroup has more of them than its list takes).
@@ -234,40 +235,59 @@ __global__ __launch_bounds__(kSBlock) void k_kv_select(KvEvict p) {
     found = mine.digit << 21;
     need = mine.need;
   }
-  // a tile's weights that may be the last to stay: use(key)
-  auto candidates = [&](int t, uint32_t mask, auto&& use) {
-    if constexpr (MANY) {
-      const uint32_t same = told_of(p, x.pair, t)->same;
-      const uint32_t* const list = list_of(p, x.pair, t);
-      if (same <= kList) {
-        for (uint32_t i = tid; i < same; i += kSBlock)
-          if ((list[i] & mask) == (found & mask)) use(list[i]);
-        return;
+  // the weights of the row's first tiles that may be the last to stay: use(key).
+  // Lists are read eight at a time, a thread's two places of each: loads that
+  // do not wait for each other; eight stay in registers for all passes.
+  uint32_t same[8], key[8][2];
+  auto read = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) same[i] = t0 + i < ntile ? told_of(p, x.pair, t0 + i)->same : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t at = tid + j * kSBlock;
+        key[i][j] = same[i] <= kList && at < same[i] ? list_of(p, x.pair, t0 + i)[at] : 0u;
       }
-      if (t != tile) {
-        Held other;
-        other.load(x.row, x.len, p.capacity, t);
-        other.each(x.len, [&](int at, float y) {
-          const uint32_t key = weight_key(y);
-          if (at < x.n && (key & mask) == (found & mask)) use(key);
-        });
-        return;
-      }
-    }
-    v.each(x.len, [&](int at, float y) {
-      const uint32_t key = weight_key(y);
-      if (at < x.n && (key & mask) == (found & mask)) use(key);
-    });
   };
+  if (MANY && some) read(0);
+  auto candidates = [&](int tiles, uint32_t mask, auto&& use) {
+    if constexpr (MANY) {
+      for (int t0 = 0; t0 < tiles; t0 += 8) {
+        if (ntile > 8) read(t0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (t0 + i >= tiles) break;
+          if (same[i] <= kList) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (static_cast<uint32_t>(tid + j * kSBlock) < same[i] && (key[i][j] & mask) == (found & mask)) use(key[i][j]);
+            continue;
+          }
+          Held other;
+          other.load(x.row, x.len, p.capacity, t0 + i);
+          other.each(x.len, [&](int at, float y) {
+            const uint32_t k = weight_key(y);
+            if (at < x.n && (k & mask) == (found & mask)) use(k);
+          });
+        }
+      }
+    } else {
+      v.each(x.len, [&](int at, float y) {
+        const uint32_t key = weight_key(y);
+        if (at < x.n && (key & mask) == (found & mask)) use(key);
+      });
+    }
+  };
+  static_assert(kList <= 2 * kSBlock, "two places a thread");
   __syncthreads();
   if (some) {
     constexpr int kPasses = MANY ? 3 : 4;
-#pragma unroll
+#pragma unroll MANY ? 1 : kPasses
     for (int pass = 0; pass < kPasses; ++pass) {
       const int upper = MANY ? 21 - 8 * pass : 32 - 8 * pass, shift = upper > 8 ? upper - 8 : 0;  // bits below those found
       const uint32_t mask = upper == 32 ? 0u : ~0u << upper;
-      for (int t = 0; t < (MANY ? ntile : 1); ++t)
-        candidates(t, mask, [&](uint32_t key) { atomicAdd(&hist[pass][(key >> shift) & 255u & ~(mask >> shift)][lane & 3], 1u); });
+      candidates(ntile, mask, [&](uint32_t key) { atomicAdd(&hist[pass][(key >> shift) & 255u & ~(mask >> shift)][lane & 3], 1u); });
       __syncthreads();
       // the highest digit with `need` weights at and above it: a lane has four, counted from the top
       uint32_t n[4], sum = 0;
@@ -298,14 +318,12 @@ __global__ __launch_bounds__(kSBlock) void k_kv_select(KvEvict p) {
     if (tid < 2) before[tid] = 0;
     __syncthreads();
     uint32_t more = 0, equal = 0;
-    for (int t = 0; t < tile; ++t) {
-      if (tid == 0) more += told_of(p, x.pair, t)->over;
-      if (some)
-        candidates(t, ~0u << 21, [&](uint32_t key) {
-          more += key > found ? 1u : 0u;
-          equal += key == found ? 1u : 0u;
-        });
-    }
+    for (int t = tid; t < tile; t += kSBlock) more += told_of(p, x.pair, t)->over;
+    if (some)
+      candidates(tile, ~0u << 21, [&](uint32_t key) {
+        more += key > found ? 1u : 0u;
+        equal += key == found ? 1u : 0u;
+      });
     more = lane_of(lanes_upto(more), kWave - 1);
     equal = lane_of(lanes_upto(equal), kWave - 1);
     if (lane == 0) {
