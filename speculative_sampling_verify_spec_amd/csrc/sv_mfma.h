@@ -235,10 +235,13 @@ __device__ inline uint32_t lds_address(T* shared) {
 }
 
 // 16 bytes a lane from memory (the wave's `base`, `offset` bytes further)
-// straight to LDS: the wave's 1024 bytes from address `to` on.
+// straight to LDS: the wave's 1024 bytes from address `to` on.  The load takes
+// that address from M0, a wait state after it was written; the compiler, which
+// else sees to that, does not look into the string.
 __device__ inline void load_lds(const void* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset), "s"(base)
-               : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(to)), "v"(offset),
+               "s"(base)
+               : "memory", "m0");
 }
 
 // A barrier that orders LDS only: __syncthreads would also wait for every
