@@ -503,7 +503,9 @@ int spec_kv_attention(const specv_kv_t* kv, const void* q, int64_t q_stride, con
  * spec_prompt_attention - causal attention of whole prompts, packed: T token
  * rows, of which sequence b has the rows starts[b] .. starts[b+1]-1 (starts
  * are to ascend within [0, T]; whatever they hold, nothing outside the rows is
- * read or written).  With G = Hq / heads query heads per key head, query
+ * read or written.  Where they descend, sequences of which no two share a row
+ * are right as well, and the rows between them undefined; if some share rows,
+ * all results are).  With G = Hq / heads query heads per key head, query
  * (token i, head hq) sees the tokens j <= i of its own sequence in head hq / G:
  *   s_j = scale * (q . k_j),  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
  *   lse = ln sum_j e^(s_j).

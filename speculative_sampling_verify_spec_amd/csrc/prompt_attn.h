@@ -78,8 +78,25 @@ __global__ __launch_bounds__(kPBlock, (PromptShape<DT, D>::waves)) void k_prompt
   const int tid = threadIdx.x, lane = tid % kWave, w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane % 32, half = lane / 32;
   if (at.block < 0) {
-    // tokens of no sequence (before the first and behind the last) see nothing
-    const int lead = min(max(s.starts[0], 0), s.T), tail = min(max(s.starts[s.B], lead), s.T);
+    // Tokens of no sequence see nothing: those before and behind all that one
+    // holds, wherever it stands among starts, so that no row has two writers
+    // unless sequences share it.
+    __shared__ int held[2];
+    if (tid == 0) {
+      held[0] = s.T;
+      held[1] = 0;
+    }
+    __syncthreads();
+    for (int b = tid; b < s.B; b += kPBlock) {
+      int first, last;
+      prompt_range(s, b, first, last);
+      if (first < last) {
+        atomicMin(&held[0], first);
+        atomicMax(&held[1], last);
+      }
+    }
+    __syncthreads();
+    const int lead = held[0], tail = max(held[1], lead);
     const int gone = lead + s.T - tail;
     const unsigned free = p.slots - at.used;
     float zero[4] = {0.f, 0.f, 0.f, 0.f};

@@ -147,6 +147,29 @@ def test_ranges_that_do_not_ascend_stay_inside(gpu_lib):
         _check(got, op.attention(*host, starts, D ** -0.5), D, "bf16")
 
 
+@pytest.mark.parametrize("dtype,G", [("bf16", 4), ("f32", 1)])
+def test_clearing_leaves_the_rows_that_sequences_hold(gpu_lib, dtype, G):
+    """Starts that descend, over more blocks than the card takes at once, so that
+    the rows of no sequence are cleared when the others are long done: the same
+    bits as with starts that ascend."""
+    import torch
+    rng = np.random.default_rng(16)
+    T, H, D = 4000, 32, 64
+    (q, k, v), _ = ph.inputs(rng, T, H * G, H, D, dtype)
+    for starts, ascending in (([2000, 0, T], [0, 0, T]), ([3900, 0, 1700], [0, 1700, 1700])):
+        out, lse = gpu_lib.prompt_attention(q, k, v, _i32(starts), return_lse=True)
+        want = gpu_lib.prompt_attention(q, k, v, _i32(ascending), return_lse=True)
+        held = max(ascending)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert torch.isfinite(lse[:held]).all() and torch.isneginf(lse[held:]).all() and not out[held:].any()
+    # out of order, none shares a row: rows behind the last are cleared, those between are anyone's
+    got = gpu_lib.prompt_attention(q, k, v, _i32([2000, 3000, 100, 1500]), return_lse=True)
+    want = gpu_lib.prompt_attention(q, k, v, _i32([100, 1500, 2000, 3000]), return_lse=True)
+    for a, b in zip(got, want):
+        for rows in (slice(0, 1500), slice(2000, T)):
+            assert torch.equal(a[rows], b[rows])
+
+
 def test_many_sequences(gpu_lib):
     """More sequences than a workgroup has threads, most of one token or none."""
     rng = np.random.default_rng(12)
