@@ -32,6 +32,12 @@ constexpr int kGWaves = 4, kGBlock = kGWaves * kWave;
 constexpr int kGTile = 64;
 constexpr int kGMostLds = 64 << 10;  // bytes of row fragments: two workgroups a CU at least
 
+// A row's weight of a token; a row of lse +infinity weighs nothing, whatever its
+// score is (256 paths 88.9 us, without that 87.9).
+__device__ inline float weight(float score, float scale, float lse) {
+  return lse == INFINITY ? 0.f : ex2(fmaf(score, scale, -lse));
+}
+
 // Bytes of 16 rows in LDS.
 template <int DT, int D>
 constexpr int kRowBlock = D / 32 * kPieces<DT> * kWave * 16 + 64;
@@ -150,7 +156,7 @@ __global__ __launch_bounds__(kGBlock, D == 256 ? 2 : D == 128 ? 3 : 4) void k_kv
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[t] += ex2(fmaf(s[t][i], kc[t], -l4[i]));
+          for (int i = 0; i < 4; ++i) sum[t] += weight(s[t][i], kc[t], l4[i]);
       }
       // lane 16 t + col gets its token's sum
       float mine = 0.f;
@@ -187,7 +193,7 @@ __global__ __launch_bounds__(kGBlock, D == 256 ? 2 : D == 128 ? 3 : 4) void k_kv
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (row0 + 4 * g + i >= mine * p.G) sum += ex2(fmaf(s[i], kscale, -l4[i]));
+          if (row0 + 4 * g + i >= mine * p.G) sum += weight(s[i], kscale, l4[i]);
       }
       sum = groups_sum(sum);
       if (g == 0 && mine < count && pos < p.capacity) orow[pos] = row_at ? orow[pos] + sum : sum;

@@ -186,6 +186,23 @@ def test_node_weights(gpu_lib, fmt, dtype, P, H, G, D, N, lens, path):
         np.testing.assert_array_equal(w.cpu().numpy()[~rows], weights[~rows])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("fmt,dtype,G,D,N", [("e4m3", "bf16", 3, 128, 7), ("int8", "f32", 1, 64, 33), ("e4m3", "bf16", 2, 256, 2)])
+def test_node_queries_that_weigh_nothing(gpu_lib, fmt, dtype, G, D, N, bad):
+    """Nodes that no one looked at (lse -infinity, as an attention gives those past
+    num_nodes) and whose queries are anything weigh nothing, the last ones too,
+    whose rows fill up the block."""
+    import torch
+    rng = np.random.default_rng(N)
+    c, table, q, k, host, _, weights, lse = _nodes(gpu_lib, rng, fmt, dtype, 32, 2, G, D, N, [70, 0, 33], False)
+    lse[0, N - 1], lse[1, N // 2, G], lse[2] = -np.inf, np.inf, -np.inf
+    want, written = ob.kv_weights(c, table, host[0], lse.astype(np.float64), [70, 0, 33], weights, D ** -0.5, host[1])
+    q[0, N - 1] = q[1, N // 2, G] = q[2] = bad
+    got = gpu_lib.kv_weights(kh.to_device(gpu_lib, c), _i32(table), q, _f32(lse), _i32([70, 0, 33]), _f32(weights), k)
+    _weights_close(got, want, D, np.broadcast_to(written[:, None], weights.shape))
+    assert torch.isfinite(got).all()
+
+
 def test_node_weights_read_no_free_memory(gpu_lib):
     """Free slots, pages and table entries hold NaN (make_cache's poison), as
     do the nodes that are not kept; positions without a page gather nothing."""
