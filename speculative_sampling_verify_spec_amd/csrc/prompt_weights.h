@@ -151,77 +151,89 @@ __global__ __launch_bounds__(kWBlock, (WeightShape<DT, D>::waves)) void k_prompt
   // From the last tile on: all workgroups of a head begin with the same rows
   // and go on together, so that they find them in the cache (2 x 8191: 795 us,
   // from each one's own first rows on 814 us, at an earlier build).
-  request(ntile - 1, 0);
-  float next = stat(ntile - 1);
-  float sum = 0.f, lost = 0.f;  // the tiles' sums are added with what each addition rounds away
-  if constexpr (DT == SPECV_BF16) {
-    put_stat(0, next);
-    landed_barrier();
-  }
-  for (int tile = ntile - 1; tile >= 0; --tile) {
-    const int buf = Shape::buffers == 2 ? (ntile - 1 - tile) & 1 : 0;
-    const bool more = tile > 0;
-    if constexpr (DT == SPECV_F32) {
-      fill(tile);
+  //
+  // A query that weighs nothing (lse infinite) makes e^(s - lse) 0 by itself,
+  // unless its score is not finite: then the sums are NaN, and are made again
+  // with every statistic looked at (done at once, in the tiles that have such
+  // queries: 48 prompts 230 us from 217, 2 x 8191 690 from 649; so 211 from 209
+  // and 645.5 from 644.6, both sides in turn).
+  float sum;
+  for (bool careful = false;; careful = true) {
+    request(ntile - 1, 0);
+    float next = stat(ntile - 1), lost = 0.f;  // the tiles' sums are added with what each addition rounds away
+    sum = 0.f;
+    if constexpr (DT == SPECV_BF16) {
       put_stat(0, next);
-      if (more) next = stat(tile - 1);
-      __syncthreads();
-    } else if (more) {
-      next = stat(tile - 1);
-      request(tile - 1, buf ^ 1);
+      landed_barrier();
     }
-    const int r0 = row_first + tile * step;
-    if (wkey < len && r0 + BM > wkey * s.G) {  // a row sees a key of the wave
-      float part = 0.f;
-      // The products of a block of 32 rows are under way while the exponentials
-      // of the block before are taken: the matrix unit and the vector unit work
-      // at the same time, and a product's result is not waited for.
-      auto scores = [&](int n, f32x16& sc) {
+    for (int tile = ntile - 1; tile >= 0; --tile) {
+      const int buf = Shape::buffers == 2 ? (ntile - 1 - tile) & 1 : 0;
+      const bool more = tile > 0;
+      if constexpr (DT == SPECV_F32) {
+        fill(tile);
+        put_stat(0, next);
+        if (more) next = stat(tile - 1);
+        __syncthreads();
+      } else if (more) {
+        next = stat(tile - 1);
+        request(tile - 1, buf ^ 1);
+      }
+      const int r0 = row_first + tile * step;
+      if (wkey < len && r0 + BM > wkey * s.G) {  // a row sees a key of the wave
+        float part = 0.f;
+        // The products of a block of 32 rows are under way while the exponentials
+        // of the block before are taken: the matrix unit and the vector unit work
+        // at the same time, and a product's result is not waited for.
+        auto scores = [&](int n, f32x16& sc) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[i] = 0.f;
+          for (int i = 0; i < 16; ++i) sc[i] = 0.f;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          bf16x8 a[NP];
-          const int t = 32 * n + col;
+          for (int f = 0; f < NF; ++f) {
+            bf16x8 a[NP];
+            const int t = 32 * n + col;
 #pragma unroll
-          for (int j = 0; j < NP; ++j)
-            a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
+            for (int j = 0; j < NP; ++j)
+              a[j] = *reinterpret_cast<const bf16x8*>(&lq[buf][j * kPlane + t * D + 8 * swizzle<D>(t, 2 * f + half)]);
 #pragma unroll
-          for (int z = NP - 1; z >= 0; --z)
+            for (int z = NP - 1; z >= 0; --z)
 #pragma unroll
-            for (int i = 0; i <= z; ++i) sc = mfma32(a[z - i], k[f][i], sc);
-        }
-      };
-      // mixed: some rows do not see some of the wave's keys
-      auto blocks = [&](auto mixed) {
-        f32x16 sc[2];
-        scores(0, sc[0]);
+              for (int i = 0; i <= z; ++i) sc = mfma32(a[z - i], k[f][i], sc);
+          }
+        };
+        // mixed: some rows do not see some of the wave's keys; wild: some that weigh nothing have scores that are not finite
+        auto blocks = [&](auto mixed, auto wild) {
+          f32x16 sc[2];
+          scores(0, sc[0]);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          if (n + 1 < NB) scores(n + 1, sc[(n + 1) & 1]);
-          // rows from `first` on see the lane's key; from `past` on they are others' copies
-          const int first = key * s.G - (r0 + 32 * n + 4 * half), past = step - (32 * n + 4 * half);
+          for (int n = 0; n < NB; ++n) {
+            if (n + 1 < NB) scores(n + 1, sc[(n + 1) & 1]);
+            // rows from `first` on see the lane's key; from `past` on they are others' copies
+            const int first = key * s.G - (r0 + 32 * n + 4 * half), past = step - (32 * n + 4 * half);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
+            for (int j = 0; j < 4; ++j) {
+              const f32x4 l4 = *reinterpret_cast<const f32x4*>(&ll[buf][32 * n + 8 * j + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e = ex2(fmaf(sc[n & 1][4 * j + i], kscale, -l4[i]));
-              part += decltype(mixed)::value && (8 * j + i < first || 8 * j + i >= past) ? 0.f : e;  // whatever an unseen score is
+              for (int i = 0; i < 4; ++i) {
+                const float e = ex2(fmaf(sc[n & 1][4 * j + i], kscale, -l4[i]));
+                const bool none = (decltype(mixed)::value && (8 * j + i < first || 8 * j + i >= past)) || (decltype(wild)::value && l4[i] == INFINITY);
+                part += none ? 0.f : e;  // whatever an unseen score is
+              }
             }
           }
-        }
-      };
-      if (r0 >= (wkey + 31) * s.G) blocks(std::false_type{});
-      else blocks(std::true_type{});
-      const float y = part - lost, z = sum + y;
-      lost = (z - sum) - y;
-      sum = z;
+        };
+        if (careful) blocks(std::true_type{}, std::true_type{});
+        else if (r0 >= (wkey + 31) * s.G) blocks(std::false_type{}, std::false_type{});
+        else blocks(std::true_type{}, std::false_type{});
+        const float y = part - lost, z = sum + y;
+        lost = (z - sum) - y;
+        sum = z;
+      }
+      if constexpr (DT == SPECV_BF16) {
+        if (more) put_stat(buf ^ 1, next);
+      }
+      landed_barrier();
     }
-    if constexpr (DT == SPECV_BF16) {
-      if (more) put_stat(buf ^ 1, next);
-    }
-    landed_barrier();
+    if (careful || !__syncthreads_or(sum != sum)) break;
   }
   sum = halves_sum(sum);
   if (half == 0 && key < len && key < p.capacity) wrow[key] = sum;

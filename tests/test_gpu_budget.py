@@ -108,6 +108,24 @@ def test_prompt_weights_of_statistics_that_are_not_finite(gpu_lib, dtype, D):
     _weights_close(got, want, D, rows)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 4), ("bf16", 64, 3), ("f32", 64, 1), ("f32", 256, 5), ("bf16", 96, 40)])
+def test_prompt_queries_that_weigh_nothing(gpu_lib, dtype, D, G, bad):
+    """Queries of lse -infinity or +infinity weigh nothing whatever they hold, also
+    where a tile's further rows are copies of the last one."""
+    import torch
+    rng = np.random.default_rng(G)
+    n, H = 300, 2
+    (q, k, v), host = ph.inputs(rng, n, H * G, H, D, dtype)
+    _, lse = gpu_lib.prompt_attention(q, k, v, _i32([0, n]), return_lse=True)
+    for rows, value in ((n - 1, -np.inf), (slice(20, 23), np.inf), (slice(130, 150), -np.inf), ((200, H * G - 1), -np.inf)):
+        lse[rows], q[rows] = value, bad
+    want = ob.prompt_weights(*host[:2], lse.double().cpu().numpy(), [0, n], D ** -0.5, n)
+    got = gpu_lib.prompt_weights(q, k, lse, _i32([0, n]), n)
+    _weights_close(got, want, D)
+    assert torch.isfinite(got).all()
+
+
 @pytest.mark.parametrize("dtype,D,H,G,n", [("bf16", 128, 1, 4, 2500), ("bf16", 256, 1, 2, 1111), ("f32", 64, 2, 1, 901)])
 def test_long_prompt_weights(gpu_lib, dtype, D, H, G, n):
     """Against 64 bits on the device: the weights of long prompts, to 1e-6 of
