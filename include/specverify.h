@@ -581,7 +581,8 @@ int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t 
  *   lse         [B][N][Hq] float: out_lse of spec_kv_attention; -infinity: a
  *               query that weighs nothing
  *   weights, out_weights  [B][heads][capacity] float; the same array, or
- *               arrays that do not overlap (SPECV_E_OVERLAP)
+ *               arrays that do not overlap; out_weights overlaps nothing
+ *               else that the call reads (SPECV_E_OVERLAP)
  *   max_pages * page_size <= capacity < 2^31 and at most 2^31 - 2^15;
  *   B * heads < 2^24
  * The other limits are those of spec_kv_attention.  Sums are in 32 bits, in

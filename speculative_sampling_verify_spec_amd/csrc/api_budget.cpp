@@ -16,6 +16,13 @@ bool apart(const void* a, long na, const void* b, long nb) {
   return !overlap(static_cast<const int32_t*>(a), na, static_cast<const int32_t*>(b), nb);
 }
 
+// Words from the first to the last of `rows` token rows `stride` elements
+// apart, of `row` elements each (strides that no memory has are cut short).
+long row_words(long rows, int64_t stride, long row, int dtype) {
+  const long n = (rows - 1) * std::min<int64_t>(stride, int64_t(1) << 36) + row;
+  return dtype == SPECV_F32 ? n : n / 2;
+}
+
 // Positions are rounded up to a workgroup's in 32 bits.
 constexpr int64_t kMostPositions = (int64_t(1) << 31) - 2 * kEvictTile;
 int64_t positions(const KvView& c) { return static_cast<int64_t>(c.width) << c.pshift; }
@@ -56,6 +63,13 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
   if (!aligned16(q) || !aligned16(k_new)) return SPECV_E_ALIGN;
   const long all = static_cast<long>(B) * p.c.H * capacity;
   if (weights != out_weights && !apart(weights, all, out_weights, all)) return SPECV_E_OVERLAP;
+  // workgroups write a head's weights while others still read these
+  const long nodes = static_cast<long>(B) * N, blocks = static_cast<long>(p.c.pages) * p.c.H;
+  const struct { const void* at; long n; } in[] = {{q, row_words(nodes, q_stride, Hq * p.c.D, dtype)},
+      {k_new, row_words(nodes, k_stride, p.c.H * p.c.D, dtype)}, {lse, nodes * Hq}, {lengths, B}, {counts, B}, {index, nodes},
+      {p.c.table, static_cast<long>(B) * p.c.width}, {p.c.kp, blocks * p.c.P * p.c.D / 4}, {p.c.ks, blocks}};
+  for (const auto& x : in)
+    if (!apart(x.at, x.n, out_weights, all)) return SPECV_E_OVERLAP;
   p.q = q;
   p.kn = k_new;
   p.q_row = q_stride;

@@ -53,6 +53,24 @@ def test_weights_refusals(lib, kw, code):
     assert weigh(lib, **kw) == code
 
 
+def test_weights_overlap(lib):
+    """The weights written may touch nothing else that the call reads, at either end of it."""
+    B, N, Hq, H, D, C, width = 4, 3, 32, 8, 128, 640, 10
+    all_ = 4 * B * H * C
+    sizes = dict(q=2 * (B * N * 5000 - 5000 + Hq * D), lse=4 * B * N * Hq, k=2 * (B * N * 2000 - 2000 + H * D), lengths=4 * B,
+                 counts=4 * B, index=4 * B * N, w=all_)
+    at = {n: (i + 3) * FAR for i, n in enumerate(sizes)}
+    for n, size in sizes.items():
+        edges = (at[n] + size - 4, at[n] - all_ + 4) + ((at[n],) if n != "w" else ())
+        for out in edges:
+            assert weigh(lib, **{**at, "out": out, "qs": 5000, "ks": 2000}) == -9, n
+    cache = dict(page_table=4 * B * width, k_pages=100 * H * 64 * D, k_scales=4 * 100 * H)
+    far = {n: (i + 20) * FAR for i, n in enumerate(("k_pages", "v_pages", "k_scales", "v_scales", "page_table"))}
+    for n, size in cache.items():
+        for out in (far[n], far[n] + size - 4, far[n] - all_ + 4):
+            assert weigh(lib, kv(**far), **{**at, "out": out}) == -9, n
+
+
 def test_weights_of_too_many_heads(lib):
     assert weigh(lib, kv(heads=512), B=32768, Hq=512) == -2
 
