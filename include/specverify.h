@@ -622,7 +622,8 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
  *   out_kept    [B][heads][budget] int32: the old positions, or -1 where the
  *               sequence was not cut
  *   workspace   spec_kv_evict_workspace_size() bytes, 256-byte aligned
- * The outputs overlap neither the inputs nor each other (SPECV_E_OVERLAP).
+ * The outputs and the workspace overlap neither the inputs nor each other
+ * (SPECV_E_OVERLAP; the workspace is not compared with the cache's arrays).
  * Every layer can be cut by weights of its own: tables and lengths come out
  * alike.  Nothing synchronises.
  */

@@ -118,7 +118,7 @@ int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* wei
   if (!need || heads * width >= (1L << 23)) return SPECV_E_SHAPE;  // a grid's threads stay below 2^32
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign || workspace_bytes < need) return SPECV_E_WORKSPACE;
   // workgroups write these while others still read those
-  const struct { const void* at; long n; } in[] = {{lengths, B}, {p.c.table, table}, {new_pages, pages}, {weights, all}},
+  const struct Words { const void* at; long n; } in[] = {{lengths, B}, {p.c.table, table}, {new_pages, pages}, {weights, all}},
       out[] = {{out_table, table}, {out_lengths, B}, {out_weights, all}, {kept, keep}};
   for (int i = 0; i < 4; ++i) {
     for (const auto& x : in)
@@ -126,6 +126,9 @@ int spec_kv_evict(const specv_kv_t* kv, const int32_t* lengths, const float* wei
     for (int j = 0; j < i; ++j)
       if (!apart(out[j].at, out[j].n, out[i].at, out[i].n)) return SPECV_E_OVERLAP;
   }
+  // the workspace too; the cache's own arrays, the page table among them, are not compared with it
+  for (const auto& x : {in[0], in[2], in[3], out[0], out[1], out[2], out[3]})
+    if (!apart(x.at, x.n, workspace, static_cast<long>(need / 4))) return SPECV_E_OVERLAP;
   p.lengths = lengths;
   p.w = weights;
   p.capacity = capacity;

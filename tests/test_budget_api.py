@@ -99,6 +99,19 @@ def test_evict_overlap(lib):
             assert evict(lib, **{**at, o: x}) == -9, o
 
 
+def test_evict_workspace_overlap(lib):
+    """The workspace may touch no input and no output, at either end of it."""
+    B, H, C, width, budget, new = 4, 8, 1 << 15, 257, 100, 2
+    c = kv(max_pages=width)
+    need = lib.spec_kv_evict_workspace_size(ctypes.byref(c), B)
+    assert need == B * H * 2 * 16384
+    sizes = dict(lengths=B, w=B * H * C, new=B * new, table=B * width, out_len=B, out=B * H * C, kept=B * H * budget)
+    at = {n: (i + 2) * FAR for i, n in enumerate(sizes)}
+    for n, size in sizes.items():
+        for ws in (at[n], at[n] - need + 256, at[n] + (4 * size - 1) // 256 * 256):
+            assert evict(lib, c, **{**at, "C": C, "ws": ws}) == -9, n
+
+
 def test_evict_of_too_many_pages(lib):
     c = kv(heads=512, page_size=16, max_pages=1 << 15)
     far = {n: (i + 1) << 44 for i, n in enumerate(("lengths", "w", "new", "table", "out_len", "out", "kept"))}
