@@ -148,6 +148,48 @@ def test_long_prompt_weights(gpu_lib, dtype, D, H, G, n):
     assert ((got - want).abs() <= 1.01 * slack + 48 * U * want).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prompt_weights_of_many_blocks_in_order(gpu_lib, dtype):
+    """64 ragged sequences, some empty, of more blocks than the card takes at
+    once: each block's weights once, the same bits as found the other way."""
+    import torch
+    rng = np.random.default_rng(17)
+    lens = rng.integers(0, 400, 64)
+    lens[[0, 20, 21, 63]] = 0
+    starts = 1 + np.concatenate([[0], np.cumsum(lens)])
+    T, H, cap = int(starts[-1]) + 2, 32, 300
+    assert (-(-T // 128) + 64) * H >= 4096
+    (q, k, v), host = ph.inputs(rng, T, H, H, 64, dtype)
+    _, lse = gpu_lib.prompt_attention(q, k, v, _i32(starts), return_lse=True)
+    got = gpu_lib.prompt_weights(q, k, lse, _i32(starts), cap)
+    more = gpu_lib.prompt_weights(q, k, lse, _i32(np.concatenate([starts, [starts[-1]] * 9])), cap)
+    assert torch.equal(got, more[:64]) and not more[64:].any()
+    for b in (1, 40, 62):
+        rows = slice(starts[b], starts[b + 1])
+        want = ob.prompt_weights(host[0][rows, :2], host[1][rows, :2], lse[rows, :2].double().cpu().numpy(), [0, lens[b]], 0.125, cap)
+        _weights_close(got[b:b + 1, :2], want, 64)
+    fit = lens <= cap  # every query gives a weight of 1
+    np.testing.assert_allclose(got.sum(2).cpu().numpy()[fit], np.outer(lens[fit], np.ones(H)), rtol=2e-3)
+
+
+def test_prompt_weights_of_many_sequences(gpu_lib):
+    """700 sequences, most of them empty or short: the same bits as in groups of 50."""
+    import torch
+    rng = np.random.default_rng(18)
+    lens = rng.integers(0, 4, 700) * rng.integers(0, 2, 700)
+    lens[[3, 300, 699]] = 200, 140, 33
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    (q, k, v), host = ph.inputs(rng, int(starts[-1]), 4, 2, 64, "bf16")
+    _, lse = gpu_lib.prompt_attention(q, k, v, _i32(starts), return_lse=True)
+    got = gpu_lib.prompt_weights(q, k, lse, _i32(starts), 180)
+    for b in range(0, 700, 50):
+        rows = slice(starts[b], starts[b + 50])
+        part = gpu_lib.prompt_weights(q[rows], k[rows], lse[rows], _i32(starts[b:b + 51] - starts[b]), 180)
+        assert torch.equal(got[b:b + 50], part)
+    assert not got[torch.from_numpy(lens == 0)].any()
+    _weights_close(got, ob.prompt_weights(*host[:2], lse.double().cpu().numpy(), starts, 0.125, 180), 64)
+
+
 # --------------------------------------------------------------- nodes --
 NODES = [  # fmt, dtype, P, H, G, D, N, lens, path
     ("e4m3", "bf16", 16, 2, 4, 128, 1, [0, 1, 15, 16, 17, 200], False),
@@ -379,6 +421,27 @@ def test_evict_rows_of_several_workgroups(gpu_lib, kind, budget, recent):
         weights = np.where(pick < 0.7, 1.0, 1.0 + 2.0 ** -23).astype(np.float32)
     elif kind == "nan":
         weights[pick < 0.999] = np.nan
+    _evict_check(gpu_lib, c, table, lens, weights, new, budget, recent, budget)
+
+
+@pytest.mark.parametrize("kind", ["any", "decaying", "equal", "ties behind", "two"])
+def test_evict_rows_of_more_than_eight_workgroups(gpu_lib, kind):
+    """Rows of 9 and 17 workgroups, more than keep each other's lists in registers:
+    weights that fit the lists, that decay slowly (as flat attention's do) and do
+    not, that are all the same, the same from the ninth workgroup on, and of two
+    values."""
+    rng = np.random.default_rng(len(kind))
+    lens, budget, recent = [9 * 16384 - 77, 17 * 16384, 3000], 400, 33
+    c, table, new, weights = _evict_state(rng, "int8", 128, 1, 64, lens, budget)
+    n, at = weights.shape[2], np.arange(weights.shape[2])
+    if kind == "decaying":
+        weights[:] = np.log(n / (at + 1.0)) * (1 + 0.01 * rng.random(weights.shape))
+    elif kind == "equal":
+        weights[:] = 0.3
+    elif kind == "ties behind":
+        weights[:] = np.where(at < 8 * 16384 + 9000, 0.25 * (at % 500 == 3), 0.125)
+    elif kind == "two":
+        weights[:] = np.where(rng.random(weights.shape) < 0.002, 1.0 + 2.0 ** -23, 1.0)
     _evict_check(gpu_lib, c, table, lens, weights, new, budget, recent, budget)
 
 

@@ -201,6 +201,28 @@ def test_blocks_of_few_sequences_in_any_order(gpu_lib):
                 _check((out[first:last], lse[first:last]), _exact(q[first:last], k[first:last], v[first:last], 0.125), 64, "bf16")
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 64), ("bf16", 256)])
+def test_many_blocks_in_order(gpu_lib, dtype, D):
+    """64 ragged sequences, some empty, of more blocks than the card takes at
+    once: these are handed out in order.  Each block once, the same bits as with
+    more sequences, whose blocks are found another way."""
+    import torch
+    rng = np.random.default_rng(17)
+    lens = rng.integers(0, 400, 64)
+    lens[[0, 20, 21, 63]] = 0
+    starts = 1 + np.concatenate([[0], np.cumsum(lens)])
+    T, H = int(starts[-1]) + 2, 32
+    assert (-(-T // 128) + 64) * H >= 4096
+    (q, k, v), _ = ph.inputs(rng, T, H, H, D, dtype)
+    got = gpu_lib.prompt_attention(q, k, v, _i32(starts), return_lse=True)
+    more = gpu_lib.prompt_attention(q, k, v, _i32(np.concatenate([starts, [starts[-1]] * 9])), return_lse=True)
+    assert torch.equal(got[0], more[0]) and torch.equal(got[1], more[1])
+    assert torch.isneginf(got[1][:1]).all() and torch.isneginf(got[1][starts[-1]:]).all()
+    for b in (1, 40, 62):
+        rows = slice(starts[b], starts[b + 1])
+        _check([t[rows] for t in got], _exact(q[rows], k[rows], v[rows], D ** -0.5), D, dtype)
+
+
 def _exact(q, k, v, scale):
     """One sequence in 64 bits on the device: what op.attention gives."""
     import torch
