@@ -32,12 +32,18 @@ bool covers(const KvView& c, int64_t capacity) {
   return capacity >= positions(c) && positions(c) <= kMostPositions && capacity <= INT32_MAX;
 }
 
-// Workgroups that share a head's tokens, for `pairs` sequences' heads: two a CU
-// where that fills them; more of one for so many pairs that the longest sequence
-// would end alone.  512 and 2048 workgroups aimed at: 1 sequence of 131072 tokens
-// 24 and 28 us, 16 of up to 4096 13 and 16, 64 of up to 2111 22.8 and 24.4, but
-// 100 of up to 4096 (800 pairs) 53 and 45.
-long weight_splits(long pairs) { return pairs <= 512 ? 512 / pairs : std::max(1L, 2048 / pairs); }
+// Workgroups that share a head's tokens, for `pairs` sequences' heads of up to
+// `turns` times 256 tokens: two a CU where that fills them, and up to eight as
+// long as each has eight turns, so that the longest sequence does not end alone;
+// eight a CU for so many pairs that its length alone would decide.  512, 2048
+// and this many (us; heads of 8): 1 sequence of 131072 tokens 23.7, 26.7, 23.6; 16 of
+// up to 4096 13.7, 16.2, 13.7; 64 of up to 2111 22.4, 24.4, 22.5; 32 of up to 32768 170,
+// 140, 140, 33 of them 278, 146, 145, 64 of them 327, 262, 262; 40 of 8192 88, 73, 73.
+// 40 of up to 2111 tokens take 20.5 so, with six workgroups a head 17.5.
+long weight_splits(long pairs, long turns) {
+  const long most = std::max(1L, 2048 / pairs);
+  return pairs > 512 ? most : std::max(512 / pairs, std::min(most, turns / 8));
+}
 
 }  // namespace
 }  // namespace sv
@@ -87,7 +93,7 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
   p.out = out_weights;
   p.capacity = capacity;
   const long turns = ((static_cast<long>(p.c.width) << p.c.pshift) + 255) / 256, pairs = static_cast<long>(B) * p.c.H;
-  p.splits = static_cast<unsigned>(std::min(turns, weight_splits(pairs)));
+  p.splits = static_cast<unsigned>(std::min(turns, weight_splits(pairs, turns)));
   return launch_kv_weights(p, dtype, kv->type, static_cast<hipStream_t>(stream)) == hipSuccess ? SPECV_OK : SPECV_E_HIP;
 }
 
