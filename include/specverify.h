@@ -554,7 +554,7 @@ int spec_prompt_attention(const void* q, int64_t q_stride, const void* k, const 
  *   out_weights[b][h][j] = sum over tokens i >= j of sequence b and query heads
  *                          of head h of e^(s_ij - lse_i),
  * 0 behind the sequence's tokens; those at and behind `capacity` are left out.
- * A query whose lse is -infinity weighs nothing.
+ * A query whose lse is infinite weighs nothing, whatever it holds.
  *   lse         [T][Hq] float: out_lse of spec_prompt_attention
  *   out_weights [B][heads][capacity] float; overlaps no input
  *   1 <= capacity < 2^31;  (ceil(T / 128) + B) * heads < 2^24
@@ -578,12 +578,12 @@ int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t 
  * lengths[b] + m the sum over itself and the kept nodes after it alone.
  * Positions behind are left as they were.
  *   q, k_new    as for spec_kv_attention (k_new NULL: the cached tokens only)
- *   lse         [B][N][Hq] float: out_lse of spec_kv_attention; -infinity: a
- *               query that weighs nothing
+ *   lse         [B][N][Hq] float: out_lse of spec_kv_attention; infinite: a
+ *               query that weighs nothing, whatever it holds
  *   weights, out_weights  [B][heads][capacity] float; the same array, or
  *               arrays that do not overlap; out_weights overlaps nothing
  *               else that the call reads (SPECV_E_OVERLAP)
- *   max_pages * page_size <= capacity < 2^31 and at most 2^31 - 2^15;
+ *   max_pages * page_size at most 2^31 - 2^15 and at most capacity < 2^31;
  *   B * heads < 2^24
  * The other limits are those of spec_kv_attention.  Sums are in 32 bits, in
  * an order that does not change from call to call.  Needs no workspace;
@@ -611,12 +611,13 @@ int spec_kv_weights(const specv_kv_t* kv, const void* q, int64_t q_stride, const
  *               table row holds and no other sequence is given; read for the
  *               sequences that are cut only
  *   1 <= budget <= max_pages * page_size;  0 <= recent <= budget <= limit;
- *   max_pages * page_size <= capacity < 2^31 and at most 2^31 - 2^15;
- *   B <= 65535;  B * heads *
- *   ceil(budget / page_size) < 2^23;  B * heads * ceil(max_pages * page_size /
- *   16384) < 2^22
+ *   max_pages * page_size at most 2^31 - 2^15 and at most capacity < 2^31;
+ *   B <= 65535;  B * heads * ceil(budget / page_size) < 2^23;  B * heads *
+ *   ceil(max_pages * page_size / 16384) < 2^22
  *   out_table   [B][max_pages] int32: the new pages, then -1, of a sequence
- *               that was cut; else its row of the page table
+ *               that was cut; else its row of the page table.  Where budget
+ *               fills the last new page, the next spec_kv_append needs one
+ *               more in the row: it takes no token from a missing page on
  *   out_lengths [B] int32: budget, or the length (clamped as the cache's calls do)
  *   out_weights [B][heads][capacity] float: the weights by new position, 0 behind
  *   out_kept    [B][heads][budget] int32: the old positions, or -1 where the

@@ -330,13 +330,14 @@ def kv_weights(cache: KVCache, page_table, q, lse, lengths, weights, k_new=None,
     nodes a round keeps (spec_kv_weights).
 
     q [B, N, Hq, dim] and k_new [B, N, heads, dim] as for kv_attention, lse [B,
-    N, Hq] as it returns it, lengths [B] the tokens cached before the round,
+    N, Hq] as it returns it (infinite: a query that weighs nothing), lengths [B] the
+    tokens cached before the round,
     counts [B] and index [B, N] the kept nodes as for kv_append; weights [B,
     heads, capacity] float32 by cached position, capacity at least max_pages *
     page_size.  Kept nodes get their own weights behind the cached positions
     when k_new is given.  Works in weights itself, or into `out` (positions
-    behind are left as they were).  Returns the tensor written, without
-    gradients."""
+    behind are left as they were), which overlaps no other tensor of the call.
+    Returns the tensor written, without gradients."""
     _check_table(cache, page_table)
     B, width = page_table.shape
     if q.dim() != 4:
@@ -382,8 +383,10 @@ def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: in
     ceil(budget / page_size)] int32, pages that no table holds.  Returns
     (page_table, lengths, weights) as they are after the call, in new tensors,
     and when asked the kept positions [B, heads, budget] int32 (-1 where a
-    sequence was not cut).  The old pages of the sequences that were cut can be
-    used again once the call's work is done."""
+    sequence was not cut).  The table rows of the sequences that were cut hold
+    their new pages and -1 behind: kv_append takes tokens up to the last of these
+    only, until the rows are given more.  The old pages can be used again once the
+    call's work is done."""
     _check_table(cache, page_table)
     B, width = page_table.shape
     limit = budget if limit is None else limit
@@ -398,7 +401,7 @@ def kv_evict(cache: KVCache, page_table, lengths, weights, new_pages, budget: in
     workspace, have = _workspace(cache, lib.spec_kv_evict_workspace_size(kv, B), workspace)
     out_table, out_lengths, out_weights = torch.empty_like(page_table), torch.empty_like(lengths), torch.empty_like(weights)
     kept = torch.empty((B, cache._heads, budget), dtype=torch.int32, device=cache._device)
-    _call(cache._device, lib.spec_kv_evict, kv, lengths.data_ptr(), weights.data_ptr(), weights.shape[2], new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B,
-          out_table.data_ptr(), out_lengths.data_ptr(), out_weights.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
-          have)
+    _call(cache._device, lib.spec_kv_evict, kv, lengths.data_ptr(), weights.data_ptr(), weights.shape[2],
+          new_pages.data_ptr(), budget, recent, min(limit, 2 ** 31 - 1), B, out_table.data_ptr(), out_lengths.data_ptr(),
+          out_weights.data_ptr(), kept.data_ptr(), workspace.data_ptr(), have)
     return (out_table, out_lengths, out_weights) + ((kept,) if return_kept else ())

@@ -51,7 +51,7 @@ def prompt_attention(q, k, v, starts, *, scale: Optional[float] = None, return_l
 
     q [T, Hq, dim], k and v [T, heads, dim] (bf16 or fp32; slices of a fused
     projection's rows will do; k and v with the same strides), Hq a multiple of
-    heads; starts [B + 1] int32: sequence b has the rows starts[b] ..
+    heads; starts [B + 1] int32, ascending: sequence b has the rows starts[b] ..
     starts[b+1]-1.  scale defaults to dim ** -0.5.  Returns out [T, Hq, dim]
     and, when asked, lse [T, Hq] float32; rows of no sequence are 0 and
     -infinity.  Forward only: a backward pass through the results raises
@@ -76,10 +76,11 @@ def prompt_weights(q, k, lse, starts, capacity: int, *, scale: Optional[float] =
     prompts themselves (spec_prompt_weights).
 
     q, k, starts and scale as for prompt_attention, lse [T, Hq] float32 as it
-    returns it.  Returns weights [B, heads, capacity] float32: by token of the
-    sequence, the sum of e^(score - lse) over the queries that see it and the
-    query heads of its head; 0 behind the sequence (tokens at and behind
-    capacity are left out).  Without gradients."""
+    returns it (infinite: a query that weighs nothing).  Returns weights [B,
+    heads, capacity] float32: by token of the sequence, the sum of e^(score -
+    lse) over the queries that see it and the query heads of its head; 0 behind
+    the sequence (tokens at and behind capacity are left out).  Without
+    gradients."""
     _bind_torch()
     T, Hq, dim, heads, B, q_row, kv_row, code = _packed(q, k, starts)
     if lse.dtype is not _kv.torch.float32 or lse.shape != (T, Hq) or lse.device != q.device or not lse.is_contiguous():

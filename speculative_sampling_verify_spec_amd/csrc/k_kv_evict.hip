@@ -196,7 +196,11 @@ __global__ __launch_bounds__(kSBlock) void k_kv_list(KvEvict p) {
 // (MANY false); 512 rows of up to 4096 take 15 us, the passes' chain, as 32 rows
 // of 700 take 9.  Of longer ones the first 11 bits are known, and the weights
 // that have them are listed by the workgroups of the row (or read again, where
-// a workgroup has more of them than its list takes).
+// a workgroup has more of them than its list takes: where all weights are the same,
+// every workgroup reads the whole row in every pass.  A call of 2 rows of up to
+// 131072 takes 176 us then, of 1 of 278528 314 and of 1 of 2^20 1911, with weights
+// spread over many powers of two 117, 129 and 385, with weights that decay as the
+// logarithm of the position 85, 98 and 329).
 template <bool MANY>
 __global__ __launch_bounds__(kSBlock) void k_kv_select(KvEvict p) {
   const KvView& c = p.c;
@@ -426,7 +430,7 @@ __host__ __device__ inline int v_row(int P) { return P + 4; }
 //
 // Bound by the lines of V that the kept tokens lie in, nearly all of them even
 // if one token in 16 stays: 64 sequences of up to 4096 tokens to 1024 (8 heads
-// of 128) 88 us, 4.1 TB/s; 2 of up to 131072 to 8192 74 us, 4.1 TB/s.
+// of 128) 88 us, 4.1 TB/s; 2 of up to 131072 to 8192 74 us, 3.9 TB/s.
 template <int FMT, int kMost>  // kMost: pieces of 16 K codes of a block that a thread has at most
 __global__ __launch_bounds__(kMBlock) void k_kv_move(KvEvict p) {
   const KvView& c = p.c;

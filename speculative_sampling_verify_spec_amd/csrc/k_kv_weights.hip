@@ -13,9 +13,10 @@
 // than LDS takes are gone through in turns, which add to each other's sums.
 //
 // Bound by reading K, every page once a turn: 256 paths of trees over 97-2500
-// tokens (8 heads of 128, int8) 88 us, 4.0 TB/s; 64 single tokens over 301-2111
+// tokens (8 heads of 128, int8) 89 us, 4.0 TB/s; 64 single tokens over 301-2111
 // 23 us, of which the chain length - page - codes at the beginning and the join
-// are 10.  Turns of 32 instead of 64 KiB of rows take the same there.
+// are 10.  Turns of 32 instead of 64 KiB of rows take the same there.  With 32-bit
+// queries the paths take 119 us, the single tokens 27.
 #include <algorithm>
 
 #include "sv_budget.h"

@@ -22,10 +22,11 @@
 // are in 32 bits), so most tiles rescale nothing.  The weights are rounded to
 // bf16 for the product with the values, as the output is.
 //
-// Measured (32 heads on 8 of 128): a prompt of 16384 tokens 2015 us, 1.09 PFLOP/s,
-// 89 % of what a large matrix product reaches here, bound by the matrix cores at
-// the clock that they leave; 48 prompts of 25 to 1405 tokens 410 us, whose blocks
-// of 8 tiles spend a third of their time on queries, first tile and results.
+// Measured (32 heads on 8 of 128): a prompt of 16384 tokens 2045-2085 us, 1.05-1.08
+// PFLOP/s, nine tenths of what a large matrix product reaches on the same card,
+// bound by the matrix cores at the clock that they leave; 48 prompts of 25 to 1405
+// tokens 410-418 us, the matrix cores busy for 41 % of the cycles: a block of 8 tiles
+// on average has its queries, first tile and results to wait for.
 //
 // 32-bit inputs: every operand is split into three bf16 pieces whose sum has
 // 24 bits; products take the six largest of nine pieces' products.

@@ -11,10 +11,14 @@
 // no atomics join anything.  The rows pass through LDS, 64 at a time and for
 // all waves, from memory without registers between.
 //
-// Bound by the exponentials: a score costs one quarter-rate instruction and two
-// of full rate, 24 cycles of a SIMD for 64, against 16 of its products.  2 prompts
-// of 8000 and 8191 tokens (32 heads on 8 of 128) 640 us, 0.85 PFLOP/s; 48 of 25 to
-// 1405 tokens 211 us.  Tiles of 128 rows: 6 and 26 % more; four waves a SIMD: 45 %.
+// A score costs one quarter-rate instruction and two of full rate, 24 cycles of a
+// SIMD for 64, against 16 of its products: about 400 of the 645-667 us that 2 prompts
+// of 8000 and 8191 tokens (32 heads on 8 of 128) take, 0.81-0.84 PFLOP/s.  Vector
+// instructions are issued in 67 % of the cycles and the matrix cores busy in 48 %:
+// neither is full, and the barrier of every tile and the reads of the rows from LDS
+// stand between.  48 prompts of 25 to 1405 tokens 217-225 us.  Tiles of 128 rows: 6
+// and 26 % more; four waves a SIMD: 45 %.  32-bit inputs: 16 prompts of 3 to 600
+// tokens (16 heads of 64) 29 us, 2 of 4000 and 4095 (32 heads on 8 of 128) 1080 us.
 #pragma once
 
 #include <type_traits>

@@ -151,6 +151,9 @@ __device__ inline PromptBlock prompt_block_of_few(const Packed& s, int place, in
 
 // The block in a place, for any number of sequences: in their order, a
 // sequence's blocks as above.  Every thread of a workgroup of THREADS calls it.
+// Every workgroup looks through all starts up to its own sequence, so that the
+// cost grows with the square of their number: prompts of 4 tokens (32 heads on 8
+// of 64), 65 of them 12 us, 1000 107, 4000 918, 16000 12 ms.
 template <int THREADS, bool FROM_START>
 __device__ inline PromptBlock prompt_block(const Packed& s, unsigned place, int per_token, int size) {
   if (s.B <= 64) return prompt_block_of_few<FROM_START>(s, static_cast<int>(place), per_token, size);
