@@ -582,7 +582,8 @@ int spec_prompt_weights(const void* q, int64_t q_stride, const void* k, int64_t 
  *               query that weighs nothing, whatever it holds
  *   weights, out_weights  [B][heads][capacity] float; the same array, or
  *               arrays that do not overlap; out_weights overlaps nothing
- *               else that the call reads (SPECV_E_OVERLAP)
+ *               else that the call reads, nor what lies between token rows
+ *               (SPECV_E_OVERLAP)
  *   max_pages * page_size at most 2^31 - 2^15 and at most capacity < 2^31;
  *   B * heads < 2^24
  * The other limits are those of spec_kv_attention.  Sums are in 32 bits, in

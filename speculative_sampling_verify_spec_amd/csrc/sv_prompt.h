@@ -95,10 +95,14 @@ __device__ inline int lanes_sum_upto(int v) {
 // rows see).  Where the chip has work for several turns (places from kInOrder
 // on), sequences come one after the other, so that blocks that read the same
 // keys do so together; else the highest blocks of all sequences come first,
-// so that no long one begins late.  In order and highest first: 48 prompts of 25
-// to 1405 tokens 411 and 448 us (9648 places), their weights 234 and 211 (2704
-// places), those of 2 prompts of 8000 and 8191 755 and 640 (1032), 6 prompts
-// with heads of 256 71 and 66 us (618).
+// so that no long one begins late.  In order and highest first (us, places):
+// attention of 48 prompts of 25 to 1405 tokens 411 and 448 (9648), of 16 of up to
+// 4000 890 and 920 (9424), of 64 of up to 300 54 and 64 (2976), of 16 of up to 1500 143
+// and 146 (3280), of 6 with heads of 256 71 and 66 (618); weights of 64 prompts of up to
+// 2000 with a head of their own 165 and 168 (5048), of 32 of up to 1500 60 and 57
+// (3488), of 48 of 25 to 1405 234 and 211 (2704), of 2 of 8000 and 8191 749 and 640
+// (1032).  So the attention would take the order from fewer places on than the
+// weights; one number serves both.
 constexpr unsigned kInOrder = 4096;
 
 template <bool FROM_START>
